@@ -11,6 +11,9 @@ every call raises -- there is no fallback.
 
 x is a contiguous bf16 CUDA tensor [rows, cols] or [E, rows, cols] (a leading
 expert dimension selects the batched entry points), cols % 16 == 0.
+
+The operators of a distillation step around it (layer norm, distillation loss, AdamW) are in
+``train.py`` and exported here; ``include/nvfp4_train.h`` defines them.
 """
 from __future__ import annotations
 
@@ -23,6 +26,8 @@ __all__ = ["quantize", "fakequant", "amax", "quantize_from_amax", "fakequant_fro
            "dequantize", "quantize_diag", "quantize_fused", "fakequant_fused",
            "quantize_fused_noalloc", "fused_blocks_per_lane", "set_fused_wait_limit",
            "diag_ws_words", "lib",
+           "layer_norm", "layer_norm_backward", "distill_loss", "adamw_plan", "adamw_step",
+           "AdamWPlan", "ADAMW_BLOCK",
            "NVFP4Error", "MODES", "RULES", "STATS", "FUSED_WS_WORDS", "LIB_PATH"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnvfp4_amax.so")
@@ -32,8 +37,8 @@ BLOCK = 16
 
 
 class NVFP4Error(RuntimeError):
-    def __init__(self, status: int, where: str):
-        msg = lib().nvfp4_status_str(status).decode()
+    def __init__(self, status: int, where: str, text: str = None):
+        msg = text or lib().nvfp4_status_str(status).decode()
         super().__init__("%s: %s (status %d)" % (where, msg, status))
         self.status = status
 
@@ -88,6 +93,7 @@ def lib() -> ctypes.CDLL:
                      "nvfp4_quantize_fused", "nvfp4_fakequant_fused",
                      "nvfp4_quantize_fused_noalloc"):
             getattr(L, name).restype = i32
+        train.bind(L)
         _lib = L
     return _lib
 
@@ -350,3 +356,8 @@ def set_fused_wait_limit(polls: int) -> None:
     """Test hook: polls before a fused workgroup stops waiting for the others and computes the
     tensor amax itself (0 = never wait, negative = the default)."""
     lib().nvfp4_fused_set_wait_limit(int(polls))
+
+
+from . import train  # noqa: E402  (it uses the helpers above)
+from .train import (ADAMW_BLOCK, AdamWPlan, adamw_plan, adamw_step, distill_loss,  # noqa: E402
+                    layer_norm, layer_norm_backward)

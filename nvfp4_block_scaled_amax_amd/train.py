@@ -1,0 +1,353 @@
+"""The operators of a quantization-aware distillation step around fake-quantization: layer norm
+forward and backward, the distillation loss with its gradient, AdamW over many tensors.
+
+A thin binding over ``libnvfp4_amax.so`` (``include/nvfp4_train.h`` defines the operations).
+As in the quantization calls, torch provides memory and the current stream and every step of the
+computation runs in the library's kernels.
+
+    y, h, mean, rstd = layer_norm(x, weight, bias, residual=r, amax=top)   # h = x + r
+    q, _ = fakequant_from_amax(y, top, ...)                                # no amax pass over y
+    loss, grad = distill_loss(student_logits, teacher_logits, row_weight)
+    dx, dweight, dbias = layer_norm_backward(dy, h, weight, mean, rstd, dres=dh)
+    plan = adamw_plan(params, state="e4m3")
+    adamw_step(plan, grads, step=1, lr=1e-4, seed=0)
+
+Tensors are bfloat16 or float32, on one GPU, with a contiguous last dimension.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import NVFP4Error, _on, _out, _ptr, _stream, lib
+
+TYPES = {torch.bfloat16: 0, torch.float32: 1}
+STATES = {"f32": 0, "e4m3": 1}
+ADAMW_BLOCK = 128               # NVFP4_ADAMW_BLOCK: elements per scale of an 8-bit state
+TRAIN_ABI_VERSION = 1           # NVFP4_TRAIN_ABI_VERSION
+
+
+class AdamWTensor(ctypes.Structure):
+    """nvfp4_adamw_tensor."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("param", "grad", "exp_avg", "exp_avg_sq", "master",
+                                               "avg_scale", "sq_scale")] + [("numel", ctypes.c_int64)]
+
+
+class AdamWArgs(ctypes.Structure):
+    """nvfp4_adamw_args."""
+    _fields_ = [(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps", "weight_decay")] + [
+        ("step", ctypes.c_int64), ("seed", ctypes.c_uint32)]
+
+
+def bind(L: ctypes.CDLL) -> None:
+    """Argument types of the entry points of nvfp4_train.h."""
+    P, i64, i32, f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
+    L.nvfp4_train_abi_version.restype = i32
+    if L.nvfp4_train_abi_version() != TRAIN_ABI_VERSION:
+        raise RuntimeError("libnvfp4_amax.so has training ABI version %d, this binding needs %d: "
+                           "rebuild it" % (L.nvfp4_train_abi_version(), TRAIN_ABI_VERSION))
+    L.nvfp4_train_status_str.argtypes, L.nvfp4_train_status_str.restype = [i32], ctypes.c_char_p
+    L.nvfp4_layernorm_forward.argtypes = [P, i64, P, i64, P, P, i64, i64, i32, i32, i32, f32, P, P,
+                                          P, P, P, P]
+    L.nvfp4_layernorm_backward_workspace.argtypes = [i64, i64]
+    L.nvfp4_layernorm_backward_workspace.restype = i64
+    L.nvfp4_layernorm_backward.argtypes = [P, P, P, P, P, P, i64, i64, i32, i32, P, P, P, P, P]
+    L.nvfp4_distill_loss_workspace.argtypes = [i64, i64]
+    L.nvfp4_distill_loss_workspace.restype = i64
+    L.nvfp4_distill_loss.argtypes = [P, i64, P, i64, P, i64, i64, i32, i32, f32, P, P, i64, P, P]
+    L.nvfp4_adamw_step.argtypes = [P, i64, i32, i32, i32, P, P, P, P]
+    for name in ("nvfp4_layernorm_forward", "nvfp4_layernorm_backward", "nvfp4_distill_loss",
+                 "nvfp4_adamw_step"):
+        getattr(L, name).restype = i32
+
+
+def _check(status: int, where: str):
+    if status != 0:
+        raise NVFP4Error(status, where, lib().nvfp4_train_status_str(status).decode())
+
+
+def _type(t: torch.Tensor, what: str) -> int:
+    if t.dtype not in TYPES:
+        raise TypeError("%s must be bfloat16 or float32, got %s" % (what, t.dtype))
+    return TYPES[t.dtype]
+
+
+def _rows(t: torch.Tensor, what: str):
+    """(rows, cols, row stride) of a tensor seen as rows of its last dimension."""
+    if not t.is_cuda:
+        raise ValueError("%s must be a GPU tensor" % what)
+    if t.dim() == 0 or t.shape[-1] < 1:
+        raise ValueError("%s must have a last dimension of at least 1" % what)
+    cols = t.shape[-1]
+    if t.is_contiguous():
+        return t.numel() // cols, cols, cols
+    if t.dim() == 2 and (t.stride(1) == 1 or cols == 1) and t.stride(0) >= cols:
+        return t.shape[0], cols, t.stride(0)
+    raise ValueError("%s must be contiguous, or 2-D with a contiguous last dimension and rows "
+                     "that do not overlap" % what)
+
+
+def _like(t: torch.Tensor, shape, dtypes, x: torch.Tensor, what: str):
+    """Checks an input that goes with x: its shape, its type, its device."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, got %s" % (what, tuple(shape), tuple(t.shape)))
+    if t.dtype not in dtypes:
+        raise TypeError("%s must be %s, got %s" % (what, " or ".join(map(str, dtypes)), t.dtype))
+    if t.device != x.device:
+        raise ValueError("%s must be on %s" % (what, x.device))
+
+
+def _vector(t: torch.Tensor, shape, dtypes, x: torch.Tensor, what: str):
+    _like(t, shape, dtypes, x, what)
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % what)
+
+
+def _work(workspace, nbytes: int, x: torch.Tensor):
+    """The caller's workspace, checked, or one of `nbytes` bytes."""
+    if nbytes < 0:
+        raise ValueError("bad shape")
+    if workspace is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+    if (workspace.device != x.device or not workspace.is_contiguous()
+            or workspace.numel() * workspace.element_size() < nbytes):
+        raise ValueError("workspace must be a contiguous tensor of at least %d bytes on %s"
+                         % (nbytes, x.device))
+    return workspace
+
+
+_F32 = (torch.float32,)
+_BOTH = (torch.bfloat16, torch.float32)
+
+
+def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor = None, *,
+               residual: torch.Tensor = None, eps: float = 1e-5, center: bool = True,
+               amax: torch.Tensor = None, y=None, h=None, mean=None, rstd=None):
+    """Layer norm of the last dimension -> (y, h, mean, rstd).
+
+    h = x + residual rounded to x's type (x itself without residual); y = (h - mean) * rstd *
+    weight + bias.  center=False is the root-mean-square norm (mean is None).  mean and rstd
+    are float32, one per row, for the backward pass.  amax: float32 [1], receives max |y| for
+    fakequant_from_amax / quantize_from_amax.  x and residual may be 2-D with a row stride.
+    y may be x (without residual) and h may be x or residual, where they are contiguous."""
+    rows, cols, xs = _rows(x, "x")
+    kind = _type(x, "x")
+    _vector(weight, (cols,), _BOTH, x, "weight")
+    if bias is not None:
+        _vector(bias, (cols,), (weight.dtype,), x, "bias")
+    rs = cols
+    if residual is not None:
+        _like(residual, x.shape, (x.dtype,), x, "residual")
+        rs = _rows(residual, "residual")[2]
+        h = _out(h, x.shape, x.dtype, x)
+    elif h is not None:
+        raise ValueError("h is an output of the residual form only")
+    lead = tuple(x.shape[:-1])
+    y = _out(y, x.shape, x.dtype, x)
+    rstd = _out(rstd, lead, torch.float32, x)
+    mean = _out(mean, lead, torch.float32, x) if center else None
+    if amax is not None:
+        _vector(amax, (1,), _F32, x, "amax")
+    with _on(x):
+        st = lib().nvfp4_layernorm_forward(
+            _ptr(x), xs, _ptr(residual), rs, _ptr(weight), _ptr(bias), rows, cols, kind,
+            TYPES[weight.dtype], int(center), eps, _ptr(y), _ptr(h), _ptr(mean), _ptr(rstd),
+            _ptr(amax), _stream(x))
+    _check(st, "nvfp4_layernorm_forward")
+    return y, x if residual is None else h, mean, rstd
+
+
+def layer_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor,
+                        mean: torch.Tensor, rstd: torch.Tensor, *, dres: torch.Tensor = None,
+                        bias: bool = True, dx=None, dweight=None, dbias=None, workspace=None):
+    """Gradient of layer_norm -> (dx, dweight, dbias).
+
+    h, mean and rstd as layer_norm returned them (mean None for center=False).  dres: gradient
+    that reaches h past the norm, added to dx.  dx is the gradient of x and of residual alike, and may
+    be written over dy or dres.  bias=False leaves dbias out (None)."""
+    rows, cols, _ = _rows(dy, "dy")
+    kind = _type(dy, "dy")
+    for t, what in ((dy, "dy"), (h, "h"), (dres, "dres")):
+        if t is not None:
+            _vector(t, dy.shape, (dy.dtype,), dy, what)
+    _vector(weight, (cols,), _BOTH, dy, "weight")
+    lead = tuple(dy.shape[:-1])
+    _vector(rstd, lead, _F32, dy, "rstd")
+    if mean is not None:
+        _vector(mean, lead, _F32, dy, "mean")
+    dx = _out(dx, dy.shape, dy.dtype, dy)
+    dweight = _out(dweight, (cols,), weight.dtype, dy)
+    dbias = _out(dbias, (cols,), weight.dtype, dy) if bias else None
+    L = lib()
+    ws = _work(workspace, L.nvfp4_layernorm_backward_workspace(rows, cols), dy)
+    with _on(dy):
+        st = L.nvfp4_layernorm_backward(
+            _ptr(dy), _ptr(h), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dres), rows, cols, kind,
+            TYPES[weight.dtype], _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(ws), _stream(dy))
+    _check(st, "nvfp4_layernorm_backward")
+    return dx, dweight, dbias
+
+
+def distill_loss(student: torch.Tensor, teacher: torch.Tensor, weight: torch.Tensor = None, *,
+                 temperature: float = 1.0, want_grad: bool = True, loss=None, grad=None,
+                 workspace=None):
+    """weight * KL(softmax(teacher / T) || softmax(student / T)) per row, and its gradient with
+    respect to the student's logits -> (loss float32 [...], grad in student's type or None).
+
+    Logits are [..., vocab]; 2-D ones may have a row stride.  weight: float32 [...]; rows of
+    weight 0 are not read.  grad may be the student itself (written in place)."""
+    rows, vocab, ss = _rows(student, "student")
+    kinds = _type(student, "student"), _type(teacher, "teacher")
+    _like(teacher, student.shape, _BOTH, student, "teacher")
+    ts = _rows(teacher, "teacher")[2]
+    lead = tuple(student.shape[:-1])
+    if weight is not None:
+        _vector(weight, lead, _F32, student, "weight")
+    loss = _out(loss, lead, torch.float32, student)
+    gs = vocab
+    if grad is not None:
+        if not want_grad:
+            raise ValueError("grad is an output of the form with a gradient only")
+        _like(grad, student.shape, (student.dtype,), student, "grad")
+        gs = _rows(grad, "grad")[2]
+    elif want_grad:
+        grad = torch.empty(student.shape, dtype=student.dtype, device=student.device)
+    L = lib()
+    ws = _work(workspace, L.nvfp4_distill_loss_workspace(rows, vocab), student)
+    with _on(student):
+        st = L.nvfp4_distill_loss(
+            _ptr(student), ss, _ptr(teacher), ts, _ptr(weight), rows, vocab, kinds[0], kinds[1],
+            temperature, _ptr(loss), _ptr(grad), gs, _ptr(ws), _stream(student))
+    _check(st, "nvfp4_distill_loss")
+    return loss, grad
+
+
+class AdamWPlan:
+    """Parameters and their optimizer state, checked once: what adamw_step updates in place.
+
+    params, master, exp_avg, exp_avg_sq, avg_scale, sq_scale are lists of tensors (None for a
+    kind that is not there); a checkpoint saves and restores their contents.  With 8-bit states
+    exp_avg holds E4M3 codes of m / avg_scale and exp_avg_sq those of sqrt(v) / sq_scale, one
+    scale per 128 elements.  The tensors' memory is read at each step, so `p.data = ...` is
+    noticed; their number, sizes and types are the plan's."""
+
+    KINDS = ("params", "exp_avg", "exp_avg_sq", "master", "avg_scale", "sq_scale")
+
+    def __init__(self, params, exp_avg, exp_avg_sq, master, avg_scale, sq_scale):
+        self.params, self.exp_avg, self.exp_avg_sq = params, exp_avg, exp_avg_sq
+        self.master, self.avg_scale, self.sq_scale = master, avg_scale, sq_scale
+        self.device = params[0].device
+        self.numels = [p.numel() for p in params]
+        self.ptype = _type(params[0], "parameters")
+        self.dtype = params[0].dtype
+        state = exp_avg[0].dtype
+        if state not in (torch.float32, torch.float8_e4m3fn):
+            raise TypeError("states must be float32 or float8_e4m3fn, got %s" % state)
+        self.state = STATES["f32" if state == torch.float32 else "e4m3"]
+        if (self.state == 1) != (avg_scale is not None) or (self.state == 1) != (sq_scale is not None):
+            raise ValueError("avg_scale and sq_scale go with float8_e4m3fn states, and only with them")
+        if master is not None and self.dtype != torch.bfloat16:
+            raise ValueError("a master copy goes with bfloat16 parameters only")
+        blocks = [-(-n // ADAMW_BLOCK) for n in self.numels]
+        for kind, sizes, dtype in (("params", self.numels, self.dtype), ("exp_avg", self.numels, state),
+                                   ("exp_avg_sq", self.numels, state),
+                                   ("master", self.numels, torch.float32),
+                                   ("avg_scale", blocks, torch.float32),
+                                   ("sq_scale", blocks, torch.float32)):
+            tensors = getattr(self, kind)
+            if tensors is None:
+                continue
+            if len(tensors) != len(params):
+                raise ValueError("%s: %d tensors for %d parameters" % (kind, len(tensors), len(params)))
+            for t, n in zip(tensors, sizes):
+                self._look(kind, t, n, dtype)
+        self._table = (AdamWTensor * len(params))()
+        for row, n in zip(self._table, self.numels):
+            row.numel = n
+
+    def _look(self, kind, t, numel, dtype):
+        if t.dtype != dtype:
+            raise TypeError("%s must be %s, got %s" % (kind, dtype, t.dtype))
+        if not t.is_cuda or t.device != self.device:
+            raise ValueError("%s must be GPU tensors, all on one device" % kind)
+        if t.numel() != numel or not t.is_contiguous():
+            raise ValueError("%s must be contiguous, with %d elements, got %s"
+                             % (kind, numel, tuple(t.shape)))
+
+    def table(self, grads):
+        """The entries of nvfp4_adamw_tensor for these gradients."""
+        rows = self._table
+        for name, tensors in (("param", self.params), ("grad", grads), ("exp_avg", self.exp_avg),
+                              ("exp_avg_sq", self.exp_avg_sq), ("master", self.master),
+                              ("avg_scale", self.avg_scale), ("sq_scale", self.sq_scale)):
+            if tensors is not None:
+                for row, t in zip(rows, tensors):
+                    setattr(row, name, t.data_ptr())
+        return rows
+
+
+def adamw_plan(params, exp_avg=None, exp_avg_sq=None, *, master=None, avg_scale=None,
+               sq_scale=None, state: str = "f32") -> AdamWPlan:
+    """An AdamWPlan over `params` (float32, or bfloat16).
+
+    Without exp_avg and exp_avg_sq the state is made here, zero: float32, or with
+    state="e4m3" 8 bits plus scales.  master: a list of float32 tensors that bfloat16
+    parameters are copies of, True to make them from the parameters, or None: bfloat16 parameters are
+    then updated by stochastic rounding."""
+    params = list(params)
+    if not params:
+        raise ValueError("no parameters")
+    if not all(p.is_cuda for p in params):
+        raise ValueError("params must be GPU tensors")
+    if (exp_avg is None) != (exp_avg_sq is None):
+        raise ValueError("exp_avg and exp_avg_sq come together")
+    if exp_avg is None:
+        if state not in STATES:
+            raise ValueError("state must be one of %s" % ", ".join(STATES))
+        if avg_scale is not None or sq_scale is not None:
+            raise ValueError("avg_scale and sq_scale come with exp_avg and exp_avg_sq")
+        dtype = torch.float32 if state == "f32" else torch.float8_e4m3fn
+        zeros = lambda: [torch.zeros(p.shape, dtype=dtype, device=p.device) for p in params]
+        exp_avg, exp_avg_sq = zeros(), zeros()
+        if state == "e4m3":
+            scales = lambda: [torch.zeros(-(-p.numel() // ADAMW_BLOCK), dtype=torch.float32,
+                                          device=p.device) for p in params]
+            avg_scale, sq_scale = scales(), scales()
+    if master is True:
+        master = [p.detach().to(torch.float32, copy=True) for p in params]
+    listed = lambda v: None if v is None else list(v)
+    return AdamWPlan(params, list(exp_avg), list(exp_avg_sq), listed(master), listed(avg_scale),
+                     listed(sq_scale))
+
+
+def adamw_step(plan: AdamWPlan, grads, *, step: int, lr: float, betas=(0.9, 0.999),
+               eps: float = 1e-8, weight_decay: float = 0.01, grad_scale: torch.Tensor = None,
+               amax: torch.Tensor = None, seed: int = 0) -> None:
+    """One AdamW step on the plan's tensors, in place.
+
+    grads: one tensor per parameter, all bfloat16 or all float32.  step: 1 for the first.
+    grad_scale: float32 [1] on the GPU that multiplies the gradients (a clipping coefficient).
+    amax: float32 [tensors], receives max |param| as written, for the *_from_amax calls.
+    seed: of the stochastic rounding of 8-bit states and of bfloat16 parameters without a master
+    copy."""
+    grads = list(grads)
+    if len(grads) != len(plan.params):
+        raise ValueError("%d gradients for %d parameters" % (len(grads), len(plan.params)))
+    gtype = grads[0].dtype
+    kind = _type(grads[0], "gradients")
+    for g, n in zip(grads, plan.numels):
+        plan._look("grads", g, n, gtype)
+    like = plan.params[0]
+    if grad_scale is not None:
+        _vector(grad_scale, (1,), _F32, like, "grad_scale")
+    if amax is not None:
+        _vector(amax, (len(grads),), _F32, like, "amax")
+    if not 0 <= seed < 1 << 32:
+        raise ValueError("seed must be in 0 .. 2^32 - 1")
+    args = AdamWArgs(lr, betas[0], betas[1], eps, weight_decay, step, seed)
+    with _on(like):
+        st = lib().nvfp4_adamw_step(plan.table(grads), len(grads), plan.ptype, kind, plan.state,
+                                    ctypes.byref(args), _ptr(grad_scale), _ptr(amax),
+                                    _stream(like))
+    _check(st, "nvfp4_adamw_step")

@@ -1,0 +1,289 @@
+"""The distillation loss and its gradient on the GPU against the definition in 64 bits.
+
+Tolerances.  u = 2^-24.  Probabilities: the exponent y = (x - max) c - log2 Z (binary logarithms)
+is off by u of its three parts, Z by the s = 16 * ceil(V / 8192) + 64 additions behind it, and
+each power of two by one step (2u); together a relative error of e = u (4 + s + 3 (|x - max| c +
+log2 Z)).  The gradient is (w / T) (q - p) with these errors and its own rounding.  The loss is a
+sum of q - p + p d (d = log p - log q), in which a common error of log Z or of the exponents
+cancels against p d: what stays are the steps of the powers of two, 2u (q + p) each, e of |q - p|
+and of p |d|, and the additions, s u of the same.
+"""
+from __future__ import annotations
+
+import math
+import sys
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+HALF = {T: torch.finfo(T).eps / 2 for T in (torch.bfloat16, torch.float32)}     # 2^-8, 2^-24
+BF, F = torch.bfloat16, torch.float32
+INF = math.inf
+
+
+def say(*a):
+    print(*a, flush=True)
+    sys.stdout.flush()
+
+
+@pytest.fixture(scope="module")
+def nv():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import nvfp4_block_scaled_amax_amd as m
+    m.lib()
+    return m
+
+
+def logits(rows, vocab, S, T, seed=0, near=0.3, size=2.5):
+    gen = torch.Generator("cuda").manual_seed(seed + 31 * rows + vocab)
+    t = torch.randn(rows, vocab, generator=gen, device="cuda") * size
+    s = t + near * torch.randn(rows, vocab, generator=gen, device="cuda")
+    return s.to(S), t.to(T)
+
+
+def reference(s, t, w, T):
+    """loss, gradient, and the tolerances of both."""
+    s, t = s.double() / T, t.double() / T
+    w = torch.ones(s.shape[0], dtype=torch.float64, device="cuda") if w is None else w.double()
+    ls, lt = s.logsumexp(1, keepdim=True), t.logsumexp(1, keepdim=True)
+    lq, lp = s - ls, t - lt
+    q, p = lq.exp(), lp.exp()
+    d = torch.where(p > 0, lp - lq, 0.0)
+    loss = (p * d).sum(1)
+    steps = 16 * -(-s.shape[1] // 8192) + 64
+    def rel(x, l):
+        top = x.amax(1, keepdim=True)
+        far = torch.where(x > -INF, top - x, 0.0) / math.log(2)
+        return U * (4 + steps + 3 * (far + (l - top).abs() / math.log(2)))
+    # probabilities below 2^-126 come out as 0
+    tol_grad = q * rel(s, ls) + p * rel(t, lt) + 2.0 ** -125
+    flat, bent = (q - p).abs(), p * d.abs()
+    tol_loss = (4 * U * (q + p) + flat * rel(s, ls) + bent * rel(t, lt)
+                + steps * U * (flat + bent)).sum(1) + 4 * U * loss.abs()
+    grad = (q - p) * (w / T)[:, None]
+    return w * loss, grad, tol_loss * w.abs(), tol_grad * (w.abs() / T)[:, None] + 4 * U * grad.abs()
+
+
+def check(nv, s, t, w=None, T=1.0, **kw):
+    want_loss, want_grad, tol_loss, tol_grad = reference(s, t, w, T)
+    S = s.dtype
+    loss, grad = nv.distill_loss(s, t, w, temperature=T, **kw)
+    off = (loss.double() - want_loss).abs()
+    assert (off <= tol_loss + 1e-38).all(), ("loss", float((off / (tol_loss + 1e-38)).max()))
+    off = (grad.double() - want_grad).abs()
+    tol = tol_grad * (1 + HALF[S]) + HALF[S] * want_grad.abs() + 2.0 ** -126
+    assert (off <= tol).all(), ("grad", float((off / tol).max()))
+    return loss, grad
+
+
+SIZES = [(1, 1), (3, 2), (2, 7), (5, 8), (4, 9), (1, 1000), (7, 8191), (2, 8192), (3, 16384),
+         (1, 16385), (2, 32769), (5, 50251), (1, 200001), (200, 1000), (191, 20000), (192, 20000),
+         (300, 4099), (1100, 513)]
+
+
+@pytest.mark.parametrize("S,T", [(BF, BF), (F, F), (BF, F), (F, BF)], ids=str)
+@pytest.mark.parametrize("rows,vocab", SIZES)
+def test_loss_and_gradient(nv, rows, vocab, S, T):
+    say("[distill]", rows, vocab, S, T)
+    s, t = logits(rows, vocab, S, T)
+    loss, grad = check(nv, s, t)
+    gen = torch.Generator("cuda").manual_seed(1)
+    w = torch.rand(rows, generator=gen, device="cuda") + 0.1
+    w[::3] = 0
+    for temp in (2.0, 0.5):
+        loss, grad = check(nv, s, t, w, temp)
+        assert (loss[::3] == 0).all() and (grad[::3] == 0).all()
+    again = nv.distill_loss(s, t, w, temperature=0.5)
+    assert torch.equal(again[0], loss) and torch.equal(again[1], grad)
+    only, none = nv.distill_loss(s, t, w, temperature=0.5, want_grad=False)
+    assert none is None and torch.equal(only, loss)
+
+
+@pytest.mark.parametrize("rows", [2, 250])
+def test_near_and_far_students(nv, rows):
+    """A student very close to its teacher keeps its relative precision; one far away, and
+    logits of a thousand, stay finite."""
+    for near, size in ((0.01, 2.5), (0.1, 2.5), (5.0, 5.0), (0.3, 1000.0)):
+        s, t = logits(rows, 20011, F, F, near=near, size=size)
+        check(nv, s, t)
+    s, t = logits(rows, 20011, F, F, near=0.01)
+    loss, _ = nv.distill_loss(s, t)
+    want = reference(s, t, None, 1.0)[0]              # about 5e-5, where 8u + ... is 6e-7
+    assert ((loss.double() - want).abs() <= 0.02 * want).all()
+    loss, grad = nv.distill_loss(t, t)
+    assert (loss.abs() <= 64 * U).all() and (grad == 0).all()
+
+
+@pytest.mark.parametrize("rows,vocab", [(3, 40000), (260, 3001)])
+def test_masked_vocabulary_and_rows(nv, rows, vocab):
+    """-inf in both (padding), the type's lowest value as a mask, rows of weight 0 full of NaN."""
+    for S in (BF, F):
+        s, t = logits(rows, vocab, S, S)
+        cols = torch.randperm(vocab, generator=torch.Generator().manual_seed(2))[:vocab // 5].cuda()
+        s[:, cols] = -INF
+        t[:, cols] = -INF
+        s[:, -11:] = -INF
+        t[:, -11:] = -INF
+        w = torch.ones(rows, device="cuda")
+        w[1] = 0
+        loss, grad = check(nv, s, t, w)
+        assert (grad[:, cols] == 0).all()
+        s2, t2 = s.clone(), t.clone()
+        s2[1] = float("nan")
+        t2[1] = INF
+        loss2, grad2 = nv.distill_loss(s2, t2, w)
+        assert torch.equal(loss2, loss) and torch.equal(grad2, grad)
+        low = torch.finfo(S).min
+        loss3, grad3 = nv.distill_loss(s.masked_fill(s == -INF, low), t.masked_fill(t == -INF, low), w)
+        assert torch.equal(loss3, loss) and torch.equal(grad3, grad)
+        # a row in which every entry is the lowest value is uniform, in both: no loss
+        s4 = torch.full((rows, vocab), low, device="cuda", dtype=S)
+        loss4, grad4 = nv.distill_loss(s4, s4)
+        assert (loss4.abs() <= 64 * U).all() and (grad4 == 0).all()
+        # only the student excludes an entry that the teacher expects
+        s5 = s.clone()
+        at = int(t[0].float().argmax())
+        s5[0, at] = -INF
+        loss5, grad5 = nv.distill_loss(s5, t, w)
+        assert loss5[0] == INF and torch.isfinite(grad5[0]).all()
+        assert torch.equal(loss5[2:], loss[2:]) and torch.equal(grad5[2:], grad[2:])
+        # only the teacher excludes entries: they pull the student down
+        t6 = t.clone()
+        t6[0, :100] = -INF
+        check(nv, s, t6, w)
+
+
+@pytest.mark.parametrize("rows,vocab", [(2, 40000), (260, 3001)])
+@pytest.mark.parametrize("which", ["student", "teacher"])
+def test_rows_without_a_distribution(nv, rows, vocab, which):
+    s, t = logits(rows, vocab, BF, BF)
+    loss, grad = nv.distill_loss(s, t)
+    for bad in ("nan", "inf", "empty"):
+        s2, t2 = s.clone(), t.clone()
+        x = s2 if which == "student" else t2
+        if bad == "empty":
+            x[0] = -INF
+        else:
+            x[0, vocab - 1] = float(bad)
+        loss2, grad2 = nv.distill_loss(s2, t2)
+        assert torch.isnan(loss2[0]) and torch.isnan(grad2[0]).all(), bad
+        assert torch.equal(loss2[1:], loss[1:]) and torch.equal(grad2[1:], grad[1:])
+
+
+@pytest.mark.parametrize("rows,vocab", [(3, 30011), (220, 1003)])
+def test_strides_offsets_and_in_place(nv, rows, vocab):
+    for S in (BF, F):
+        s, t = logits(rows, vocab, S, S)
+        loss, grad = nv.distill_loss(s, t)
+        sb = torch.zeros(rows * (vocab + 5) + 8, device="cuda", dtype=S)
+        sv = sb[3:3 + rows * (vocab + 5)].view(rows, vocab + 5)[:, :vocab]
+        sv.copy_(s)
+        tb = torch.zeros(rows * (vocab + 9) + 8, device="cuda", dtype=S)
+        tv = tb[1:1 + rows * (vocab + 9)].view(rows, vocab + 9)[:, :vocab]
+        tv.copy_(t)
+        gb = torch.full((rows * (vocab + 3) + 8,), 5.0, device="cuda", dtype=S)
+        whole = gb[5:5 + rows * (vocab + 3)].view(rows, vocab + 3)
+        loss2, grad2 = nv.distill_loss(sv, tv, grad=whole[:, :vocab])
+        assert torch.equal(loss2, loss) and torch.equal(grad2, grad)
+        assert (whole[:, vocab:] == 5).all() and (gb[:5] == 5).all() and (gb[5 + whole.numel():] == 5).all()
+        loss3, grad3 = nv.distill_loss(sv, tv, grad=sv)
+        assert torch.equal(loss3, loss) and torch.equal(sv, grad) and grad3.data_ptr() == sv.data_ptr()
+        a = s.clone()
+        nv.distill_loss(a, t, grad=a)
+        assert torch.equal(a, grad)
+    s3 = s[:rows // 2 * 2].view(2, -1, vocab)
+    loss4, grad4 = nv.distill_loss(s3, t[:rows // 2 * 2].view(2, -1, vocab))
+    assert loss4.shape == s3.shape[:2] and grad4.shape == s3.shape
+
+
+@pytest.mark.parametrize("vocab", [5, 1000, 30000])
+def test_gradient_against_differences(nv, vocab):
+    """Differences of the 64-bit loss along random directions.  Step 1e-4: the differences' own
+    error is 1e-8 of third derivatives that are below 1."""
+    s, t = logits(4, vocab, F, F)
+    w = torch.tensor([0.7, 1.0, 0.0, 2.5], device="cuda")
+    for T in (1.0, 3.0):
+        _, grad = nv.distill_loss(s, t, w, temperature=T)
+        gen = torch.Generator("cuda").manual_seed(9)
+        for _ in range(3):
+            v = torch.randn(4, vocab, generator=gen, device="cuda").double()
+            e = 1e-4
+            want = (reference(s.double() + e * v, t, w, T)[0] - reference(s.double() - e * v, t, w, T)[0]) / (2 * e)
+            got = (grad.double() * v).sum(1)
+            tol = (reference(s, t, w, T)[3] * v.abs()).sum(1) + 1e-6
+            assert ((got - want).abs() <= tol).all(), (got, want)
+
+
+def test_no_rows_and_streams(nv):
+    e = torch.empty(0, 100, device="cuda")
+    loss, grad = nv.distill_loss(e, e)
+    assert loss.shape == (0,) and grad.shape == (0, 100)
+    for rows, vocab in ((2, 100000), (400, 5000)):
+        s, t = logits(rows, vocab, BF, BF)
+        first = nv.distill_loss(s, t)
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        with torch.cuda.stream(side):
+            second = nv.distill_loss(s, t)
+        side.synchronize()
+        assert torch.equal(first[0], second[0]) and torch.equal(first[1], second[1])
+
+
+@pytest.mark.parametrize("rows,vocab", [(2, 60000), (300, 3000)])
+def test_graph_replays(nv, rows, vocab):
+    s, t = logits(rows, vocab, BF, BF)
+    loss, grad = torch.empty(rows, device="cuda"), torch.empty_like(s)
+    ws = torch.full((nv.lib().nvfp4_distill_loss_workspace(rows, vocab) + 16,), 255, dtype=torch.uint8,
+                    device="cuda")
+    work = lambda: nv.distill_loss(s, t, loss=loss, grad=grad, workspace=ws)
+    work()
+    torch.cuda.synchronize()
+    want = loss.clone(), grad.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        work()
+    for turn in range(4):
+        loss.fill_(3)
+        grad.fill_(3)
+        ws.fill_(turn)
+        nv.distill_loss(t, s)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(loss, want[0]) and torch.equal(grad, want[1]), turn
+
+
+def test_offsets_past_32_bits(nv):
+    """2^31 elements are passed by the last rows of a large batch with a wide row stride."""
+    vocab, stride, rows = 1000, 12_000_000, 200
+    buf = torch.empty(rows * stride, device="cuda", dtype=BF)
+    s, t = logits(rows, vocab, BF, BF)
+    view = buf.view(rows, stride)[:, :vocab]
+    view.copy_(s)
+    loss, grad = nv.distill_loss(view, t)
+    want = nv.distill_loss(s, t)
+    assert torch.equal(loss, want[0]) and torch.equal(grad, want[1])
+    y = nv.layer_norm(view, torch.ones(vocab, device="cuda", dtype=BF))[0]
+    assert torch.equal(y, nv.layer_norm(s, torch.ones(vocab, device="cuda", dtype=BF))[0])
+
+
+def test_refusals(nv):
+    s, t = logits(4, 100, BF, BF)
+    w = torch.ones(4, device="cuda")
+    for err, call in (
+            (TypeError, lambda: nv.distill_loss(s.half(), t)),
+            (TypeError, lambda: nv.distill_loss(s, t.half())),
+            (ValueError, lambda: nv.distill_loss(s, t[:, :99])),
+            (ValueError, lambda: nv.distill_loss(s, t.cpu())),
+            (ValueError, lambda: nv.distill_loss(s, t, w[:3])),
+            (TypeError, lambda: nv.distill_loss(s, t, w.double())),
+            (ValueError, lambda: nv.distill_loss(s, t, want_grad=False, grad=s)),
+            (TypeError, lambda: nv.distill_loss(s, t, grad=s.float())),
+            (ValueError, lambda: nv.distill_loss(s.t(), t.t())),
+            (nv.NVFP4Error, lambda: nv.distill_loss(s, t, temperature=0.0)),
+            (nv.NVFP4Error, lambda: nv.distill_loss(s, t, grad=t))):
+        with pytest.raises(err):
+            call()
