@@ -1,22 +1,47 @@
 // The distillation loss KL(softmax(teacher / T) || softmax(student / T)) per row and its
 // gradient for gfx950 (include/nvfp4_train.h defines the operation).
 //
-// Each row is read twice: once for both maxima and both sums of exponentials together (running
-// maximum and sum, so one pass serves), and once, from the caches where the row fits, for the
-// loss and the gradient.  Exponentials are powers of two of (x - max) * log2(e) / T; the
-// subtraction comes first, so that logits of any size (the lowest finite value, too) keep their
-// differences.  The loss is summed in the second pass as q - p + p (log p - log q), whose sum
-// over a row is that of the plain definition but whose terms are all >= 0.
+// Each row is read twice: once for both sums of exponentials, and once, from the caches where
+// the row fits, for the loss and the gradient.  All exponentials are powers of two,
+//   2^(fma(x, c, -R)),  c = log2(e) / T,
+// with R the rounded product of c and some entry near the row's largest: whatever float R is, it
+// cancels exactly between an entry and its sum, so one fma per exponent loses nothing.
+//   first pass:   Zq = sum 2^(fma(s, c, -Rq)), Zp = sum 2^(fma(t, c, -Rp)); a lane moves its R
+//                 only when an entry passes it by 2^16, which is rare after the first steps
+//   in between:   Rq moves by log2(Zq / Zp) (the rounding of that sum is kept), so that both
+//                 probabilities come out over the same 1 / Zp and log2 p - log2 q is X - Y
+//   second pass:  Y, X the exponents of both; q - p = (2^Y - 2^X) / Zp;
+//                 loss = sum (q - p) + ln 2 sum p (X - Y)
+// The sum of q - p is zero in exact arithmetic.  With it, the terms are all >= 0, and an error
+// that q's normalization brings into both its parts cancels to second order: the loss of a
+// student near its teacher keeps its precision.
 //
-// With rows for every compute unit a workgroup takes a row.  With fewer, a row is split over
-// several workgroups in two launches: partial statistics, then gradient and partial losses,
-// which the last workgroup of a row adds in order.
+// Where c x overflows (rows of the lowest finite value; logits near the largest) the fast form
+// has no sum; such a row is done again with (x - max) c, which keeps their differences.
+//
+// With rows for every compute unit a workgroup takes a row and holds what it can of it between
+// the passes: 64 registers per thread, and up to 128 KB of a compute unit's shared memory.  The
+// more workgroups share a compute unit the better their passes overlap, so a row gets as few
+// threads as can hold it: 256 (4 workgroups a compute unit) to 16384 bf16 logits, 512 (2) to
+// 32768, or 49152 with shared memory; and 512 up to twice that, the rest being read again, before
+// 1024 (1), which hold 98304.  bf16, us per call: 8192 x 32000 270 with 512 threads, 437 with 1024;
+// 4096 x 60000 330 and 383, 98000 534 and 556, 128000 686 and 660.  Without holding anything,
+// 4096 x 128000 took 805 us with one workgroup a compute unit and 985 with two, whose rows
+// together pass the last-level cache: the second reading is what costs, not the exponentials.
+// Loads and stores bypass the caches (660 against 692 us; the rest of a long row, which is read
+// again, does not).  Rows of an odd length start at odd addresses and take longer (4096 x 127999:
+// 827 us); starting each at a 16-byte boundary (707 us) would let a row's last bits depend on
+// where it lies.
+//
+// With fewer rows than compute units, a row is split over several workgroups in two launches:
+// partial statistics, then gradient and partial losses, which the last workgroup of a row adds
+// in order.
 #include "train_common.h"
 
 namespace train {
 namespace {
 
-constexpr int kThreads = 1024, kWaves = kThreads / 64;
+constexpr int kThreads = 1024;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -3.402823466e38f;
 
@@ -26,177 +51,383 @@ struct Distill {
   const float* weight;
   float* loss;
   void* grad;
-  float* stats;           // split rows: [rows][splits][4]
+  float* stats;           // split rows: [rows][splits][2] of Split
   float* part;            // split rows: [rows][splits] losses
   uint32_t* arrived;      // split rows: [rows]
-  int64_t student_stride, teacher_stride, grad_stride, rows, vocab;
-  int64_t split_size;     // elements of a split, a multiple of 8
+  int64_t student_stride, teacher_stride, grad_stride, rows;
+  uint32_t vocab;
+  uint32_t split_size;    // elements of a split, a multiple of 8
   int splits;
-  float c, inv_t;         // log2(e) / T and 1 / T
+  float c, temperature;   // log2(e) / T, T
 };
 
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
-__device__ __forceinline__ float log2_(float x) { return __builtin_amdgcn_logf(x); }
 
-// max x, and the sum of 2^((x - max) c).  An empty one has max = the lowest finite value and
-// sum 0; an entry of -inf adds 0 to any.
-struct Stat {
-  float m, z;
-  __device__ __forceinline__ void join(float m2, float z2, float c) {
-    const float top = fmaxf(m, m2);
-    z = z * exp2_((m - top) * c) + z2 * exp2_((m2 - top) * c);
-    m = top;
+constexpr float kSlack = 16.0f;      // how far (in powers of two) entries may pass a lane's R
+
+// A unit is what a lane loads of both logits at once: eight elements, or four where both are
+// binary32, so that a wavefront's 16-byte loads are next to each other.
+template <typename S, typename T>
+constexpr int kUnit = sizeof(S) == 4 && sizeof(T) == 4 ? 4 : 8;
+template <typename T, int N>
+struct UnitOf {
+  typedef Vec8<T> type;
+  static __device__ __forceinline__ type load(const T* p) { return load_vec(p); }
+  static __device__ __forceinline__ type stream(const T* p) { return load_stream(p); }
+  static __device__ __forceinline__ void store(T* p, const float (&v)[N]) {
+    store_stream(p, make_vec(v, T()));
   }
-  template <typename T>
-  __device__ __forceinline__ void add(const Vec8<T>& v, float c) {
-    float top = fmaxf(m, v[0]);
-#pragma unroll
-    for (int i = 1; i < 8; ++i) top = fmaxf(top, v[i]);
-    z *= exp2_((m - top) * c);
-    m = top;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) z += exp2_((v[i] - top) * c);
+};
+template <>
+struct UnitOf<float, 4> {
+  typedef Vec4 type;
+  static __device__ __forceinline__ type load(const float* p) {
+    return {*reinterpret_cast<const u32x4_a2*>(p)};
   }
-  __device__ __forceinline__ void add(float v, float c) { join(v, 1.0f, c); }
+  static __device__ __forceinline__ type stream(const float* p) {
+    return {__builtin_nontemporal_load(reinterpret_cast<const u32x4_a2*>(p))};
+  }
+  static __device__ __forceinline__ void store(float* p, const float (&v)[4]) {
+    const u32x4 w = {__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                     __float_as_uint(v[3])};
+    __builtin_nontemporal_store(w, reinterpret_cast<u32x4_a2*>(p));
+  }
 };
 
-// Statistics of elements [lo, hi) of a row, over the workgroup; every thread gets them.
-template <typename S, typename T>
-__device__ __forceinline__ void row_stats(const S* s, const T* t, int64_t lo, int64_t hi, float c,
-                                          Stat& qs, Stat& ps, float (*slots)[4]) {
-  qs = ps = Stat{kLowest, 0.0f};
-  const int64_t whole = lo + (hi - lo) / 8 * 8;
-  for (int64_t at = lo + threadIdx.x * 8; at < whole; at += kThreads * 8) {
-    const Vec8<S> a = load_vec(s + at);
-    const Vec8<T> b = load_vec(t + at);
-    qs.add(a, c);
-    ps.add(b, c);
+// sum 2^(fma(x, c, -r)).  An empty one has r = the lowest finite value and sum 0; an entry of
+// -inf adds 0 to any.  `m` is an entry with r = c m (an r that overflows makes the sum useless:
+// see good()).
+struct Stat {
+  float r, z;
+  __device__ __forceinline__ void join(Stat o) {
+    const float top = fmaxf(r, o.r);
+    z = z * exp2_(r - top) + o.z * exp2_(o.r - top);
+    r = top;
   }
-  if (whole + threadIdx.x < hi) {     // the last up to 7
-    const float a = to_f32(s[whole + threadIdx.x]), b = to_f32(t[whole + threadIdx.x]);
-    if (a != -INFINITY) qs.add(a, c);
-    if (b != -INFINITY) ps.add(b, c);
+  template <int N, typename V>
+  __device__ __forceinline__ void add(const V& v, float c) {
+    float top = v[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) top = fmaxf(top, v[i]);
+    top *= c;
+    if (top > r + kSlack) {
+      z *= exp2_(r - top);
+      r = top;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) z += exp2_(fmaf(v[i], c, -r));
   }
-  // over the wavefront, then over the workgroup
-  const float mq = reduce64(qs.m, Max()), mp = reduce64(ps.m, Max());
-  const float zq = reduce64(qs.z * exp2_((qs.m - mq) * c), Sum());
-  const float zp = reduce64(ps.z * exp2_((ps.m - mp) * c), Sum());
+  __device__ __forceinline__ bool good() const { return z > 0.0f && z < INFINITY; }
+};
+
+// The same with exact differences: max x, and sum 2^((x - max) c).
+struct Exact {
+  float m, z;
+  __device__ __forceinline__ void join(Exact o, float c) {
+    const float top = fmaxf(m, o.m);
+    z = z * exp2_((m - top) * c) + o.z * exp2_((o.m - top) * c);
+    m = top;
+  }
+};
+
+// Both sums over a workgroup of WAVES wavefronts; every thread gets them.
+template <int WAVES>
+__device__ __forceinline__ void join_group(Stat& q, Stat& p, float (*slots)[4]) {
+  const float rq = reduce64(q.r, Max()), rp = reduce64(p.r, Max());
+  const float zq = reduce64(q.z * exp2_(q.r - rq), Sum());
+  const float zp = reduce64(p.z * exp2_(p.r - rp), Sum());
   const int wave = threadIdx.x >> 6;
   if ((threadIdx.x & 63) == 0) {
-    slots[wave][0] = mq;
+    slots[wave][0] = rq;
     slots[wave][1] = zq;
-    slots[wave][2] = mp;
+    slots[wave][2] = rp;
     slots[wave][3] = zp;
   }
   __syncthreads();
-  qs = Stat{slots[0][0], slots[0][1]};
-  ps = Stat{slots[0][2], slots[0][3]};
-  for (int i = 1; i < kWaves; ++i) {
-    qs.join(slots[i][0], slots[i][1], c);
-    ps.join(slots[i][2], slots[i][3], c);
-  }
+  const float* mine = slots[threadIdx.x % WAVES];
+  q.r = reduce_few<WAVES>(mine[0], Max());
+  p.r = reduce_few<WAVES>(mine[2], Max());
+  q.z = reduce_few<WAVES>(mine[1] * exp2_(mine[0] - q.r), Sum());
+  p.z = reduce_few<WAVES>(mine[3] * exp2_(mine[2] - p.r), Sum());
 }
 
-// The second pass over elements [lo, hi): writes the gradient, returns the workgroup's part of
-// the loss (without the row's weight) to every thread.
-template <typename S, typename T>
-__device__ __forceinline__ float row_grad(const S* s, const T* t, S* grad, int64_t lo, int64_t hi,
-                                          float c, Stat qs, Stat ps, float scale, float* slots) {
-  const float lq = log2_(qs.z), lp = log2_(ps.z);
-  float flat = 0.0f, bent = 0.0f;    // sums of q - p and of p (log2 p - log2 q)
-  auto one = [&](float a, float b) {
-    const float y = (a - qs.m) * c - lq, x = (b - ps.m) * c - lp;
-    const float q = exp2_(y), p = exp2_(x);
-    flat += q - p;
-    bent += p == 0.0f ? 0.0f : p * (x - y);
-    return (q - p) * scale;
-  };
-  const int64_t whole = lo + (hi - lo) / 8 * 8;
-  for (int64_t at = lo + threadIdx.x * 8; at < whole; at += kThreads * 8) {
-    const Vec8<S> a = load_vec(s + at);
-    const Vec8<T> b = load_vec(t + at);
-    float g[8];
+// A row's elements [lo, hi) as the threads of a workgroup hold them between the two passes.
+// The first REGS units of each thread stay in registers, the next LDS ones in shared memory, the
+// rest is read again; the up to 7 elements behind the last unit are single threads'.
+template <typename S, typename T, int THREADS, int REGS, int LDS>
+struct Row {
+  const S* s;
+  const T* t;
+  uint32_t lo, hi, whole;      // whole: end of the last unit
+  static constexpr int N = kUnit<S, T>;
+  typedef UnitOf<S, N> US;
+  typedef UnitOf<T, N> UT;
+  typedef typename US::type VS;
+  typedef typename UT::type VT;
+  VS a[REGS > 0 ? REGS : 1];
+  VT b[REGS > 0 ? REGS : 1];
+
+  static constexpr int64_t kBytes = (int64_t)LDS * THREADS * N * (sizeof(S) + sizeof(T));
+
+  __device__ __forceinline__ Row(const S* s_, const T* t_, uint32_t lo_, uint32_t hi_)
+      : s(s_), t(t_), lo(lo_), hi(hi_), whole(lo_ + (hi_ - lo_) / N * N) {}
+  __device__ __forceinline__ uint32_t place(int k) const {
+    return lo + (k * THREADS + threadIdx.x) * N;
+  }
+  // where a vector past the row's end is loaded from: its first one (unused, but no branch
+  // stands between the loads)
+  __device__ __forceinline__ uint32_t inside(int k) const {
+    const uint32_t at = place(k);
+    return at < whole ? at : lo;
+  }
+  static __device__ __forceinline__ VS* lds_a(void* lds, int k) {
+    return (VS*)lds + k * THREADS + threadIdx.x;
+  }
+  static __device__ __forceinline__ VT* lds_b(void* lds, int k) {
+    return (VT*)((VS*)lds + LDS * THREADS) + k * THREADS + threadIdx.x;
+  }
+
+  // First pass: f(vector of s, vector of t) for every vector, then g(s, t) for the singles.
+  template <typename F, typename G>
+  __device__ __forceinline__ void load(void* lds, F f, G g) {
+    if (lo < whole) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) g[i] = one(a[i], b[i]);
-    if (grad) store_vec(grad + at, make_vec(g, S()));
+      for (int k = 0; k < REGS; ++k) {
+        a[k] = US::stream(s + inside(k));
+        b[k] = UT::stream(t + inside(k));
+      }
+#pragma unroll
+      for (int k = 0; k < LDS; ++k) {
+        const VS x = US::stream(s + inside(REGS + k));
+        const VT y = UT::stream(t + inside(REGS + k));
+        *lds_a(lds, k) = x;
+        *lds_b(lds, k) = y;
+        if (place(REGS + k) < whole) f(x, y);
+      }
+#pragma unroll
+      for (int k = 0; k < REGS; ++k)
+        if (place(k) < whole) f(a[k], b[k]);
+    }
+    for (uint32_t at = place(REGS + LDS); at < whole; at += THREADS * N)
+      f(US::load(s + at), UT::load(t + at));
+    const uint32_t at = whole + threadIdx.x;
+    if (at < hi) g(to_f32(s[at]), to_f32(t[at]));
   }
-  const int64_t at = whole + threadIdx.x;
-  if (at < hi) {
-    const float g = one(to_f32(s[at]), to_f32(t[at]));
-    if (grad) grad[at] = from_f32<S>(g);
+  // Second pass: f(place, vectors), g(place, s, t).
+  template <typename F, typename G>
+  __device__ __forceinline__ void again(void* lds, F f, G g) {
+#pragma unroll
+    for (int k = 0; k < REGS; ++k)
+      if (place(k) < whole) {
+        opaque(a[k]);       // unpacked again: the floats do not stay in registers, too
+        opaque(b[k]);
+        f(place(k), a[k], b[k]);
+      }
+#pragma unroll
+    for (int k = 0; k < LDS; ++k)
+      if (place(REGS + k) < whole) f(place(REGS + k), *lds_a(lds, k), *lds_b(lds, k));
+    for (uint32_t at = place(REGS + LDS); at < whole; at += THREADS * N)
+      f(at, US::load(s + at), UT::load(t + at));
+    const uint32_t at = whole + threadIdx.x;
+    if (at < hi) g(at, to_f32(s[at]), to_f32(t[at]));
   }
-  return reduce_group<kWaves>(flat + kLn2 * bent, Sum(), slots);
+};
+
+// Sums of a row's elements.
+template <int THREADS, typename R>
+__device__ __forceinline__ void row_stats(R& row, void* lds, float c, Stat& q, Stat& p,
+                                          float (*slots)[4]) {
+  q = p = Stat{kLowest, 0.0f};
+  row.load(lds, [&](const auto& a, const auto& b) { q.template add<R::N>(a, c), p.template add<R::N>(b, c); },
+           [&](float a, float b) {
+             if (a != -INFINITY) q.join(Stat{a * c, 1.0f});
+             if (b != -INFINITY) p.join(Stat{b * c, 1.0f});
+           });
+  join_group<THREADS / 64>(q, p, slots);
 }
 
-template <typename S>
-__device__ __forceinline__ void zero_grad(S* grad, int64_t lo, int64_t hi) {
-  const int64_t whole = lo + (hi - lo) / 8 * 8;
+// The same with exact differences, for the rare row.
+template <int THREADS, typename S>
+__device__ __forceinline__ Exact row_exact(const S* s, uint32_t lo, uint32_t hi, float c, float* slots) {
+  Exact e{kLowest, 0.0f};
+#pragma unroll 1
+  for (uint32_t at = lo + threadIdx.x; at < hi; at += THREADS) {
+    const float a = to_f32(s[at]);
+    if (a != -INFINITY) e.join(Exact{a, 1.0f}, c);
+  }
+  const float m = reduce_group<THREADS / 64>(e.m, Max(), slots);
+  const float z = e.z * exp2_((e.m - m) * c);
+  __syncthreads();
+  e = Exact{m, reduce_group<THREADS / 64>(z, Sum(), slots)};
+  __syncthreads();
+  return e;
+}
+
+// The second pass: writes the gradient, returns the workgroup's part of the loss (with the row's
+// weight) to every thread.
+template <int THREADS, typename S, typename R>
+__device__ __forceinline__ float row_grad(R& row, void* lds, S* grad, float c, float temperature,
+                                          float weight, Stat q, Stat p, float* slots) {
+  constexpr int N = R::N;
+  // R of the student + log2(Zq / Zp) = r + off, r rounded
+  const float by = log2f(q.z / p.z), r = q.r + by;
+  const float part = r - q.r, off = (q.r - (r - part)) + (by - part);
+  const float scale = weight / (temperature * p.z);
+  const float back = 1.0f - off * kLn2;       // 2^-off
+  float flat = 0.0f, bent = 0.0f;    // sums of (q - p) weight / T and of p Zp (log2 p - log2 q)
+  row.again(
+      lds,
+      [&](uint32_t at, const auto& a, const auto& b) {
+        float x[N], y[N], g[N], least = INFINITY;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          y[i] = fmaf(a[i], c, -r);
+          x[i] = fmaf(b[i], c, -p.r);
+          least = fminf(least, fminf(x[i], y[i]));
+        }
+        if (least == -INFINITY) {     // log2 p - log2 q counts where p is not 0
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const float eq = exp2_(y[i]), ep = exp2_(x[i]);
+            bent += ep == 0.0f ? 0.0f : ep * (x[i] - y[i]);
+            g[i] = fmaf(eq, back, -ep) * scale;
+            flat += g[i];
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const float eq = exp2_(y[i]), ep = exp2_(x[i]);
+            bent = fmaf(ep, x[i] - y[i], bent);
+            g[i] = fmaf(eq, back, -ep) * scale;
+            flat += g[i];
+          }
+        }
+        if (grad) R::US::store(grad + at, g);
+      },
+      [&](uint32_t at, float a, float b) {
+        const float y = fmaf(a, c, -r), x = fmaf(b, c, -p.r);
+        const float eq = exp2_(y), ep = exp2_(x);
+        bent += ep == 0.0f ? 0.0f : ep * (x - y);
+        const float g = fmaf(eq, back, -ep) * scale;
+        flat += g;
+        if (grad) grad[at] = from_f32<S>(g);
+      });
+  // log2 p - log2 q = X - Y + off, and the p add up to 1
+  const float mine = flat * temperature + weight * kLn2 * (bent / p.z);
+  const float all = reduce_group<THREADS / 64>(mine, Sum(), slots);
+  return row.lo == 0 ? all + weight * kLn2 * off : all;
+}
+
+// The same from the sums with exact differences.
+template <int THREADS, typename S, typename T>
+__device__ __forceinline__ float row_grad_exact(const S* s, const T* t, S* grad, uint32_t lo,
+                                             uint32_t hi, float c, float temperature, float weight,
+                                             Exact q, Exact p, float* slots) {
+  const float lq = log2f(q.z), lp = log2f(p.z), scale = weight / temperature;
+  float sum = 0.0f;
+#pragma unroll 1
+  for (uint32_t at = lo + threadIdx.x; at < hi; at += THREADS) {
+    const float y = (to_f32(s[at]) - q.m) * c - lq, x = (to_f32(t[at]) - p.m) * c - lp;
+    const float eq = exp2_(y), ep = exp2_(x);
+    sum += (eq - ep) + (ep == 0.0f ? 0.0f : kLn2 * ep * (x - y));
+    if (grad) grad[at] = from_f32<S>((eq - ep) * scale);
+  }
+  return reduce_group<THREADS / 64>(weight * sum, Sum(), slots);
+}
+
+template <int THREADS, typename S>
+__device__ __forceinline__ void zero_grad(S* grad, uint32_t lo, uint32_t hi) {
+  const uint32_t whole = lo + (hi - lo) / 8 * 8;
   const Vec8<S> z = zero_vec<S>();
-  for (int64_t at = lo + threadIdx.x * 8; at < whole; at += kThreads * 8) store_vec(grad + at, z);
+  for (uint32_t at = lo + threadIdx.x * 8; at < whole; at += THREADS * 8) store_vec(grad + at, z);
   if (whole + threadIdx.x < hi) grad[whole + threadIdx.x] = from_f32<S>(0.0f);
 }
 
-template <typename S, typename T>
-__global__ __launch_bounds__(kThreads) void row_kernel(const Distill a) {
-  __shared__ float slots[kWaves][4], sums[kWaves];
-  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    const float w = a.weight ? a.weight[row] : 1.0f;
-    S* grad = a.grad ? (S*)a.grad + row * a.grad_stride : nullptr;
-    if (w == 0.0f) {
-      if (grad) zero_grad(grad, 0, a.vocab);
-      if (threadIdx.x == 0) a.loss[row] = 0.0f;
-      continue;
-    }
-    const S* s = (const S*)a.student + row * a.student_stride;
-    const T* t = (const T*)a.teacher + row * a.teacher_stride;
-    Stat qs, ps;
-    row_stats(s, t, 0, a.vocab, a.c, qs, ps, slots);
-    const float loss = row_grad(s, t, grad, 0, a.vocab, a.c, qs, ps, w * a.inv_t, sums);
-    if (threadIdx.x == 0) a.loss[row] = w * loss;
-    __syncthreads();
+template <typename S, typename T, int THREADS, int REGS, int LDS>
+__global__ __launch_bounds__(THREADS) void row_kernel(const Distill a) {
+  __shared__ float slots[THREADS / 64][4], sums[THREADS / 64];
+  extern __shared__ __align__(16) char held[];
+  const int64_t row = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  if (row >= a.rows) return;
+  const float w = a.weight ? a.weight[row] : 1.0f;
+  S* grad = a.grad ? (S*)a.grad + row * a.grad_stride : nullptr;
+  if (w == 0.0f) {
+    if (grad) zero_grad<THREADS>(grad, 0, a.vocab);
+    if (threadIdx.x == 0) a.loss[row] = 0.0f;
+    return;
   }
+  const S* s = (const S*)a.student + row * a.student_stride;
+  const T* t = (const T*)a.teacher + row * a.teacher_stride;
+  Row<S, T, THREADS, REGS, LDS> r(s, t, 0, a.vocab);
+  Stat q, p;
+  row_stats<THREADS>(r, held, a.c, q, p, slots);
+  float loss;
+  if (q.good() && p.good()) {
+    loss = row_grad<THREADS>(r, held, grad, a.c, a.temperature, w, q, p, sums);
+  } else {
+    const Exact eq = row_exact<THREADS>(s, 0, a.vocab, a.c, sums);
+    const Exact ep = row_exact<THREADS>(t, 0, a.vocab, a.c, sums);
+    loss = row_grad_exact<THREADS>(s, t, grad, 0, a.vocab, a.c, a.temperature, w, eq, ep, sums);
+  }
+  if (threadIdx.x == 0) a.loss[row] = loss;
 }
+
+// What a split of a row leaves for both of its logits: r and z of Stat, m and z of Exact (where
+// the fast sum is good, Exact has its value: c m = r but for r's rounding).
+struct Split {
+  float r, z, m, e;
+};
 
 template <typename S, typename T>
 __global__ __launch_bounds__(kThreads) void split_stats_kernel(const Distill a) {
-  __shared__ float slots[kWaves][4];
+  __shared__ float slots[kThreads / 64][4], sums[kThreads / 64];
   const int64_t row = blockIdx.y;
   if (blockIdx.x == 0 && threadIdx.x == 0) a.arrived[row] = 0u;
   if (a.weight && a.weight[row] == 0.0f) return;
-  const int64_t lo = min(blockIdx.x * a.split_size, a.vocab), hi = min(lo + a.split_size, a.vocab);
-  Stat qs, ps;
-  row_stats((const S*)a.student + row * a.student_stride,
-            (const T*)a.teacher + row * a.teacher_stride, lo, hi, a.c, qs, ps, slots);
+  const uint32_t lo = min(blockIdx.x * a.split_size, a.vocab), hi = min(lo + a.split_size, a.vocab);
+  const S* s = (const S*)a.student + row * a.student_stride;
+  const T* t = (const T*)a.teacher + row * a.teacher_stride;
+  Stat q, p;
+  Row<S, T, kThreads, 0, 0> r(s, t, lo, hi);
+  row_stats<kThreads>(r, nullptr, a.c, q, p, slots);
+  Exact eq{q.r / a.c, q.z}, ep{p.r / a.c, p.z};
+  if (!q.good()) eq = row_exact<kThreads>(s, lo, hi, a.c, sums);
+  if (!p.good()) ep = row_exact<kThreads>(t, lo, hi, a.c, sums);
   if (threadIdx.x == 0) {
-    float* out = a.stats + (row * a.splits + blockIdx.x) * 4;
-    out[0] = qs.m;
-    out[1] = qs.z;
-    out[2] = ps.m;
-    out[3] = ps.z;
+    Split* out = (Split*)a.stats + (row * a.splits + blockIdx.x) * 2;
+    out[0] = Split{q.r, q.z, eq.m, eq.z};
+    out[1] = Split{p.r, p.z, ep.m, ep.z};
   }
 }
 
 template <typename S, typename T>
 __global__ __launch_bounds__(kThreads) void split_grad_kernel(const Distill a) {
-  __shared__ float sums[kWaves];
+  __shared__ float sums[kThreads / 64];
   const int64_t row = blockIdx.y;
-  const int64_t lo = min(blockIdx.x * a.split_size, a.vocab), hi = min(lo + a.split_size, a.vocab);
+  const uint32_t lo = min(blockIdx.x * a.split_size, a.vocab), hi = min(lo + a.split_size, a.vocab);
   const float w = a.weight ? a.weight[row] : 1.0f;
   S* grad = a.grad ? (S*)a.grad + row * a.grad_stride : nullptr;
   if (w == 0.0f) {
-    if (grad) zero_grad(grad, lo, hi);
+    if (grad) zero_grad<kThreads>(grad, lo, hi);
     if (blockIdx.x == 0 && threadIdx.x == 0) a.loss[row] = 0.0f;
     return;
   }
-  const float* in = a.stats + row * a.splits * 4;
-  Stat qs{in[0], in[1]}, ps{in[2], in[3]};
+  const S* s = (const S*)a.student + row * a.student_stride;
+  const T* t = (const T*)a.teacher + row * a.teacher_stride;
+  const Split* in = (const Split*)a.stats + row * a.splits * 2;
+  Stat q{in[0].r, in[0].z}, p{in[1].r, in[1].z};
+  Exact eq{in[0].m, in[0].e}, ep{in[1].m, in[1].e};
   for (int i = 1; i < a.splits; ++i) {
-    qs.join(in[4 * i], in[4 * i + 1], a.c);
-    ps.join(in[4 * i + 2], in[4 * i + 3], a.c);
+    q.join(Stat{in[2 * i].r, in[2 * i].z});
+    p.join(Stat{in[2 * i + 1].r, in[2 * i + 1].z});
+    eq.join(Exact{in[2 * i].m, in[2 * i].e}, a.c);
+    ep.join(Exact{in[2 * i + 1].m, in[2 * i + 1].e}, a.c);
   }
-  const float loss = row_grad((const S*)a.student + row * a.student_stride,
-                              (const T*)a.teacher + row * a.teacher_stride, grad, lo, hi, a.c, qs,
-                              ps, w * a.inv_t, sums);
+  Row<S, T, kThreads, 0, 0> r(s, t, lo, hi);
+  const float loss =
+      q.good() && p.good()
+          ? row_grad<kThreads>(r, nullptr, grad, a.c, a.temperature, w, q, p, sums)
+          : row_grad_exact<kThreads>(s, t, grad, lo, hi, a.c, a.temperature, w, eq, ep, sums);
   if (threadIdx.x == 0) {
     float* part = a.part + row * a.splits;
     __hip_atomic_store(part + blockIdx.x, loss, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -206,10 +437,13 @@ __global__ __launch_bounds__(kThreads) void split_grad_kernel(const Distill a) {
       float sum = 0.0f;
       for (int i = 0; i < a.splits; ++i)
         sum += __hip_atomic_load(part + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      a.loss[row] = w * sum;
+      a.loss[row] = sum;
     }
   }
 }
+
+// Places within a row fit 32 bits, their bytes and those of a whole split past them too.
+constexpr int64_t kMaxVocab = int64_t(1) << 28;
 
 // Workgroups per row: one where there are rows for the 256 compute units, else enough for
 // them, each with two vectors per thread at the least.
@@ -219,14 +453,34 @@ int splits_of(int64_t rows, int64_t vocab) {
   return (int)(want < most ? want : most);
 }
 
+template <typename S, typename T, int THREADS, int REGS, int LDS>
+void launch_rows(const Distill& a, hipStream_t stream) {
+  const int bytes = (int)Row<S, T, THREADS, REGS, LDS>::kBytes;
+  auto kernel = row_kernel<S, T, THREADS, REGS, LDS>;
+  if (bytes > 65536 - 512)
+    (void)hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  constexpr int64_t kLine = 1 << 20;                // workgroups in x: threads stay below 2^32
+  const dim3 grid((unsigned)(a.rows < kLine ? a.rows : kLine), (unsigned)((a.rows + kLine - 1) / kLine));
+  kernel<<<grid, THREADS, bytes, stream>>>(a);
+}
+
 template <typename S, typename T>
 void launch(const Distill& a, hipStream_t stream) {
-  if (a.splits == 1) {
-    row_kernel<S, T><<<(unsigned)(a.rows < (1 << 20) ? a.rows : (1 << 20)), kThreads, 0, stream>>>(a);
-  } else {
+  // units that a thread holds: 64 registers, and of 1024 threads 128 KB of shared memory
+  constexpr int unit = kUnit<S, T>, bytes = unit * (sizeof(S) + sizeof(T));
+  constexpr int regs = 256 / bytes, lds = 128 / bytes;
+  if (a.splits > 1) {
     const dim3 grid((unsigned)a.splits, (unsigned)a.rows);
     split_stats_kernel<S, T><<<grid, kThreads, 0, stream>>>(a);
     split_grad_kernel<S, T><<<grid, kThreads, 0, stream>>>(a);
+  } else if (a.vocab <= 256 * unit * regs) {
+    launch_rows<S, T, 256, regs, 0>(a, stream);
+  } else if (a.vocab <= 512 * unit * regs) {
+    launch_rows<S, T, 512, regs, 0>(a, stream);
+  } else if (a.vocab <= 2 * 512 * unit * (regs + lds)) {
+    launch_rows<S, T, 512, regs, lds>(a, stream);
+  } else {
+    launch_rows<S, T, 1024, regs, lds>(a, stream);
   }
 }
 
@@ -237,7 +491,7 @@ using namespace train;
 
 NVFP4_EXPORT int64_t nvfp4_distill_loss_workspace(int64_t rows, int64_t vocab) {
   const int64_t splits = vocab < 1 ? 1 : splits_of(rows, vocab);
-  return splits == 1 ? 0 : rows * (splits * 5 + 1) * 4;
+  return splits == 1 ? 0 : rows * (splits * 9 + 1) * 4;
 }
 
 NVFP4_EXPORT nvfp4_status nvfp4_distill_loss(const void* student, int64_t student_stride,
@@ -248,7 +502,7 @@ NVFP4_EXPORT nvfp4_status nvfp4_distill_loss(const void* student, int64_t studen
                                              int64_t grad_stride, void* workspace,
                                              hipStream_t stream) {
   if (!known(stype) || !known(ttype)) return NVFP4_ERR_ENUM;
-  if (!shape_ok(rows, vocab, student_stride) || !shape_ok(rows, vocab, teacher_stride) ||
+  if (vocab > kMaxVocab || !shape_ok(rows, vocab, student_stride) || !shape_ok(rows, vocab, teacher_stride) ||
       (grad && !shape_ok(rows, vocab, grad_stride)))
     return NVFP4_ERR_SHAPE;
   const float inv_t = 1.0f / temperature, c = (float)(1.4426950408889634 / (double)temperature);
@@ -275,9 +529,10 @@ NVFP4_EXPORT nvfp4_status nvfp4_distill_loss(const void* student, int64_t studen
   }
   const int splits = splits_of(rows, vocab);
   float* ws = (float*)workspace;
-  Distill a = {student, teacher, weight, loss, grad, ws, ws + rows * splits * 4,
-               (uint32_t*)(ws + rows * splits * 5), student_stride, teacher_stride, grad_stride,
-               rows, vocab, ((vocab + splits - 1) / splits + 7) / 8 * 8, splits, c, inv_t};
+  Distill a = {student, teacher, weight, loss, grad, ws, ws + rows * splits * 8,
+               (uint32_t*)(ws + rows * splits * 9), student_stride, teacher_stride, grad_stride,
+               rows, (uint32_t)vocab, (uint32_t)(((vocab + splits - 1) / splits + 7) / 8 * 8), splits,
+               c, temperature};
   (void)hipGetLastError();
   if (stype == NVFP4_T_BF16 && ttype == NVFP4_T_BF16) launch<bf16, bf16>(a, stream);
   else if (stype == NVFP4_T_BF16) launch<bf16, float>(a, stream);

@@ -265,12 +265,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void backward_kernel(const B
         slots[turn][1][threadIdx.x >> 6] = s2;
       }
       __syncthreads();
-      s1 = s2 = 0.0f;
-#pragma unroll
-      for (int i = 0; i < WAVES; ++i) {
-        s1 += slots[turn][0][i];
-        s2 += slots[turn][1][i];
-      }
+      s1 = reduce_few<WAVES>(slots[turn][0][threadIdx.x % WAVES], Sum());
+      s2 = reduce_few<WAVES>(slots[turn][1][threadIdx.x % WAVES], Sum());
     }
     const float c1 = a.mean ? s1 * inv : 0.0f, c2 = s2 * inv;
 #pragma unroll

@@ -100,10 +100,34 @@ __device__ __forceinline__ void store_vec(float* p, const Vec8<float>& v) {
   q[1] = v.w2;
 }
 
+// Four binary32 elements, where a lane's 16 bytes are to touch its neighbours'.
+struct Vec4 {
+  u32x4 w;
+  __device__ __forceinline__ float operator[](int i) const { return __uint_as_float(w[i]); }
+};
+
 // Makes the compiler forget how v came about (no instruction): what was computed from it
 // before is computed again rather than kept in registers.
 __device__ __forceinline__ void opaque(Vec8<bf16>& v) { asm("" : "+v"(v.w)); }
 __device__ __forceinline__ void opaque(Vec8<float>& v) { asm("" : "+v"(v.w), "+v"(v.w2)); }
+__device__ __forceinline__ void opaque(Vec4& v) { asm("" : "+v"(v.w)); }
+
+// The same past the caches, for data that no later kernel is likely to find there.
+__device__ __forceinline__ void store_stream(bf16* p, const Vec8<bf16>& v) {
+  __builtin_nontemporal_store(v.w, reinterpret_cast<u32x4_a2*>(p));
+}
+__device__ __forceinline__ void store_stream(float* p, const Vec8<float>& v) {
+  u32x4_a2* q = reinterpret_cast<u32x4_a2*>(p);
+  __builtin_nontemporal_store(v.w, q);
+  __builtin_nontemporal_store(v.w2, q + 1);
+}
+__device__ __forceinline__ Vec8<bf16> load_stream(const bf16* p) {
+  return {__builtin_nontemporal_load(reinterpret_cast<const u32x4_a2*>(p))};
+}
+__device__ __forceinline__ Vec8<float> load_stream(const float* p) {
+  const u32x4_a2* q = reinterpret_cast<const u32x4_a2*>(p);
+  return {__builtin_nontemporal_load(q), __builtin_nontemporal_load(q + 1)};
+}
 
 template <typename T>
 __device__ __forceinline__ Vec8<T> zero_vec() {
@@ -209,18 +233,24 @@ __device__ __forceinline__ V reduce64(V v, Op op) {
   v = reduce16(v, op);
   return op(op(read_lane(v, 0), read_lane(v, 16)), op(read_lane(v, 32), read_lane(v, 48)));
 }
-// Over a workgroup of WAVES wavefronts through `slots` (WAVES entries of LDS): every lane gets
-// the result.  The caller keeps a barrier between two uses of the same slots.
+// Over groups of N neighbouring lanes that hold N values, repeated: every lane gets the result.
+template <int N, typename Op, typename V>
+__device__ __forceinline__ V reduce_few(V v, Op op) {
+  if (N >= 16) v = op(v, rotate16<8>(v));
+  if (N >= 8) v = op(v, rotate16<4>(v));
+  if (N >= 4) v = op(v, rotate16<2>(v));
+  if (N >= 2) v = op(v, rotate16<1>(v));
+  return v;
+}
+// Over a workgroup of WAVES (a power of two) wavefronts through `slots` (WAVES entries of LDS):
+// every lane gets the result.  The caller keeps a barrier between two uses of the same slots.
 template <int WAVES, typename Op, typename V>
 __device__ __forceinline__ V reduce_group(V v, Op op, V* slots) {
   v = reduce64(v, op);
   if (WAVES == 1) return v;
   if ((threadIdx.x & 63) == 0) slots[threadIdx.x >> 6] = v;
   __syncthreads();
-  V r = slots[0];
-#pragma unroll
-  for (int i = 1; i < WAVES; ++i) r = op(r, slots[i]);
-  return r;
+  return reduce_few<WAVES>(slots[threadIdx.x % WAVES], op);
 }
 
 __global__ void clear_words(uint32_t* p, int64_t n);
