@@ -127,7 +127,7 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const Batch a) {
 #pragma unroll 1
   for (int step = 0; step < kSteps; ++step) {
     const int64_t at = base + (int64_t)(step * kThreads + threadIdx.x) * 8;
-    const Vec8<G> g8 = load_vec<kAny>((const G*)t.grad, at, n);
+    const Vec<G, 8> g8 = load_vec<8, kAny>((const G*)t.grad, at, n);
     float m[8], v[8], p[8];
     if (E4M3) {
       const int64_t block = at / NVFP4_ADAMW_BLOCK;
@@ -135,8 +135,8 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const Batch a) {
       decode(load_bytes((const uint8_t*)t.exp_avg, at, n), ms, m);
       decode(load_bytes((const uint8_t*)t.exp_avg_sq, at, n), vs, v);
     } else {
-      const Vec8<float> m8 = load_vec<kAny>((const float*)t.exp_avg, at, n);
-      const Vec8<float> v8 = load_vec<kAny>((const float*)t.exp_avg_sq, at, n);
+      const Vec<float, 8> m8 = load_vec<8, kAny>((const float*)t.exp_avg, at, n);
+      const Vec<float, 8> v8 = load_vec<8, kAny>((const float*)t.exp_avg_sq, at, n);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         m[i] = m8[i];
@@ -144,11 +144,11 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const Batch a) {
       }
     }
     if (P == kAlone) {
-      const Vec8<bf16> p8 = load_vec<kAny>((const bf16*)t.param, at, n);
+      const Vec<bf16, 8> p8 = load_vec<8, kAny>((const bf16*)t.param, at, n);
 #pragma unroll
       for (int i = 0; i < 8; ++i) p[i] = p8[i];
     } else {
-      const Vec8<float> p8 = load_vec<kAny>(P == kF32 ? (const float*)t.param : t.master, at, n);
+      const Vec<float, 8> p8 = load_vec<8, kAny>(P == kF32 ? (const float*)t.param : t.master, at, n);
 #pragma unroll
       for (int i = 0; i < 8; ++i) p[i] = p8[i];
     }
@@ -177,10 +177,10 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const Batch a) {
         t.sq_scale[at / NVFP4_ADAMW_BLOCK] = vs;
       }
     } else {
-      store_vec<kAny>((float*)t.exp_avg, at, n, make_vec(m, 0.0f));
-      store_vec<kAny>((float*)t.exp_avg_sq, at, n, make_vec(v, 0.0f));
+      store_vec<kAny>((float*)t.exp_avg, at, n, make_vec<float>(m));
+      store_vec<kAny>((float*)t.exp_avg_sq, at, n, make_vec<float>(v));
     }
-    if (P == kMaster) store_vec<kAny>(t.master, at, n, make_vec(p, 0.0f));
+    if (P == kMaster) store_vec<kAny>(t.master, at, n, make_vec<float>(p));
     if (P == kAlone) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -190,9 +190,9 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const Batch a) {
       }
     }
     if (P == kF32) {
-      store_vec<kAny>((float*)t.param, at, n, make_vec(p, 0.0f));
+      store_vec<kAny>((float*)t.param, at, n, make_vec<float>(p));
     } else {
-      const Vec8<bf16> out = make_vec(p, bf16());
+      const Vec<bf16, 8> out = make_vec<bf16>(p);
       store_vec<kAny>((bf16*)t.param, at, n, out);
 #pragma unroll
       for (int i = 0; i < 8; ++i) p[i] = out[i];
@@ -203,10 +203,7 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const Batch a) {
         if (at + i < n) most = max(most, __float_as_uint(p[i]) & 0x7FFFFFFFu);
     }
   }
-  if (AMAX) {
-    most = reduce_group<kThreads / 64>(most, Max(), slots);
-    if (threadIdx.x == 0 && most != 0) atomicMax(a.amax + a.index + lo, most);
-  }
+  if (AMAX) publish_amax<kThreads / 64>(most, a.amax + a.index + lo, slots);
 }
 
 template <Param P, typename G, bool E4M3>

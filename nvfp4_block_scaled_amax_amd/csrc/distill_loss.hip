@@ -69,31 +69,6 @@ constexpr float kSlack = 16.0f;      // how far (in powers of two) entries may p
 // binary32, so that a wavefront's 16-byte loads are next to each other.
 template <typename S, typename T>
 constexpr int kUnit = sizeof(S) == 4 && sizeof(T) == 4 ? 4 : 8;
-template <typename T, int N>
-struct UnitOf {
-  typedef Vec8<T> type;
-  static __device__ __forceinline__ type load(const T* p) { return load_vec(p); }
-  static __device__ __forceinline__ type stream(const T* p) { return load_stream(p); }
-  static __device__ __forceinline__ void store(T* p, const float (&v)[N]) {
-    store_stream(p, make_vec(v, T()));
-  }
-};
-template <>
-struct UnitOf<float, 4> {
-  typedef Vec4 type;
-  static __device__ __forceinline__ type load(const float* p) {
-    return {*reinterpret_cast<const u32x4_a2*>(p)};
-  }
-  static __device__ __forceinline__ type stream(const float* p) {
-    return {__builtin_nontemporal_load(reinterpret_cast<const u32x4_a2*>(p))};
-  }
-  static __device__ __forceinline__ void store(float* p, const float (&v)[4]) {
-    const u32x4 w = {__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
-                     __float_as_uint(v[3])};
-    __builtin_nontemporal_store(w, reinterpret_cast<u32x4_a2*>(p));
-  }
-};
-
 // sum 2^(fma(x, c, -r)).  An empty one has r = the lowest finite value and sum 0; an entry of
 // -inf adds 0 to any.  `m` is an entry with r = c m (an r that overflows makes the sum useless:
 // see good()).
@@ -104,8 +79,8 @@ struct Stat {
     z = z * exp2_(r - top) + o.z * exp2_(o.r - top);
     r = top;
   }
-  template <int N, typename V>
-  __device__ __forceinline__ void add(const V& v, float c) {
+  template <typename T, int N>
+  __device__ __forceinline__ void add(const Vec<T, N>& v, float c) {
     float top = v[0];
 #pragma unroll
     for (int i = 1; i < N; ++i) top = fmaxf(top, v[i]);
@@ -160,10 +135,8 @@ struct Row {
   const T* t;
   uint32_t lo, hi, whole;      // whole: end of the last unit
   static constexpr int N = kUnit<S, T>;
-  typedef UnitOf<S, N> US;
-  typedef UnitOf<T, N> UT;
-  typedef typename US::type VS;
-  typedef typename UT::type VT;
+  typedef Vec<S, N> VS;
+  typedef Vec<T, N> VT;
   VS a[REGS > 0 ? REGS : 1];
   VT b[REGS > 0 ? REGS : 1];
 
@@ -193,13 +166,13 @@ struct Row {
     if (lo < whole) {
 #pragma unroll
       for (int k = 0; k < REGS; ++k) {
-        a[k] = US::stream(s + inside(k));
-        b[k] = UT::stream(t + inside(k));
+        a[k] = load_vec<N, true>(s + inside(k));
+        b[k] = load_vec<N, true>(t + inside(k));
       }
 #pragma unroll
       for (int k = 0; k < LDS; ++k) {
-        const VS x = US::stream(s + inside(REGS + k));
-        const VT y = UT::stream(t + inside(REGS + k));
+        const VS x = load_vec<N, true>(s + inside(REGS + k));
+        const VT y = load_vec<N, true>(t + inside(REGS + k));
         *lds_a(lds, k) = x;
         *lds_b(lds, k) = y;
         if (place(REGS + k) < whole) f(x, y);
@@ -209,7 +182,7 @@ struct Row {
         if (place(k) < whole) f(a[k], b[k]);
     }
     for (uint32_t at = place(REGS + LDS); at < whole; at += THREADS * N)
-      f(US::load(s + at), UT::load(t + at));
+      f(load_vec<N>(s + at), load_vec<N>(t + at));
     const uint32_t at = whole + threadIdx.x;
     if (at < hi) g(to_f32(s[at]), to_f32(t[at]));
   }
@@ -227,7 +200,7 @@ struct Row {
     for (int k = 0; k < LDS; ++k)
       if (place(REGS + k) < whole) f(place(REGS + k), *lds_a(lds, k), *lds_b(lds, k));
     for (uint32_t at = place(REGS + LDS); at < whole; at += THREADS * N)
-      f(at, US::load(s + at), UT::load(t + at));
+      f(at, load_vec<N>(s + at), load_vec<N>(t + at));
     const uint32_t at = whole + threadIdx.x;
     if (at < hi) g(at, to_f32(s[at]), to_f32(t[at]));
   }
@@ -238,7 +211,7 @@ template <int THREADS, typename R>
 __device__ __forceinline__ void row_stats(R& row, void* lds, float c, Stat& q, Stat& p,
                                           float (*slots)[4]) {
   q = p = Stat{kLowest, 0.0f};
-  row.load(lds, [&](const auto& a, const auto& b) { q.template add<R::N>(a, c), p.template add<R::N>(b, c); },
+  row.load(lds, [&](const auto& a, const auto& b) { q.add(a, c), p.add(b, c); },
            [&](float a, float b) {
              if (a != -INFINITY) q.join(Stat{a * c, 1.0f});
              if (b != -INFINITY) p.join(Stat{b * c, 1.0f});
@@ -302,7 +275,7 @@ __device__ __forceinline__ float row_grad(R& row, void* lds, S* grad, float c, f
             flat += g[i];
           }
         }
-        if (grad) R::US::store(grad + at, g);
+        if (grad) store_vec<true>(grad + at, make_vec<S>(g));
       },
       [&](uint32_t at, float a, float b) {
         const float y = fmaf(a, c, -r), x = fmaf(b, c, -p.r);
@@ -338,7 +311,7 @@ __device__ __forceinline__ float row_grad_exact(const S* s, const T* t, S* grad,
 template <int THREADS, typename S>
 __device__ __forceinline__ void zero_grad(S* grad, uint32_t lo, uint32_t hi) {
   const uint32_t whole = lo + (hi - lo) / 8 * 8;
-  const Vec8<S> z = zero_vec<S>();
+  const Vec<S, 8> z = zero_vec<S, 8>();
   for (uint32_t at = lo + threadIdx.x * 8; at < whole; at += THREADS * 8) store_vec(grad + at, z);
   if (whole + threadIdx.x < hi) grad[whole + threadIdx.x] = from_f32<S>(0.0f);
 }

@@ -36,65 +36,70 @@ struct Backward {
   const float* rstd;
   const void* dres;
   void* dx;
-  float* partial;     // [groups][2][cols]: dweight, dbias
+  float* partial;     // [groups][sums][cols]: dweight, and with sums == 2 dbias
   int64_t rows;
-  int cols;
+  int cols, sums;
 };
 
-// The columns of a held row: known to be in 8 .. TPR * K * 8, so that offsets take 32 bits.
-template <int TPR, int K>
+// A lane's vector: 16 bytes of T, so that a wavefront's loads are next to each other.
+template <typename T>
+constexpr int kVec = 16 / sizeof(T);
+template <typename T>
+constexpr int kUnits = 8 / kVec<T>;
+
+// The columns of a held row: known to be in 8 .. MOST, so that offsets take 32 bits.
+template <int MOST>
 __device__ __forceinline__ uint32_t held_cols(int cols) {
-  __builtin_assume(cols >= 8 && cols <= TPR * K * 8);
+  __builtin_assume(cols >= 8 && cols <= MOST);
   return (uint32_t)cols;
 }
 // Which row of the workgroup's this thread is at, as a scalar.
 template <int TPR>
 __device__ __forceinline__ uint32_t wave_of() {
-  return TPR < 256 ? __builtin_amdgcn_readfirstlane(threadIdx.x / TPR) : 0u;
+  return TPR == 64 ? __builtin_amdgcn_readfirstlane(threadIdx.x / TPR) : 0u;
+}
+
+// A value that the whole wavefront wants from memory that no kernel in flight writes, through the
+// scalar cache.
+__device__ __forceinline__ float scalar_load(const float* p) {
+  return *(const __attribute__((address_space(4))) float*)(uintptr_t)p;
 }
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
-// A workgroup's part of the tensor maximum: on the bits, where inf and NaN sort above the rest.
-template <int WAVES>
-__device__ __forceinline__ void publish_amax(uint32_t m, uint32_t* amax, uint32_t* slots) {
-  m = reduce_group<WAVES>(m, Max(), slots);
-  if (threadIdx.x == 0 && m != 0) atomicMax(amax, m);
-}
-
 // One row: TPR lanes hold K vectors each.  With TPR == 64 a workgroup takes 4 rows at a time.
 template <typename T, typename W, int TPR, int K, End E>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void forward_kernel(const Forward a) {
-  constexpr int WAVES = TPR / 64, ROWS = TPR < 256 ? 256 / TPR : 1;
+__global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void forward_kernel(const Forward a) {
+  constexpr int N = kVec<T>, WAVES = TPR / 64, ROWS = TPR == 64 ? 4 : 1;
   __shared__ float slots[2][WAVES];
-  __shared__ uint32_t top[TPR < 256 ? 4 : WAVES];
-  const uint32_t lane = threadIdx.x % TPR, cols = held_cols<TPR, K>(a.cols);
+  __shared__ uint32_t top[TPR == 64 ? 4 : WAVES];
+  const uint32_t lane = threadIdx.x % TPR, cols = held_cols<TPR * K * N>(a.cols);
   const float inv = 1.0f / (float)a.cols;
   uint32_t most = 0;
   for (int64_t row = (int64_t)blockIdx.x * ROWS + wave_of<TPR>(); row < a.rows;
        row += (int64_t)gridDim.x * ROWS) {
     const T* x = (const T*)a.x + row * a.x_stride;
-    float v[K][8];
+    float v[K][N];
     float sum = 0.0f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const Vec8<T> q = load_vec<E>(x, (k * TPR + lane) * 8, cols);
+      const Vec<T, N> q = load_vec<N, E>(x, (k * TPR + lane) * N, cols);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[k][i] = q[i];
+      for (int i = 0; i < N; ++i) v[k][i] = q[i];
     }
     if (a.residual) {
       const T* r = (const T*)a.residual + row * a.residual_stride;
       T* h = (T*)a.h + row * a.cols;
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        const uint32_t at = (k * TPR + lane) * 8;
-        const Vec8<T> q = load_vec<E>(r, at, cols);
+        const uint32_t at = (k * TPR + lane) * N;
+        const Vec<T, N> q = load_vec<N, E>(r, at, cols);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[k][i] += q[i];
-        const Vec8<T> s = make_vec(v[k], T());
+        for (int i = 0; i < N; ++i) v[k][i] += q[i];
+        const Vec<T, N> s = make_vec<T>(v[k]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[k][i] = s[i];
-        store_vec<E>(h, at, cols, s);
+        for (int i = 0; i < N; ++i) v[k][i] = s[i];
+        store_vec<E, true>(h, at, cols, s);
       }
     }
     float mean = 0.0f;
@@ -102,15 +107,15 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void forward_kernel(const Fo
 #pragma unroll
       for (int k = 0; k < K; ++k)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum += v[k][i];
+        for (int i = 0; i < N; ++i) sum += v[k][i];
       mean = reduce_group<WAVES>(sum, Sum(), slots[0]) * inv;
     }
     float sq = 0.0f;
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float d = (k * TPR + lane) * 8 + i < cols ? v[k][i] - mean : 0.0f;
+      for (int i = 0; i < N; ++i) {
+        const float d = (k * TPR + lane) * N + i < cols ? v[k][i] - mean : 0.0f;
         sq += d * d;
       }
     const float var = reduce_group<WAVES>(sq, Sum(), slots[1]) * inv;
@@ -122,26 +127,26 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void forward_kernel(const Fo
     T* y = (T*)a.y + row * a.cols;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const uint32_t at = (k * TPR + lane) * 8;
-      const Vec8<W> w = load_vec<E>((const W*)a.weight, at, cols);
+      const uint32_t at = (k * TPR + lane) * N;
+      const Vec<W, N> w = load_vec<N, E>((const W*)a.weight, at, cols);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[k][i] = (v[k][i] - mean) * rstd * w[i];
+      for (int i = 0; i < N; ++i) v[k][i] = (v[k][i] - mean) * rstd * w[i];
       if (a.bias) {
-        const Vec8<W> b = load_vec<E>((const W*)a.bias, at, cols);
+        const Vec<W, N> b = load_vec<N, E>((const W*)a.bias, at, cols);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[k][i] += b[i];
+        for (int i = 0; i < N; ++i) v[k][i] += b[i];
       }
-      const Vec8<T> out = make_vec(v[k], T());
-      store_vec<E>(y, at, cols, out);
+      const Vec<T, N> out = make_vec<T>(v[k]);
+      store_vec<E, true>(y, at, cols, out);
       if (a.amax) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < N; ++i)
           if (at + i < cols) most = max(most, abs_bits(out[i]));
       }
     }
     if (WAVES > 1) __syncthreads();     // the slots are free for the next row
   }
-  if (a.amax) publish_amax<(TPR < 256 ? 4 : WAVES)>(most, a.amax, top);
+  if (a.amax) publish_amax<(TPR == 64 ? 4 : WAVES)>(most, a.amax, top);
 }
 
 // Rows longer than the registers hold (and those under 8 columns): three passes over the row.
@@ -155,11 +160,11 @@ __global__ __launch_bounds__(1024) void forward_long_kernel(const Forward a) {
     const T* x = (const T*)a.x + row * a.x_stride;
     const T* r = a.residual ? (const T*)a.residual + row * a.residual_stride : nullptr;
     auto held = [&](int64_t at, float (&v)[8]) {
-      const Vec8<T> q = load_vec<kAny>(x, at, (int64_t)a.cols);
+      const Vec<T, 8> q = load_vec<8, kAny>(x, at, (int64_t)a.cols);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = q[i];
       if (r) {
-        const Vec8<T> p = load_vec<kAny>(r, at, (int64_t)a.cols);
+        const Vec<T, 8> p = load_vec<8, kAny>(r, at, (int64_t)a.cols);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = rounded<T>(v[i] + p[i]);
       }
@@ -189,16 +194,16 @@ __global__ __launch_bounds__(1024) void forward_long_kernel(const Forward a) {
     }
     for (int64_t at = threadIdx.x * 8; at < a.cols; at += 8192) {
       held(at, v);
-      if (r) store_vec<kAny>((T*)a.h + row * a.cols, at, (int64_t)a.cols, make_vec(v, T()));
-      const Vec8<W> w = load_vec<kAny>((const W*)a.weight, at, (int64_t)a.cols);
+      if (r) store_vec<kAny>((T*)a.h + row * a.cols, at, (int64_t)a.cols, make_vec<T>(v));
+      const Vec<W, 8> w = load_vec<8, kAny>((const W*)a.weight, at, (int64_t)a.cols);
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = (v[i] - mean) * rstd * w[i];
       if (a.bias) {
-        const Vec8<W> b = load_vec<kAny>((const W*)a.bias, at, (int64_t)a.cols);
+        const Vec<W, 8> b = load_vec<8, kAny>((const W*)a.bias, at, (int64_t)a.cols);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] += b[i];
       }
-      const Vec8<T> out = make_vec(v, T());
+      const Vec<T, 8> out = make_vec<T>(v);
       store_vec<kAny>((T*)a.y + row * a.cols, at, (int64_t)a.cols, out);
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -209,51 +214,228 @@ __global__ __launch_bounds__(1024) void forward_long_kernel(const Forward a) {
   if (a.amax) publish_amax<16>(most, a.amax, top);
 }
 
-template <typename T, typename W, int TPR, int K, End E>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void backward_kernel(const Backward a) {
-  constexpr int WAVES = TPR / 64, ROWS = TPR < 256 ? 256 / TPR : 1;
-  __shared__ float slots[2][2][WAVES];
-  const uint32_t lane = threadIdx.x % TPR, sub = wave_of<TPR>();
-  const uint32_t cols = held_cols<TPR, K>(a.cols);
+// A row in a wavefront: K vectors per lane.  Each wavefront goes its own way to the end, where the
+// workgroup adds their column sums in order.
+template <typename T, typename W, int THREADS, int K, End E>
+__global__ __launch_bounds__(THREADS) void backward_wave_kernel(const Backward a) {
+  constexpr int N = kVec<T>, WAVES = THREADS / 64;
+  __shared__ float part[WAVES][64 * N];
+  const uint32_t lane = threadIdx.x % 64, cols = held_cols<64 * K * N>(a.cols);
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const float inv = 1.0f / (float)a.cols;
-  // 1024 threads have 128 registers each: there the weights are read again for every use
-  constexpr bool HOLD = TPR < 1024;
-  auto weight = [&](int k) {
-    uint32_t at = (k * TPR + lane) * 8;
-    if (!HOLD) asm volatile("" : "+v"(at));          // not taken out of the row loop
-    return load_vec<E>((const W*)a.weight, at, cols);
-  };
-  Vec8<W> held[HOLD ? K : 1];
-  float dw[K][8], db[K][8];
+  float dw[K][N], db[K][N];
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    if (HOLD) held[k] = weight(k);
+  for (int k = 0; k < K; ++k)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) dw[k][i] = db[k][i] = 0.0f;
-  }
-  int turn = 0;
-  for (int64_t row = (int64_t)blockIdx.x * ROWS + sub; row < a.rows;
-       row += (int64_t)gridDim.x * ROWS, turn ^= 1) {
-    Vec8<T> dy[K], h[K];
+    for (int i = 0; i < N; ++i) dw[k][i] = db[k][i] = 0.0f;
+  for (int64_t row = (int64_t)blockIdx.x * WAVES + wave; row < a.rows;
+       row += (int64_t)gridDim.x * WAVES) {
+    Vec<T, N> dy[K], h[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const uint32_t at = (k * TPR + lane) * 8;
-      dy[k] = load_vec<E>((const T*)a.dy + row * a.cols, at, cols);
-      h[k] = load_vec<E>((const T*)a.h + row * a.cols, at, cols);
+      const uint32_t at = (k * 64 + lane) * N;
+      dy[k] = load_vec<N, E>((const T*)a.dy + row * a.cols, at, cols);
+      h[k] = load_vec<N, E>((const T*)a.h + row * a.cols, at, cols);
     }
     const float mean = a.mean ? a.mean[row] : 0.0f, rstd = a.rstd[row];
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const Vec8<W> w = HOLD ? held[HOLD ? k : 0] : weight(k);
+      uint32_t at = (k * 64 + lane) * N;
+      asm volatile("" : "+v"(at));       // read again for each row: not worth registers
+      const Vec<W, N> w = load_vec<N, E>((const W*)a.weight, at, cols);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float xh = (h[k][i] - mean) * rstd, g = dy[k][i] * w[i];
+      for (int i = 0; i < N; ++i) {
+        const float xh = (h[k][i] - mean) * rstd, d = dy[k][i], g = d * w[i];
         s1 += g;
         s2 = fmaf(g, xh, s2);
-        dw[k][i] = fmaf(dy[k][i], xh, dw[k][i]);
-        db[k][i] += dy[k][i];
-        asm volatile("" : "+v"(dw[k][i]), "+v"(db[k][i]));   // here, not at the loop's end
+        dw[k][i] = fmaf(d, xh, dw[k][i]);
+        db[k][i] += d;
+        asm volatile("" : "+v"(s1), "+v"(s2), "+v"(dw[k][i]), "+v"(db[k][i]));   // here, not later
+      }
+    }
+    // dx = rstd (g - c1 - xh c2), with both constants times rstd
+    const float c1 = a.mean ? reduce64(s1, Sum()) * inv * rstd : 0.0f;
+    const float c2 = reduce64(s2, Sum()) * inv * rstd * rstd;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      uint32_t at = (k * 64 + lane) * N;
+      opaque(at, c2);
+      opaque(dy[k], c2);  // unpacked again from here: the floats need not live across the sums
+      opaque(h[k], c2);
+      const Vec<W, N> w = load_vec<N, E>((const W*)a.weight, at, cols);
+      float d[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        d[i] = fmaf(mean - h[k][i], c2, fmaf(dy[k][i] * w[i], rstd, -c1));
+      }
+      if (a.dres) {
+        const Vec<T, N> r = load_vec<N, E>((const T*)a.dres + row * a.cols, at, cols);
+#pragma unroll
+        for (int i = 0; i < N; ++i) d[i] += r[i];
+      }
+      store_vec<E, true>((T*)a.dx + row * a.cols, at, cols, make_vec<T>(d));
+    }
+  }
+  float* out = a.partial + (int64_t)blockIdx.x * a.sums * a.cols;
+  for (int v = 0; v < a.sums; ++v, out += cols) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) part[wave][lane * N + i] = v ? db[k][i] : dw[k][i];
+      __syncthreads();
+      for (uint32_t c = threadIdx.x; c < 64 * N; c += THREADS) {
+        float s = part[0][c];
+#pragma unroll
+        for (int r = 1; r < WAVES; ++r) s += part[r][c];
+        if (k * 64 * N + c < cols) out[k * 64 * N + c] = s;
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// Rows of a multiple of 512 columns: a workgroup of cols / (K * N) threads takes one row at a time
+// and loads the next one meanwhile.  Nothing may stand between those loads and their use a row
+// later that waits for vector memory in order: the weights lie in shared memory, the
+// statistics come through the scalar cache, and no load or store depends on a condition, so that
+// the compiler can count them.
+template <typename T, typename W, int K, bool RES>
+__global__ __launch_bounds__(1024) void backward_full_kernel(const Backward a) {
+  constexpr int N = kVec<T>;
+  __shared__ float slots[2][2][16];
+  extern __shared__ __align__(16) char dynamic[];
+  Vec<W, N>* const weight = (Vec<W, N>*)dynamic + threadIdx.x;       // [K][threads], by vectors
+  const uint32_t threads = blockDim.x, at = threadIdx.x * N;
+  const int64_t cols = (int64_t)threads * (K * N);
+  const float inv = 1.0f / (float)a.cols;
+  float dw[K][N], db[K][N];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    weight[k * threads] = load_vec<N>((const W*)a.weight + k * threads * N + at);
+#pragma unroll
+    for (int i = 0; i < N; ++i) dw[k][i] = db[k][i] = 0.0f;
+  }
+  if (threadIdx.x < 64) ((float*)slots)[threadIdx.x] = 0.0f;         // those of wavefronts not there
+  __syncthreads();
+  const int64_t step = gridDim.x;
+  const int64_t last = a.rows - 1;
+  Vec<T, N> dy[K], h[K], dy2[K], h2[K], res[K];
+  auto load = [&](const void* base, int64_t row, Vec<T, N> (&v)[K]) {
+    const T* p = (const T*)base + row * cols;
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = load_vec<N>(p + (k * threads * N + at));
+  };
+  load(a.dy, blockIdx.x, dy2);
+  load(a.h, blockIdx.x, h2);
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row <= last; row += step, turn ^= 1) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) dy[k] = dy2[k], h[k] = h2[k];
+    if (RES) load(a.dres, row, res);
+    const int64_t ahead = row + step <= last ? row + step : last;     // one too many at the end
+    load(a.dy, ahead, dy2);
+    load(a.h, ahead, h2);
+    const float mean = a.mean ? scalar_load(a.mean + row) : 0.0f, rstd = scalar_load(a.rstd + row);
+    float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const Vec<W, N> w = weight[k * threads];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float xh = (h[k][i] - mean) * rstd, d = dy[k][i], g = d * w[i];
+        s1 += g;
+        s2 = fmaf(g, xh, s2);
+        dw[k][i] = fmaf(d, xh, dw[k][i]);
+        db[k][i] += d;
+        asm volatile("" : "+v"(s1), "+v"(s2), "+v"(dw[k][i]), "+v"(db[k][i]));   // here, not later
+      }
+    }
+    // the slots of two rows in turn: one barrier per row is enough
+    s1 = reduce64(s1, Sum());
+    s2 = reduce64(s2, Sum());
+    if ((threadIdx.x & 63) == 0) {
+      slots[turn][0][threadIdx.x >> 6] = s1;
+      slots[turn][1][threadIdx.x >> 6] = s2;
+    }
+    lds_barrier();
+    s1 = reduce16(slots[turn][0][threadIdx.x % 16], Sum());
+    s2 = reduce16(slots[turn][1][threadIdx.x % 16], Sum());
+    // dx = rstd (g - c1 - xh c2), with both constants times rstd
+    const float c1 = a.mean ? s1 * inv * rstd : 0.0f, c2 = s2 * inv * rstd * rstd;
+    T* dx = (T*)a.dx + row * cols;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float d[N];
+      opaque(dy[k], c2);      // unpacked again from here: the floats need not live across the sums
+      opaque(h[k], c2);
+      const Vec<W, N> w = weight[k * threads];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        d[i] = fmaf(mean - h[k][i], c2, fmaf(dy[k][i] * w[i], rstd, -c1));
+        if (RES) d[i] += res[k][i];
+      }
+      store_vec<true>(dx + (k * threads * N + at), make_vec<T>(d));
+    }
+  }
+  float* out = a.partial + (int64_t)blockIdx.x * a.sums * cols;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    store_vec(out + (k * threads * N + at), make_vec<float>(dw[k]));
+    if (a.sums == 2) store_vec(out + cols + (k * threads * N + at), make_vec<float>(db[k]));
+  }
+}
+
+// Other rows: workgroups of 1024 threads take 1024 / TPR rows at a time, K vectors per lane.
+template <typename T, typename W, int TPR, int K, End E>
+__global__ __launch_bounds__(1024, K * kVec<T> == 8 && sizeof(T) == 2 ? 8 : 4) void backward_kernel(
+    const Backward a) {
+  constexpr int N = kVec<T>, WAVES = TPR / 64, ROWS = 1024 / TPR;
+  __shared__ float slots[2][2][16];
+  extern __shared__ __align__(16) char dynamic[];
+  Vec<W, N>* const weight = (Vec<W, N>*)dynamic;       // [K * TPR], by vectors
+  float* const part = (float*)dynamic;                 // [ROWS][K * TPR * N], once the rows are done
+  const uint32_t lane = threadIdx.x % TPR, cols = held_cols<TPR * K * N>(a.cols);
+  const uint32_t sub = __builtin_amdgcn_readfirstlane(threadIdx.x / TPR);
+  const float inv = 1.0f / (float)a.cols;
+  for (uint32_t j = threadIdx.x; j < K * TPR; j += 1024)
+    weight[j] = load_vec<N, E>((const W*)a.weight, j * N, cols);
+  __syncthreads();
+  float dw[K][N], db[K][N];
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int i = 0; i < N; ++i) dw[k][i] = db[k][i] = 0.0f;
+  Vec<T, N> dy[K], h[K];
+  const int64_t stride = (int64_t)gridDim.x * ROWS;
+  int turn = 0;
+  for (int64_t first = (int64_t)blockIdx.x * ROWS; first < a.rows; first += stride, turn ^= 1) {
+    const int64_t row = first + sub;
+    const bool mine = row < a.rows;
+    if (mine) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const uint32_t at = (k * TPR + lane) * N;
+        dy[k] = load_vec<N, E>((const T*)a.dy + row * a.cols, at, cols);
+        h[k] = load_vec<N, E>((const T*)a.h + row * a.cols, at, cols);
+      }
+    }
+    const float mean = a.mean && mine ? scalar_load(a.mean + row) : 0.0f;
+    const float rstd = mine ? scalar_load(a.rstd + row) : 0.0f;
+    float s1 = 0.0f, s2 = 0.0f;
+    if (mine) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        const Vec<W, N> w = weight[k * TPR + lane];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const float xh = (h[k][i] - mean) * rstd, d = dy[k][i], g = d * w[i];
+          s1 += g;
+          s2 = fmaf(g, xh, s2);
+          dw[k][i] = fmaf(d, xh, dw[k][i]);
+          db[k][i] += d;
+          asm volatile("" : "+v"(s1), "+v"(s2), "+v"(dw[k][i]), "+v"(db[k][i]));   // here, not later
+        }
       }
     }
     // the slots of two rows in turn: one barrier per row is enough
@@ -265,56 +447,53 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void backward_kernel(const B
         slots[turn][1][threadIdx.x >> 6] = s2;
       }
       __syncthreads();
-      s1 = reduce_few<WAVES>(slots[turn][0][threadIdx.x % WAVES], Sum());
-      s2 = reduce_few<WAVES>(slots[turn][1][threadIdx.x % WAVES], Sum());
+      s1 = reduce_few<WAVES>(slots[turn][0][sub * WAVES + lane % WAVES], Sum());
+      s2 = reduce_few<WAVES>(slots[turn][1][sub * WAVES + lane % WAVES], Sum());
     }
-    const float c1 = a.mean ? s1 * inv : 0.0f, c2 = s2 * inv;
+    if (mine) {
+      // dx = rstd (g - c1 - xh c2), with both constants times rstd
+      const float c1 = a.mean ? s1 * inv * rstd : 0.0f, c2 = s2 * inv * rstd * rstd;
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const uint32_t at = (k * TPR + lane) * 8;
-      float d[8];
-      opaque(dy[k]);      // unpacked again from here: the floats need not live across the sums
-      opaque(h[k]);
-      const Vec8<W> w = HOLD ? held[HOLD ? k : 0] : weight(k);
+      for (int k = 0; k < K; ++k) {
+        const uint32_t at = (k * TPR + lane) * N;
+        float d[N];
+        opaque(dy[k], c2);    // unpacked again from here: the floats need not live across the sums
+        opaque(h[k], c2);
+        const Vec<W, N> w = weight[k * TPR + lane];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float xh = (h[k][i] - mean) * rstd, g = dy[k][i] * w[i];
-        d[i] = rstd * (g - c1 - xh * c2);
+        for (int i = 0; i < N; ++i) {
+          d[i] = fmaf(mean - h[k][i], c2, fmaf(dy[k][i] * w[i], rstd, -c1));
+        }
+        if (a.dres) {
+          const Vec<T, N> r = load_vec<N, E>((const T*)a.dres + row * a.cols, at, cols);
+#pragma unroll
+          for (int i = 0; i < N; ++i) d[i] += r[i];
+        }
+        store_vec<E, true>((T*)a.dx + row * a.cols, at, cols, make_vec<T>(d));
       }
-      if (a.dres) {
-        const Vec8<T> r = load_vec<E>((const T*)a.dres + row * a.cols, at, cols);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] += r[i];
-      }
-      store_vec<E>((T*)a.dx + row * a.cols, at, cols, make_vec(d, T()));
     }
   }
-  float* out = a.partial + (int64_t)blockIdx.x * 2 * a.cols;
-  if (ROWS > 1) {       // the four wavefronts' sums, added in their order
-    __shared__ float part[ROWS > 1 ? ROWS : 1][2][ROWS > 1 ? TPR * K * 8 : 1];
+  // the rows' sums, added in their order
+  float* out = a.partial + (int64_t)blockIdx.x * a.sums * a.cols;
+  for (int v = 0; v < a.sums; ++v, out += cols) {
+    if (ROWS > 1) {
+      __syncthreads();
 #pragma unroll
-    for (int k = 0; k < K; ++k)
+      for (int k = 0; k < K; ++k)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        part[sub][0][(k * TPR + lane) * 8 + i] = dw[k][i];
-        part[sub][1][(k * TPR + lane) * 8 + i] = db[k][i];
+        for (int i = 0; i < N; ++i)
+          part[(sub * K * TPR + k * TPR + lane) * N + i] = v ? db[k][i] : dw[k][i];
+      __syncthreads();
+      for (uint32_t c = threadIdx.x; c < cols; c += 1024) {
+        float s = part[c];
+#pragma unroll
+        for (int r = 1; r < ROWS; ++r) s += part[r * K * TPR * N + c];
+        out[c] = s;
       }
-    __syncthreads();
-    for (uint32_t c = threadIdx.x; c < cols; c += blockDim.x) {
-      float s = 0.0f, t = 0.0f;
-      for (int r = 0; r < ROWS; ++r) {
-        s += part[r][0][c];
-        t += part[r][1][c];
-      }
-      out[c] = s;
-      out[cols + c] = t;
-    }
-  } else {
+    } else {
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const uint32_t at = (k * TPR + lane) * 8;
-      store_vec<E>(out, at, cols, make_vec(dw[k], 0.0f));
-      store_vec<E>(out + cols, at, cols, make_vec(db[k], 0.0f));
+      for (int k = 0; k < K; ++k)
+        store_vec<E>(out, (k * TPR + lane) * N, cols, make_vec<float>(v ? db[k] : dw[k]));
     }
   }
 }
@@ -330,8 +509,8 @@ __global__ __launch_bounds__(1024) void backward_long_kernel(const Backward a) {
     const float mean = a.mean ? a.mean[row] : 0.0f, rstd = a.rstd[row];
     float s1 = 0.0f, s2 = 0.0f;
     for (int64_t at = threadIdx.x * 8; at < a.cols; at += 8192) {
-      const Vec8<T> d = load_vec<kAny>(dy, at, (int64_t)a.cols), x = load_vec<kAny>(h, at, (int64_t)a.cols);
-      const Vec8<W> w = load_vec<kAny>((const W*)a.weight, at, (int64_t)a.cols);
+      const Vec<T, 8> d = load_vec<8, kAny>(dy, at, (int64_t)a.cols), x = load_vec<8, kAny>(h, at, (int64_t)a.cols);
+      const Vec<W, 8> w = load_vec<8, kAny>((const W*)a.weight, at, (int64_t)a.cols);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float g = d[i] * w[i];
@@ -343,18 +522,18 @@ __global__ __launch_bounds__(1024) void backward_long_kernel(const Backward a) {
     s2 = reduce_group<16>(s2, Sum(), slots[1]);
     const float c1 = a.mean ? s1 * inv : 0.0f, c2 = s2 * inv;
     for (int64_t at = threadIdx.x * 8; at < a.cols; at += 8192) {
-      const Vec8<T> d = load_vec<kAny>(dy, at, (int64_t)a.cols), x = load_vec<kAny>(h, at, (int64_t)a.cols);
-      const Vec8<W> w = load_vec<kAny>((const W*)a.weight, at, (int64_t)a.cols);
+      const Vec<T, 8> d = load_vec<8, kAny>(dy, at, (int64_t)a.cols), x = load_vec<8, kAny>(h, at, (int64_t)a.cols);
+      const Vec<W, 8> w = load_vec<8, kAny>((const W*)a.weight, at, (int64_t)a.cols);
       float v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         v[i] = rstd * (d[i] * w[i] - c1 - (x[i] - mean) * rstd * c2);
       if (a.dres) {
-        const Vec8<T> r = load_vec<kAny>((const T*)a.dres + row * a.cols, at, (int64_t)a.cols);
+        const Vec<T, 8> r = load_vec<8, kAny>((const T*)a.dres + row * a.cols, at, (int64_t)a.cols);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] += r[i];
       }
-      store_vec<kAny>((T*)a.dx + row * a.cols, at, (int64_t)a.cols, make_vec(v, T()));
+      store_vec<kAny>((T*)a.dx + row * a.cols, at, (int64_t)a.cols, make_vec<T>(v));
     }
     __syncthreads();
   }
@@ -369,8 +548,8 @@ __global__ __launch_bounds__(256) void backward_long_columns_kernel(const Backwa
 #pragma unroll
   for (int i = 0; i < 8; ++i) dw[i] = db[i] = 0.0f;
   for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
-    const Vec8<T> d = load_vec<kAny>((const T*)a.dy + row * a.cols, at, (int64_t)a.cols);
-    const Vec8<T> x = load_vec<kAny>((const T*)a.h + row * a.cols, at, (int64_t)a.cols);
+    const Vec<T, 8> d = load_vec<8, kAny>((const T*)a.dy + row * a.cols, at, (int64_t)a.cols);
+    const Vec<T, 8> x = load_vec<8, kAny>((const T*)a.h + row * a.cols, at, (int64_t)a.cols);
     const float mean = a.mean ? a.mean[row] : 0.0f, rstd = a.rstd[row];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -378,9 +557,9 @@ __global__ __launch_bounds__(256) void backward_long_columns_kernel(const Backwa
       db[i] += d[i];
     }
   }
-  float* out = a.partial + (int64_t)blockIdx.y * 2 * a.cols;
-  store_vec<kAny>(out, at, (int64_t)a.cols, make_vec(dw, 0.0f));
-  store_vec<kAny>(out + a.cols, at, (int64_t)a.cols, make_vec(db, 0.0f));
+  float* out = a.partial + (int64_t)blockIdx.y * a.sums * a.cols;
+  store_vec<kAny>(out, at, (int64_t)a.cols, make_vec<float>(dw));
+  if (a.sums == 2) store_vec<kAny>(out + a.cols, at, (int64_t)a.cols, make_vec<float>(db));
 }
 
 // dweight (y == 0) and dbias (y == 1): a lane adds a column, the 16 wavefronts of a workgroup
@@ -396,8 +575,8 @@ __global__ __launch_bounds__(1024) void column_sums_kernel(const float* __restri
   float s = 0.0f;
   if (c < cols) {
     const float* p = partial + (int64_t)blockIdx.y * cols + c;
-#pragma unroll 8
-    for (int g = wave; g < groups; g += 16) s += p[(int64_t)g * 2 * cols];
+#pragma unroll 16
+    for (int g = wave; g < groups; g += 16) s += p[(int64_t)g * gridDim.y * cols];
   }
   part[wave][lane] = s;
   __syncthreads();
@@ -409,68 +588,123 @@ __global__ __launch_bounds__(1024) void column_sums_kernel(const float* __restri
 }
 
 // ----------------------------------------------------------------------------------- host
-constexpr int64_t kForwardGroups = 2048;
+// Workgroups of `threads` that fill the chip once (2048 threads on each of 256 compute units).
+constexpr int64_t resident(int threads) { return (int64_t)256 * 2048 / threads; }
 
-// Rows that a workgroup holds.
-bool held(int64_t cols) { return cols >= 8 && cols <= kMaxHeldCols; }
+// Rows of `esize` bytes an element that a workgroup holds.  (Long binary32 rows whose end cuts a
+// vector would need more than 1024 threads' 128 registers in the backward pass.)
+bool held(int64_t cols, int64_t esize) {
+  return cols >= 8 && cols <= (esize == 4 && cols % 4 ? kMaxHeldCols / 2 : kMaxHeldCols);
+}
 
 template <typename T, typename W, int TPR, int K, End E>
 void forward_held(const Forward& a, hipStream_t s) {
-  constexpr int ROWS = TPR < 256 ? 256 / TPR : 1;
+  constexpr int ROWS = TPR == 64 ? 4 : 1;
   const int64_t groups = (a.rows + ROWS - 1) / ROWS;
-  forward_kernel<T, W, TPR, K, E><<<(unsigned)(groups < kForwardGroups ? groups : kForwardGroups),
-                                    TPR < 256 ? 256 : TPR, 0, s>>>(a);
+  constexpr int threads = TPR == 64 ? 256 : TPR;
+  const int64_t most = resident(threads);
+  forward_kernel<T, W, TPR, K, E><<<(unsigned)(groups < most ? groups : most), threads, 0, s>>>(a);
 }
 template <typename T, typename W, End E>
 void forward(const Forward& a, hipStream_t s) {
-  if (a.cols <= 512) return forward_held<T, W, 64, 1, E>(a, s);
-  if (a.cols <= 1024) return forward_held<T, W, 64, 2, E>(a, s);
-  if (a.cols <= 2048) return forward_held<T, W, 256, 1, E>(a, s);
-  if (a.cols <= 4096) return forward_held<T, W, 256, 2, E>(a, s);
-  if (a.cols <= 8192) return forward_held<T, W, 512, 2, E>(a, s);
-  forward_held<T, W, 1024, 2, E>(a, s);
+  constexpr int k = kUnits<T>;       // of a lane, to hold eight elements
+  if (a.cols <= 512) return forward_held<T, W, 64, k, E>(a, s);
+  if (a.cols <= 1024) return forward_held<T, W, 128, k, E>(a, s);
+  if (a.cols <= 2048) return forward_held<T, W, 256, k, E>(a, s);
+  if (a.cols <= 4096) return forward_held<T, W, 512, k, E>(a, s);
+  if (a.cols <= 8192) return forward_held<T, W, 1024, k, E>(a, s);
+  if constexpr (E == kWhole || sizeof(T) == 2) forward_held<T, W, 512, 4 * k, E>(a, s);
 }
 template <typename T, typename W>
 void forward(const Forward& a, hipStream_t s) {
-  if (!held(a.cols)) {
-    const int64_t groups = a.rows < kForwardGroups ? a.rows : kForwardGroups;
+  if (!held(a.cols, sizeof(T))) {
+    const int64_t groups = a.rows < resident(1024) ? a.rows : resident(1024);
     forward_long_kernel<T, W><<<(unsigned)groups, 1024, 0, s>>>(a);
-  } else if (a.cols % 8) {
+  } else if (a.cols % kVec<T>) {
     forward<T, W, kCut>(a, s);
   } else {
     forward<T, W, kWhole>(a, s);
   }
 }
 
-// Partial rows of the column sums, which is also the grid of the backward pass.
-int backward_groups(int64_t rows, int64_t cols) {
-  const int64_t per = cols <= 1024 ? 4 : 1;
-  const int64_t groups = (rows + per - 1) / per;
-  const int64_t most = cols <= 4096 ? 512 : 256;
-  return (int)(groups < most ? groups : most);
+// Rows that a workgroup of the backward pass takes at a time, and the most workgroups: they fill
+// the chip once, and are also the partial rows of the column sums.
+// Rows of backward_full_kernel (binary32 ones over 8192 would not fit its registers).
+bool backward_full_cols(int64_t cols, int64_t esize) {
+  return cols > 512 && cols <= (esize == 4 ? 8192 : 16384) && cols % (cols <= 8192 ? 512 : 1024) == 0;
 }
 
+
+struct Split {
+  int rows, most;
+};
+Split backward_split(int64_t cols, int64_t esize, bool dres) {
+  if (!held(cols, esize)) return {1, 256};
+  if (backward_full_cols(cols, esize)) {
+    const int threads = (int)(cols <= 8192 ? cols / 8 : cols / 16);
+    // what a compute unit has in flight: 512 threads with 48 or 64 bytes each, 1024 with 32.  More
+    // is no faster and leaves more partial rows (8192 x 4096 bf16: with dres 52.8 us for 512
+    // threads and 57.8 for 1024, without 53.5 and 43.9).
+    const int fill = esize == 4 || dres ? 512 : 1024;
+    return {1, 256 * (fill > threads ? fill / threads : 1)};
+  }
+  if (cols <= 512) return {16, 512};
+  int threads = 128;
+  while (threads < 1024 && threads * 8 < cols) threads *= 2;
+  return {1024 / threads, cols <= 4096 && esize == 2 ? 512 : 256};
+}
+int backward_groups(int64_t rows, int64_t cols, int64_t esize, bool dres) {
+  const Split d = backward_split(cols, esize, dres);
+  const int64_t groups = (rows + d.rows - 1) / d.rows;
+  return (int)(groups < d.most ? groups : d.most);
+}
+
+template <typename T, typename W, int THREADS, int K, End E>
+void backward_wave(const Backward& a, int groups, hipStream_t s) {
+  if (a.cols == 64 * K * kVec<T>) backward_wave_kernel<T, W, THREADS, K, kFull><<<groups, THREADS, 0, s>>>(a);
+  else backward_wave_kernel<T, W, THREADS, K, E><<<groups, THREADS, 0, s>>>(a);
+}
 template <typename T, typename W, int TPR, int K, End E>
-void backward_held(const Backward& a, int groups, hipStream_t s) {
-  backward_kernel<T, W, TPR, K, E><<<groups, TPR < 256 ? 256 : TPR, 0, s>>>(a);
+void backward_rows(const Backward& a, int groups, hipStream_t s) {
+  constexpr int weights = TPR * K * kVec<T> * sizeof(W), sums = 1024 * K * kVec<T> * 4;
+  constexpr int bytes = TPR < 1024 && sums > weights ? sums : weights;
+  auto kernel = backward_kernel<T, W, TPR, K, E>;
+  if (bytes > kPlainLds)
+    (void)hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  kernel<<<groups, 1024, bytes, s>>>(a);
+}
+template <typename T, typename W, int K>
+void backward_full(const Backward& a, int groups, hipStream_t s) {
+  constexpr int most = 1024 * K * kVec<T> * sizeof(W);
+  auto kernel = a.dres ? backward_full_kernel<T, W, K, true> : backward_full_kernel<T, W, K, false>;
+  const int threads = a.cols / (K * kVec<T>), bytes = a.cols * (int)sizeof(W);
+  if (most > kPlainLds && bytes > kPlainLds)
+    (void)hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, most);
+  kernel<<<groups, threads, bytes, s>>>(a);
 }
 template <typename T, typename W, End E>
 void backward(const Backward& a, int groups, hipStream_t s) {
-  if (a.cols <= 512) return backward_held<T, W, 64, 1, E>(a, groups, s);
-  if (a.cols <= 1024) return backward_held<T, W, 64, 2, E>(a, groups, s);
-  if (a.cols <= 2048) return backward_held<T, W, 256, 1, E>(a, groups, s);
-  if (a.cols <= 4096) return backward_held<T, W, 256, 2, E>(a, groups, s);
-  if (a.cols <= 8192) return backward_held<T, W, 512, 2, E>(a, groups, s);
-  backward_held<T, W, 1024, 2, E>(a, groups, s);
+  constexpr int k = kUnits<T>;
+  constexpr bool half = sizeof(T) == 2;
+  if (backward_full_cols(a.cols, sizeof(T))) {
+    if (a.cols <= 8192) return backward_full<T, W, k>(a, groups, s);
+    if constexpr (half) return backward_full<T, W, 2 * k>(a, groups, s);
+  }
+  if (a.cols <= 512) backward_wave<T, W, 1024, k, E>(a, groups, s);
+  else if (a.cols <= 1024) backward_rows<T, W, 128, k, E>(a, groups, s);
+  else if (a.cols <= 2048) backward_rows<T, W, 256, k, E>(a, groups, s);
+  else if (a.cols <= 4096) backward_rows<T, W, 512, k, E>(a, groups, s);
+  else if (a.cols <= 8192) backward_rows<T, W, 1024, k, E>(a, groups, s);
+  else if constexpr (E == kWhole || half) backward_rows<T, W, 1024, 2 * k, E>(a, groups, s);
 }
 template <typename T, typename W>
 void backward(const Backward& a, int groups, void* dweight, void* dbias, hipStream_t s) {
   if (groups == 0) {
-  } else if (!held(a.cols)) {
+  } else if (!held(a.cols, sizeof(T))) {
     const dim3 grid((unsigned)((a.cols + 2047) / 2048), (unsigned)groups);
     backward_long_columns_kernel<T><<<grid, 256, 0, s>>>(a);
     backward_long_kernel<T, W><<<(unsigned)(a.rows < 512 ? a.rows : 512), 1024, 0, s>>>(a);
-  } else if (a.cols % 8) {
+  } else if (a.cols % kVec<T>) {
     backward<T, W, kCut>(a, groups, s);
   } else {
     backward<T, W, kWhole>(a, groups, s);
@@ -561,7 +795,8 @@ NVFP4_EXPORT nvfp4_status nvfp4_layernorm_forward(
 
 NVFP4_EXPORT int64_t nvfp4_layernorm_backward_workspace(int64_t rows, int64_t cols) {
   if (rows <= 0 || cols < 1 || cols > kMaxCols) return 0;
-  return (int64_t)backward_groups(rows, cols) * 2 * cols * 4;
+  const int a = backward_groups(rows, cols, 2, false), b = backward_groups(rows, cols, 4, false);
+  return (int64_t)(a > b ? a : b) * 2 * cols * 4;
 }
 
 NVFP4_EXPORT nvfp4_status nvfp4_layernorm_backward(const void* dy, const void* h,
@@ -592,8 +827,9 @@ NVFP4_EXPORT nvfp4_status nvfp4_layernorm_backward(const void* dy, const void* h
       if (overlap(out[o], out[q])) return NVFP4_ERR_ALIAS;
   }
   (void)hipGetLastError();
-  const Backward a = {dy, h, weight, mean, rstd, dres, dx, (float*)workspace, rows, (int)cols};
-  const int groups = rows ? backward_groups(rows, cols) : 0;
+  const Backward a = {dy, h, weight, mean, rstd, dres, dx, (float*)workspace, rows, (int)cols,
+                      dbias ? 2 : 1};
+  const int groups = rows ? backward_groups(rows, cols, es, dres != nullptr) : 0;
   if (type == NVFP4_T_BF16 && wtype == NVFP4_T_BF16) backward<bf16, bf16>(a, groups, dweight, dbias, stream);
   else if (type == NVFP4_T_BF16) backward<bf16, float>(a, groups, dweight, dbias, stream);
   else if (wtype == NVFP4_T_BF16) backward<float, bf16>(a, groups, dweight, dbias, stream);

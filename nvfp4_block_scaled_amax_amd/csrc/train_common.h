@@ -44,7 +44,7 @@ __device__ __forceinline__ float rounded(float v) {
   return to_f32(from_f32<T>(v));
 }
 
-// -------------------------------------------------------------- vectors of eight elements
+// ----------------------------------------------------------------- vectors of N elements
 // Rows of an odd length, and parts of tensors, start at any element: gfx950 loads and stores
 // 16 bytes at any byte address, so one vector form serves every alignment.
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -52,142 +52,144 @@ typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef u32x2 u32x2_a1 __attribute__((aligned(1)));
 
-template <typename T>
-struct Vec8;
-template <>
-struct Vec8<bf16> {
-  u32x4 w;
+template <typename T, int N>
+struct Vec {
+  static constexpr int kWords = N * (int)sizeof(T) / 4;      // 2, 4 or 8
+  uint32_t w[kWords];
   __device__ __forceinline__ float operator[](int i) const {
-    return __uint_as_float((i & 1) ? (w[i >> 1] & 0xFFFF0000u) : (w[i >> 1] << 16));
-  }
-};
-template <>
-struct Vec8<float> {
-  u32x4 w, w2;
-  __device__ __forceinline__ float operator[](int i) const {
-    return __uint_as_float(i < 4 ? w[i & 3] : w2[i & 3]);
+    return __uint_as_float(sizeof(T) == 4 ? w[i % kWords]
+                           : (i & 1)      ? w[i / 2 % kWords] & 0xFFFF0000u
+                                          : w[i / 2 % kWords] << 16);
   }
 };
 
-__device__ __forceinline__ Vec8<bf16> load_vec(const bf16* p) {
-  return {*reinterpret_cast<const u32x4_a2*>(p)};
-}
-__device__ __forceinline__ Vec8<float> load_vec(const float* p) {
-  const u32x4_a2* q = reinterpret_cast<const u32x4_a2*>(p);
-  return {q[0], q[1]};
-}
-__device__ __forceinline__ Vec8<bf16> make_vec(const float (&v)[8], bf16) {
-  Vec8<bf16> r;
+// STREAM: past the caches, for data that is not likely to be found there when it is wanted next.
+template <int N, bool STREAM = false, typename T>
+__device__ __forceinline__ Vec<T, N> load_vec(const T* p) {
+  constexpr int words = Vec<T, N>::kWords;
+  Vec<T, N> r;
+  if constexpr (words == 2) {
+    typedef u32x2 half __attribute__((aligned(2)));
+    const u32x2 v = *reinterpret_cast<const half*>(p);
+    r.w[0] = v[0], r.w[1] = v[1];
+  } else {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) r.w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-  return r;
-}
-__device__ __forceinline__ Vec8<float> make_vec(const float (&v)[8], float) {
-  Vec8<float> r;
+    for (int k = 0; k < words; k += 4) {
+      const u32x4_a2* q = reinterpret_cast<const u32x4_a2*>(p) + k / 4;
+      const u32x4 v = STREAM ? __builtin_nontemporal_load(q) : *q;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    r.w[i] = __float_as_uint(v[i]);
-    r.w2[i] = __float_as_uint(v[i + 4]);
+      for (int i = 0; i < 4; ++i) r.w[k + i] = v[i];
+    }
   }
   return r;
 }
-__device__ __forceinline__ void store_vec(bf16* p, const Vec8<bf16>& v) {
-  *reinterpret_cast<u32x4_a2*>(p) = v.w;
+template <bool STREAM = false, typename T, int N>
+__device__ __forceinline__ void store_vec(T* p, const Vec<T, N>& r) {
+  static_assert(Vec<T, N>::kWords >= 4, "");
+#pragma unroll
+  for (int k = 0; k < Vec<T, N>::kWords; k += 4) {
+    u32x4_a2* q = reinterpret_cast<u32x4_a2*>(p) + k / 4;
+    const u32x4 v = {r.w[k], r.w[k + 1], r.w[k + 2], r.w[k + 3]};
+    if (STREAM) __builtin_nontemporal_store(v, q);
+    else *q = v;
+  }
 }
-__device__ __forceinline__ void store_vec(float* p, const Vec8<float>& v) {
-  u32x4_a2* q = reinterpret_cast<u32x4_a2*>(p);
-  q[0] = v.w;
-  q[1] = v.w2;
+template <typename T, int N>
+__device__ __forceinline__ Vec<T, N> make_vec(const float (&v)[N]) {
+  Vec<T, N> r;
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) r.w[i] = __float_as_uint(v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) r.w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+  }
+  return r;
 }
-
-// Four binary32 elements, where a lane's 16 bytes are to touch its neighbours'.
-struct Vec4 {
-  u32x4 w;
-  __device__ __forceinline__ float operator[](int i) const { return __uint_as_float(w[i]); }
-};
+template <typename T, int N>
+__device__ __forceinline__ Vec<T, N> zero_vec() {
+  Vec<T, N> r;
+#pragma unroll
+  for (int i = 0; i < Vec<T, N>::kWords; ++i) r.w[i] = 0u;
+  return r;
+}
 
 // Makes the compiler forget how v came about (no instruction): what was computed from it
 // before is computed again rather than kept in registers.
-__device__ __forceinline__ void opaque(Vec8<bf16>& v) { asm("" : "+v"(v.w)); }
-__device__ __forceinline__ void opaque(Vec8<float>& v) { asm("" : "+v"(v.w), "+v"(v.w2)); }
-__device__ __forceinline__ void opaque(Vec4& v) { asm("" : "+v"(v.w)); }
-
-// The same past the caches, for data that no later kernel is likely to find there.
-__device__ __forceinline__ void store_stream(bf16* p, const Vec8<bf16>& v) {
-  __builtin_nontemporal_store(v.w, reinterpret_cast<u32x4_a2*>(p));
-}
-__device__ __forceinline__ void store_stream(float* p, const Vec8<float>& v) {
-  u32x4_a2* q = reinterpret_cast<u32x4_a2*>(p);
-  __builtin_nontemporal_store(v.w, q);
-  __builtin_nontemporal_store(v.w2, q + 1);
-}
-__device__ __forceinline__ Vec8<bf16> load_stream(const bf16* p) {
-  return {__builtin_nontemporal_load(reinterpret_cast<const u32x4_a2*>(p))};
-}
-__device__ __forceinline__ Vec8<float> load_stream(const float* p) {
-  const u32x4_a2* q = reinterpret_cast<const u32x4_a2*>(p);
-  return {__builtin_nontemporal_load(q), __builtin_nontemporal_load(q + 1)};
+template <typename T, int N>
+__device__ __forceinline__ void opaque(Vec<T, N>& v) {
+#pragma unroll
+  for (int i = 0; i < Vec<T, N>::kWords; ++i) asm("" : "+v"(v.w[i]));
 }
 
-template <typename T>
-__device__ __forceinline__ Vec8<T> zero_vec() {
-  const float z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  return make_vec(z, T());
+// The same, and not before `after` is there.
+template <typename T, int N>
+__device__ __forceinline__ void opaque(Vec<T, N>& v, float after) {
+#pragma unroll
+  for (int i = 0; i < Vec<T, N>::kWords; ++i) asm("" : "+v"(v.w[i]) : "v"(after));
+}
+__device__ __forceinline__ void opaque(uint32_t& v, float after) { asm volatile("" : "+v"(v) : "v"(after)); }
+
+// Elements by..N-1 moved to the front, zeros behind them (by in 1..N-1).
+template <typename T, int N>
+__device__ __forceinline__ Vec<T, N> shift(Vec<T, N> v, int by) {
+  constexpr int words = Vec<T, N>::kWords;
+  if (sizeof(T) == 2) {
+    if (by & 1) {
+#pragma unroll
+      for (int i = 0; i < words; ++i)
+        v.w[i] = (v.w[i] >> 16) | (i + 1 < words ? v.w[(i + 1) % words] << 16 : 0u);
+    }
+    by >>= 1;
+  }
+#pragma unroll
+  for (int d = 1; d < words; d *= 2)
+    if (by & d) {
+#pragma unroll
+      for (int i = 0; i < words; ++i) v.w[i] = i + d < words ? v.w[(i + d) % words] : 0u;
+    }
+  return v;
 }
 
-// Elements by..7 moved to the front, zeros behind them (by in 1..7).
-__device__ __forceinline__ Vec8<bf16> shift(Vec8<bf16> v, int by) {
-  u32x4 w = v.w;
-  if (by & 1) w = {(w[0] >> 16) | (w[1] << 16), (w[1] >> 16) | (w[2] << 16),
-                   (w[2] >> 16) | (w[3] << 16), w[3] >> 16};
-  if (by & 2) w = {w[1], w[2], w[3], 0u};
-  if (by & 4) w = {w[2], w[3], 0u, 0u};
-  return {w};
-}
-__device__ __forceinline__ Vec8<float> shift(Vec8<float> v, int by) {
-  u32x4 a = v.w, b = v.w2;
-  if (by & 1) a = {a[1], a[2], a[3], b[0]}, b = {b[1], b[2], b[3], 0u};
-  if (by & 2) a = {a[2], a[3], b[0], b[1]}, b = {b[2], b[3], 0u, 0u};
-  if (by & 4) a = b, b = {0u, 0u, 0u, 0u};
-  return {a, b};
-}
+// How a row's end falls on its vectors: there is none (every vector is in the row); on a
+// boundary; anywhere, in a row of N elements or more; anywhere.
+enum End { kFull, kWhole, kCut, kAny };
 
-// How a row's end falls on its vectors: on a boundary; anywhere, in a row of 8 elements or more;
-// anywhere.
-enum End { kWhole, kCut, kAny };
-
-// Elements [at, at + 8) of a row of n, zeros past its end.  A vector that the end cuts is loaded
-// (kCut) from the last 8 elements and shifted, which takes no further loads and registers.
-template <End E, typename T, typename I>
-__device__ __forceinline__ Vec8<T> load_vec(const T* row, I at, I n) {
-  Vec8<T> r = zero_vec<T>();
+// Elements [at, at + N) of a row of n, zeros past its end.  A vector that the end cuts is loaded
+// (kCut) from the last N elements and shifted, which takes no further loads and registers.
+template <int N, End E, bool STREAM = false, typename T, typename I>
+__device__ __forceinline__ Vec<T, N> load_vec(const T* row, I at, I n) {
+  if (E == kFull) return load_vec<N, STREAM>(row + at);
+  Vec<T, N> r = zero_vec<T, N>();
   if (E == kWhole) {
-    if (at < n) r = load_vec(row + at);
+    if (at < n) r = load_vec<N, STREAM>(row + at);
   } else if (E == kCut) {
     if (at < n) {
-      const I from = at < n - 8 ? at : n - 8;
-      r = load_vec(row + from);
+      const I from = at < n - N ? at : n - N;
+      r = load_vec<N, STREAM>(row + from);
       if (at != from) r = shift(r, (int)(at - from));
     }
-  } else if (at + 8 <= n) {
-    r = load_vec(row + at);
+  } else if (at + N <= n) {
+    r = load_vec<N, STREAM>(row + at);
   } else if (at < n) {
-    float v[8];
+    float v[N];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = at + i < n ? to_f32(row[at + i]) : 0.0f;
-    r = make_vec(v, T());
+    for (int i = 0; i < N; ++i) v[i] = at + i < n ? to_f32(row[at + i]) : 0.0f;
+    r = make_vec<T>(v);
   }
   return r;
 }
-template <End E, typename T, typename I>
-__device__ __forceinline__ void store_vec(T* row, I at, I n, const Vec8<T>& v) {
-  if (E == kWhole) {
-    if (at < n) store_vec(row + at, v);
-  } else if (at + 8 <= n) {
-    store_vec(row + at, v);
+template <End E, bool STREAM = false, typename T, typename I, int N>
+__device__ __forceinline__ void store_vec(T* row, I at, I n, const Vec<T, N>& v) {
+  if (E == kFull) {
+    store_vec<STREAM>(row + at, v);
+  } else if (E == kWhole) {
+    if (at < n) store_vec<STREAM>(row + at, v);
+  } else if (at + N <= n) {
+    store_vec<STREAM>(row + at, v);
   } else if (at < n) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < N; ++i)
       if (at + i < n) row[at + i] = from_f32<T>(v[i]);
   }
 }
@@ -227,6 +229,13 @@ __device__ __forceinline__ float read_lane(float v, int lane) {
 __device__ __forceinline__ uint32_t read_lane(uint32_t v, int lane) {
   return (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
 }
+// A barrier for shared memory alone: __syncthreads would also wait for vector memory in flight.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // Over the wavefront: every lane gets the result.  All 64 lanes must be active.
 template <typename Op, typename V>
 __device__ __forceinline__ V reduce64(V v, Op op) {
@@ -253,9 +262,22 @@ __device__ __forceinline__ V reduce_group(V v, Op op, V* slots) {
   return reduce_few<WAVES>(slots[threadIdx.x % WAVES], op);
 }
 
+// A workgroup's part of a tensor's maximum: on the bits, where inf and NaN sort above the rest.
+// Atomics on one word take turns (2048 of them 15 us or so), so one that cannot raise the word is
+// left out: after the first few that is most of them.  The maximum does not depend on who came first.
+template <int WAVES>
+__device__ __forceinline__ void publish_amax(uint32_t m, uint32_t* amax, uint32_t* slots) {
+  m = reduce_group<WAVES>(m, Max(), slots);
+  if (threadIdx.x == 0 && m > __hip_atomic_load(amax, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT))
+    atomicMax(amax, m);
+}
+
 __global__ void clear_words(uint32_t* p, int64_t n);
 
 // ---------------------------------------------------------------------------------- host
+// Dynamic shared memory that a kernel with a little static one may ask for without being told.
+constexpr int kPlainLds = 65536 - 1024;
+
 inline bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
 struct Range {
