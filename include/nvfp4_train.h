@@ -103,7 +103,8 @@ nvfp4_status nvfp4_distill_loss(const void* student, int64_t student_stride, con
                                 void* workspace, hipStream_t stream);
 
 /* One AdamW step over many tensors, in place.  Per element, in binary32 with one rounding per
- * operation as written (the quotient within 2 ulp):
+ * operation as written (the quotient within 2 ulp; with 8-bit states sqrt(v) within 1 ulp where
+ * 0 < v < 2^-96):
  *   g = grad * grad_scale[0]                  (grad_scale: device float, NULL = no factor)
  *   m = m * beta1 + g * (1 - beta1)
  *   v = v * beta2 + (g * g) * (1 - beta2)
@@ -125,7 +126,7 @@ nvfp4_status nvfp4_distill_loss(const void* student, int64_t student_stride, con
  * type, state kind, and either all or none a master copy.  Different tensors must not overlap
  * (not checked).  numel <= 2^36.
  * out_amax: device float [count] or NULL; max |param| as written, per tensor (0 if empty).
- * betas in [0, 1), eps >= 0, step >= 1.  One launch per 48 tensors, one more with out_amax. */
+ * betas in [0, 1), eps >= 0, step >= 1.  One launch per 58 tensors, one more with out_amax. */
 #define NVFP4_ADAMW_BLOCK 128
 typedef enum { NVFP4_STATE_F32 = 0, NVFP4_STATE_E4M3 = 1 } nvfp4_state;
 typedef struct {

@@ -1,6 +1,6 @@
 // One AdamW step over many tensors for gfx950 (include/nvfp4_train.h defines the update).
 //
-// A launch takes up to 48 tensors, whose table travels as a kernel argument: no copy to the
+// A launch takes up to 58 tensors, whose table travels as a kernel argument: no copy to the
 // device, no state, nothing to go stale.  A workgroup takes one chunk of one tensor; a lane
 // takes eight consecutive elements at a time, so that 16 neighbouring lanes hold one block of
 // an 8-bit state and its maximum is four rotations within a row of lanes.
@@ -14,20 +14,24 @@
 namespace train {
 namespace {
 
-constexpr int kThreads = 256, kSteps = 4;
-constexpr int64_t kChunk = kThreads * 8 * kSteps;      // elements per workgroup
-constexpr int kTable = 48;
+constexpr int kThreads = 256;
+constexpr int64_t kStep = kThreads * 8;                // elements of a workgroup at a time
+constexpr int kSteps = 4;                              // of them in a chunk of a large launch
+constexpr int kTable = 58;                             // tensors: Batch stays below 4 KB
 constexpr float kTiny = 7.8886090522101180541e-31f;    // 2^-100
 
 struct Batch {
   nvfp4_adamw_tensor t[kTable];
   uint32_t first[kTable + 1];         // first chunk of each tensor
   int count, index;                   // tensors, and the index of the first in the call
+  int steps;                          // of kStep elements: a chunk
   float beta1, beta2, rest1, rest2, keep, rate, root, eps;
   uint32_t key;
   const float* grad_scale;
   uint32_t* amax;
 };
+
+static_assert(sizeof(Batch) <= 4096 && kTable <= 64, "kernel arguments; a lane per entry");
 
 // Two rounds of xor-shift and multiply: every input bit reaches every output bit.
 __host__ __device__ __forceinline__ uint32_t hash32(uint32_t h) {
@@ -40,11 +44,22 @@ __host__ __device__ __forceinline__ uint32_t hash32(uint32_t h) {
 
 enum Param { kF32, kMaster, kAlone };       // float; bf16 with a master copy; bf16 alone
 
-// 0 <= y <= 448 (or NaN) -> the E4M3 value above or below it, up as often as the 20 random bits say.
+// y >= 0 (or NaN) -> the value above or below it in E4M3's steps, up as often as the 20 random bits say.
 __device__ __forceinline__ float round_e4m3(float y, uint32_t bits) {
   const float up = y < 0.015625f ? 0.015625f : 0.0f;
   const float cut = __uint_as_float((__float_as_uint(y + up) + bits) & 0xFFF00000u);
-  return fminf(cut - up, 448.0f);
+  return cut - up;
+}
+
+// sqrt(v), rounded to nearest for 0, inf and v >= 2^-96 (below, where a residual underflows, it may be the
+// neighbour): the hardware's root is within one step, and the residual of the value below and
+// above it tells.  (A NaN residual, of 0 and inf, tells nothing and changes nothing.)
+__device__ __forceinline__ float root(float v) {
+  const float s = __builtin_amdgcn_sqrtf(v);
+  const float below = __uint_as_float(__float_as_uint(s) - 1u);
+  const float above = __uint_as_float(__float_as_uint(s) + 1u);
+  const float r = fmaf(-below, s, v) <= 0.0f ? below : s;
+  return fmaf(-above, s, v) > 0.0f ? above : r;
 }
 
 // Eight values over 16 lanes to a block scale and eight E4M3 bytes.
@@ -60,11 +75,14 @@ __device__ __forceinline__ u32x2 encode(const float (&x)[8], const uint32_t (&bi
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float s = x[i] * inv;
-    y[i] = round_e4m3(fabsf(s), POSITIVE ? bits[i] >> 12 : bits[i] & 0xFFFFFu);
+    // at the most 448; and for the root, which is divided by, at the least 2^-9 where it is not 0
+    // (the smallest root of all times 2^120 / 448 is far above 448, so that the median is of
+    // 2^-9 and 448, or of 2^-9 and 0)
     if (POSITIVE)
-      y[i] = x[i] > 0.0f ? fmaxf(y[i], 0.001953125f) : y[i];
+      y[i] = __builtin_amdgcn_fmed3f(round_e4m3(s, bits[i] >> 12), 0.001953125f,
+                                     fminf(s * 0x1p120f, 448.0f));
     else
-      y[i] = copysignf(y[i], s);
+      y[i] = copysignf(fminf(round_e4m3(fabsf(s), bits[i] & 0xFFFFFu), 448.0f), s);
   }
   u32x2 r;
 #pragma unroll
@@ -111,22 +129,21 @@ __device__ __forceinline__ void store_bytes(uint8_t* p, int64_t at, int64_t n, u
 template <Param P, typename G, bool E4M3, bool AMAX>
 __global__ __launch_bounds__(kThreads) void adamw_kernel(const Batch a) {
   __shared__ uint32_t slots[kThreads / 64];
-  // the chunk's tensor: the last one whose first chunk is not after it
-  int lo = 0, hi = a.count - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) / 2;
-    if (a.first[mid] <= blockIdx.x) lo = mid;
-    else hi = mid - 1;
-  }
+  // the chunk's tensor: the last one whose first chunk is not after it (the lanes look at an
+  // entry each)
+  const uint32_t lane = threadIdx.x & 63;
+  const bool before = lane < (uint32_t)a.count && a.first[lane < kTable ? lane : 0] <= blockIdx.x;
+  const int lo = __builtin_amdgcn_readfirstlane(__popcll(__ballot(before)) - 1);
   const nvfp4_adamw_tensor& t = a.t[lo];
-  const int64_t n = t.numel, base = (int64_t)(blockIdx.x - a.first[lo]) * kChunk;
+  const int64_t n = t.numel, base = (int64_t)(blockIdx.x - a.first[lo]) * (a.steps * kStep);
   const float gs = a.grad_scale ? *a.grad_scale : 1.0f;
   uint32_t key = hash32(a.key ^ (uint32_t)(a.index + lo));
   if (base >> 32) key = hash32(key ^ (uint32_t)(base >> 32));    // chunks do not cross 2^32
   uint32_t most = 0;
 #pragma unroll 1
-  for (int step = 0; step < kSteps; ++step) {
+  for (int step = 0; step < a.steps; ++step) {
     const int64_t at = base + (int64_t)(step * kThreads + threadIdx.x) * 8;
+    if (base + step * kStep >= n) break;
     const Vec<G, 8> g8 = load_vec<8, kAny>((const G*)t.grad, at, n);
     float m[8], v[8], p[8];
     if (E4M3) {
@@ -164,8 +181,8 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const Batch a) {
       const float sq = E4M3 ? v[i] * v[i] : v[i];
       m[i] = m[i] * a.beta1 + g * a.rest1;
       v[i] = sq * a.beta2 + (g * g) * a.rest2;
-      low[i] = sqrtf(v[i]);
-      p[i] = p[i] * a.keep - (m[i] / (low[i] * a.root + a.eps)) * a.rate;
+      low[i] = E4M3 ? root(v[i]) : sqrtf(v[i]);
+      p[i] = p[i] * a.keep - (m[i] * __builtin_amdgcn_rcpf(low[i] * a.root + a.eps)) * a.rate;
     }
     if (E4M3) {
       float ms, vs;
@@ -292,11 +309,17 @@ NVFP4_EXPORT nvfp4_status nvfp4_adamw_step(const nvfp4_adamw_tensor* tensors, in
   b.amax = (uint32_t*)out_amax;
   int64_t at = 0;
   while (at < count) {
+    // chunks of one step where there are few elements, for the latency; of more where there are
+    // many, for fewer workgroups
+    int64_t elements = 0;
+    for (int64_t i = at; i < count && i < at + kTable; ++i) elements += tensors[i].numel;
+    b.steps = elements <= kStep * 2048 ? 1 : kSteps;
+    const int64_t chunk = b.steps * kStep;
     int64_t chunks = 0;
     b.count = 0;
     b.index = (int)at;
     for (; at < count && b.count < kTable; ++at) {
-      const int64_t need = (tensors[at].numel + kChunk - 1) / kChunk;
+      const int64_t need = (tensors[at].numel + chunk - 1) / chunk;
       if (b.count && chunks + need > kMaxChunks) break;
       b.first[b.count] = (uint32_t)chunks;
       b.t[b.count++] = tensors[at];

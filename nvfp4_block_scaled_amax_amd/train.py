@@ -18,9 +18,10 @@ from __future__ import annotations
 
 import ctypes
 
+import numpy as np
 import torch
 
-from . import NVFP4Error, _on, _out, _ptr, _stream, lib
+from . import NVFP4Error, lib
 
 TYPES = {torch.bfloat16: 0, torch.float32: 1}
 STATES = {"f32": 0, "e4m3": 1}
@@ -62,39 +63,51 @@ def bind(L: ctypes.CDLL) -> None:
         getattr(L, name).restype = i32
 
 
-def _check(status: int, where: str):
+def _call(name: str, x: torch.Tensor, *args):
+    """The entry point `name` on x's device and its current stream; raises on an error status.
+    (A call of a few microseconds: the device is only switched where it has to be.)"""
+    fn, dev = getattr(lib(), name), x.get_device()
+    if dev == torch.cuda.current_device():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     if status != 0:
-        raise NVFP4Error(status, where, lib().nvfp4_train_status_str(status).decode())
+        raise NVFP4Error(status, name, lib().nvfp4_train_status_str(status).decode())
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _type(t: torch.Tensor, what: str) -> int:
-    if t.dtype not in TYPES:
+    kind = TYPES.get(t.dtype)
+    if kind is None:
         raise TypeError("%s must be bfloat16 or float32, got %s" % (what, t.dtype))
-    return TYPES[t.dtype]
+    return kind
 
 
-def _rows(t: torch.Tensor, what: str):
-    """(rows, cols, row stride) of a tensor seen as rows of its last dimension."""
+def _rows(t: torch.Tensor, shape, what: str) -> int:
+    """The row stride of a tensor seen as rows of its last dimension."""
     if not t.is_cuda:
         raise ValueError("%s must be a GPU tensor" % what)
-    if t.dim() == 0 or t.shape[-1] < 1:
+    if len(shape) == 0 or shape[-1] < 1:
         raise ValueError("%s must have a last dimension of at least 1" % what)
-    cols = t.shape[-1]
     if t.is_contiguous():
-        return t.numel() // cols, cols, cols
-    if t.dim() == 2 and (t.stride(1) == 1 or cols == 1) and t.stride(0) >= cols:
-        return t.shape[0], cols, t.stride(0)
+        return shape[-1]
+    if len(shape) == 2 and (t.stride(1) == 1 or shape[1] == 1) and t.stride(0) >= shape[1]:
+        return t.stride(0)
     raise ValueError("%s must be contiguous, or 2-D with a contiguous last dimension and rows "
                      "that do not overlap" % what)
 
 
 def _like(t: torch.Tensor, shape, dtypes, x: torch.Tensor, what: str):
-    """Checks an input that goes with x: its shape, its type, its device."""
-    if tuple(t.shape) != tuple(shape):
+    """Checks a tensor that goes with x: its shape, its type, its device."""
+    if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (what, tuple(shape), tuple(t.shape)))
     if t.dtype not in dtypes:
         raise TypeError("%s must be %s, got %s" % (what, " or ".join(map(str, dtypes)), t.dtype))
-    if t.device != x.device:
+    if t.get_device() != x.get_device():
         raise ValueError("%s must be on %s" % (what, x.device))
 
 
@@ -102,6 +115,19 @@ def _vector(t: torch.Tensor, shape, dtypes, x: torch.Tensor, what: str):
     _like(t, shape, dtypes, x, what)
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % what)
+
+
+def _out(t, shape, dtype, x: torch.Tensor) -> torch.Tensor:
+    """The caller's output, checked, or a new one.  (empty_like of a contiguous tensor takes a
+    third of empty's time.)"""
+    if t is None:
+        if x.dtype == dtype and x.shape == shape and x.is_contiguous():
+            return torch.empty_like(x)
+        return x.new_empty(shape, dtype=dtype)
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous() or t.device != x.device:
+        raise ValueError("output must be a contiguous %s tensor of shape %s on %s"
+                         % (dtype, tuple(shape), x.device))
+    return t
 
 
 def _work(workspace, nbytes: int, x: torch.Tensor):
@@ -131,30 +157,27 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor = None,
     are float32, one per row, for the backward pass.  amax: float32 [1], receives max |y| for
     fakequant_from_amax / quantize_from_amax.  x and residual may be 2-D with a row stride.
     y may be x (without residual) and h may be x or residual, where they are contiguous."""
-    rows, cols, xs = _rows(x, "x")
-    kind = _type(x, "x")
-    _vector(weight, (cols,), _BOTH, x, "weight")
+    shape, dtype = x.shape, x.dtype
+    xs, kind = _rows(x, shape, "x"), _type(x, "x")
+    lead, cols = shape[:-1], shape[-1]
+    _vector(weight, shape[-1:], _BOTH, x, "weight")
     if bias is not None:
-        _vector(bias, (cols,), (weight.dtype,), x, "bias")
+        _vector(bias, shape[-1:], (weight.dtype,), x, "bias")
     rs = cols
     if residual is not None:
-        _like(residual, x.shape, (x.dtype,), x, "residual")
-        rs = _rows(residual, "residual")[2]
-        h = _out(h, x.shape, x.dtype, x)
+        _like(residual, shape, (dtype,), x, "residual")
+        rs = _rows(residual, shape, "residual")
+        h = _out(h, shape, dtype, x)
     elif h is not None:
         raise ValueError("h is an output of the residual form only")
-    lead = tuple(x.shape[:-1])
-    y = _out(y, x.shape, x.dtype, x)
+    y = _out(y, shape, dtype, x)
     rstd = _out(rstd, lead, torch.float32, x)
-    mean = _out(mean, lead, torch.float32, x) if center else None
+    mean = _out(mean, lead, torch.float32, rstd) if center else None
     if amax is not None:
         _vector(amax, (1,), _F32, x, "amax")
-    with _on(x):
-        st = lib().nvfp4_layernorm_forward(
-            _ptr(x), xs, _ptr(residual), rs, _ptr(weight), _ptr(bias), rows, cols, kind,
-            TYPES[weight.dtype], int(center), eps, _ptr(y), _ptr(h), _ptr(mean), _ptr(rstd),
-            _ptr(amax), _stream(x))
-    _check(st, "nvfp4_layernorm_forward")
+    _call("nvfp4_layernorm_forward", x, x.data_ptr(), xs, _ptr(residual), rs, weight.data_ptr(),
+          _ptr(bias), rstd.numel(), cols, kind, TYPES[weight.dtype], int(center), eps, y.data_ptr(),
+          _ptr(h), _ptr(mean), rstd.data_ptr(), _ptr(amax))
     return y, x if residual is None else h, mean, rstd
 
 
@@ -166,26 +189,27 @@ def layer_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor,
     h, mean and rstd as layer_norm returned them (mean None for center=False).  dres: gradient
     that reaches h past the norm, added to dx.  dx is the gradient of x and of residual alike, and may
     be written over dy or dres.  bias=False leaves dbias out (None)."""
-    rows, cols, _ = _rows(dy, "dy")
+    shape, dtype = dy.shape, dy.dtype
+    _rows(dy, shape, "dy")
     kind = _type(dy, "dy")
-    for t, what in ((dy, "dy"), (h, "h"), (dres, "dres")):
-        if t is not None:
-            _vector(t, dy.shape, (dy.dtype,), dy, what)
-    _vector(weight, (cols,), _BOTH, dy, "weight")
-    lead = tuple(dy.shape[:-1])
+    lead, cols = shape[:-1], shape[-1]
+    if not dy.is_contiguous():
+        raise ValueError("dy must be contiguous")
+    _vector(h, shape, (dtype,), dy, "h")
+    if dres is not None:
+        _vector(dres, shape, (dtype,), dy, "dres")
+    _vector(weight, shape[-1:], _BOTH, dy, "weight")
     _vector(rstd, lead, _F32, dy, "rstd")
     if mean is not None:
         _vector(mean, lead, _F32, dy, "mean")
-    dx = _out(dx, dy.shape, dy.dtype, dy)
-    dweight = _out(dweight, (cols,), weight.dtype, dy)
-    dbias = _out(dbias, (cols,), weight.dtype, dy) if bias else None
-    L = lib()
-    ws = _work(workspace, L.nvfp4_layernorm_backward_workspace(rows, cols), dy)
-    with _on(dy):
-        st = L.nvfp4_layernorm_backward(
-            _ptr(dy), _ptr(h), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dres), rows, cols, kind,
-            TYPES[weight.dtype], _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(ws), _stream(dy))
-    _check(st, "nvfp4_layernorm_backward")
+    rows, wtype = rstd.numel(), weight.dtype
+    dx = _out(dx, shape, dtype, dy)
+    dweight = _out(dweight, shape[-1:], wtype, weight)
+    dbias = _out(dbias, shape[-1:], wtype, weight) if bias else None
+    ws = _work(workspace, lib().nvfp4_layernorm_backward_workspace(rows, cols), dy)
+    _call("nvfp4_layernorm_backward", dy, dy.data_ptr(), h.data_ptr(), weight.data_ptr(), _ptr(mean),
+          rstd.data_ptr(), _ptr(dres), rows, cols, kind, TYPES[wtype], dx.data_ptr(),
+          dweight.data_ptr(), _ptr(dbias), ws.data_ptr())
     return dx, dweight, dbias
 
 
@@ -197,29 +221,28 @@ def distill_loss(student: torch.Tensor, teacher: torch.Tensor, weight: torch.Ten
 
     Logits are [..., vocab]; 2-D ones may have a row stride.  weight: float32 [...]; rows of
     weight 0 are not read.  grad may be the student itself (written in place)."""
-    rows, vocab, ss = _rows(student, "student")
-    kinds = _type(student, "student"), _type(teacher, "teacher")
-    _like(teacher, student.shape, _BOTH, student, "teacher")
-    ts = _rows(teacher, "teacher")[2]
-    lead = tuple(student.shape[:-1])
+    shape = student.shape
+    ss, kind = _rows(student, shape, "student"), _type(student, "student")
+    lead, vocab = shape[:-1], shape[-1]
+    _like(teacher, shape, _BOTH, student, "teacher")
+    ts = _rows(teacher, shape, "teacher")
     if weight is not None:
         _vector(weight, lead, _F32, student, "weight")
-    loss = _out(loss, lead, torch.float32, student)
+    loss = _out(loss, lead, torch.float32, student if weight is None else weight)
     gs = vocab
     if grad is not None:
         if not want_grad:
             raise ValueError("grad is an output of the form with a gradient only")
-        _like(grad, student.shape, (student.dtype,), student, "grad")
-        gs = _rows(grad, "grad")[2]
+        _like(grad, shape, (student.dtype,), student, "grad")
+        gs = _rows(grad, shape, "grad")
     elif want_grad:
-        grad = torch.empty(student.shape, dtype=student.dtype, device=student.device)
-    L = lib()
-    ws = _work(workspace, L.nvfp4_distill_loss_workspace(rows, vocab), student)
-    with _on(student):
-        st = L.nvfp4_distill_loss(
-            _ptr(student), ss, _ptr(teacher), ts, _ptr(weight), rows, vocab, kinds[0], kinds[1],
-            temperature, _ptr(loss), _ptr(grad), gs, _ptr(ws), _stream(student))
-    _check(st, "nvfp4_distill_loss")
+        grad = _out(None, shape, student.dtype, student)
+    rows = loss.numel()
+    need = lib().nvfp4_distill_loss_workspace(rows, vocab)
+    ws = _work(workspace, need, student) if need else None
+    _call("nvfp4_distill_loss", student, student.data_ptr(), ss, teacher.data_ptr(), ts, _ptr(weight),
+          rows, vocab, kind, TYPES[teacher.dtype], temperature, loss.data_ptr(), _ptr(grad), gs,
+          _ptr(ws))
     return loss, grad
 
 
@@ -262,9 +285,11 @@ class AdamWPlan:
                 raise ValueError("%s: %d tensors for %d parameters" % (kind, len(tensors), len(params)))
             for t, n in zip(tensors, sizes):
                 self._look(kind, t, n, dtype)
-        self._table = (AdamWTensor * len(params))()
-        for row, n in zip(self._table, self.numels):
-            row.numel = n
+        # nvfp4_adamw_tensor, an entry a row
+        self._table = np.zeros((len(params), 8), np.int64)
+        self._table[:, 7] = self.numels
+        self._columns = [(0, params), (2, exp_avg), (3, exp_avg_sq)]
+        self._columns += [(k, v) for k, v in ((4, master), (5, avg_scale), (6, sq_scale)) if v is not None]
 
     def _look(self, kind, t, numel, dtype):
         if t.dtype != dtype:
@@ -275,15 +300,12 @@ class AdamWPlan:
             raise ValueError("%s must be contiguous, with %d elements, got %s"
                              % (kind, numel, tuple(t.shape)))
 
-    def table(self, grads):
+    def table(self, grads) -> np.ndarray:
         """The entries of nvfp4_adamw_tensor for these gradients."""
         rows = self._table
-        for name, tensors in (("param", self.params), ("grad", grads), ("exp_avg", self.exp_avg),
-                              ("exp_avg_sq", self.exp_avg_sq), ("master", self.master),
-                              ("avg_scale", self.avg_scale), ("sq_scale", self.sq_scale)):
-            if tensors is not None:
-                for row, t in zip(rows, tensors):
-                    setattr(row, name, t.data_ptr())
+        for k, tensors in self._columns:
+            rows[:, k] = [t.data_ptr() for t in tensors]
+        rows[:, 1] = [g.data_ptr() for g in grads]
         return rows
 
 
@@ -336,8 +358,10 @@ def adamw_step(plan: AdamWPlan, grads, *, step: int, lr: float, betas=(0.9, 0.99
         raise ValueError("%d gradients for %d parameters" % (len(grads), len(plan.params)))
     gtype = grads[0].dtype
     kind = _type(grads[0], "gradients")
+    dev = plan.device.index
     for g, n in zip(grads, plan.numels):
-        plan._look("grads", g, n, gtype)
+        if g.dtype != gtype or g.get_device() != dev or g.numel() != n or not g.is_contiguous():
+            plan._look("grads", g, n, gtype)          # says which
     like = plan.params[0]
     if grad_scale is not None:
         _vector(grad_scale, (1,), _F32, like, "grad_scale")
@@ -346,8 +370,5 @@ def adamw_step(plan: AdamWPlan, grads, *, step: int, lr: float, betas=(0.9, 0.99
     if not 0 <= seed < 1 << 32:
         raise ValueError("seed must be in 0 .. 2^32 - 1")
     args = AdamWArgs(lr, betas[0], betas[1], eps, weight_decay, step, seed)
-    with _on(like):
-        st = lib().nvfp4_adamw_step(plan.table(grads), len(grads), plan.ptype, kind, plan.state,
-                                    ctypes.byref(args), _ptr(grad_scale), _ptr(amax),
-                                    _stream(like))
-    _check(st, "nvfp4_adamw_step")
+    _call("nvfp4_adamw_step", like, plan.table(grads).ctypes.data, len(grads), plan.ptype, kind,
+          plan.state, ctypes.byref(args), _ptr(grad_scale), _ptr(amax))
