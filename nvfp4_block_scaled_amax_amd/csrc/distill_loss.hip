@@ -247,11 +247,13 @@ __device__ __forceinline__ float row_grad(R& row, void* lds, S* grad, float c, f
   const float part = r - q.r, off = (q.r - (r - part)) + (by - part);
   const float scale = weight / (temperature * p.z);
   const float back = 1.0f - off * kLn2;       // 2^-off
-  float flat = 0.0f, bent = 0.0f;    // sums of (q - p) weight / T and of p Zp (log2 p - log2 q)
+  // Zp sum of (q - p) + ln 2 p (X - Y): both parts of a unit meet before they are added to the
+  // others, because their sums over the row are far larger than the loss
+  float sum = 0.0f;
   row.again(
       lds,
       [&](uint32_t at, const auto& a, const auto& b) {
-        float x[N], y[N], g[N], least = INFINITY;
+        float x[N], y[N], g[N], least = INFINITY, flat = 0.0f, bent = 0.0f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           y[i] = fmaf(a[i], c, -r);
@@ -261,34 +263,33 @@ __device__ __forceinline__ float row_grad(R& row, void* lds, S* grad, float c, f
         if (least == -INFINITY) {     // log2 p - log2 q counts where p is not 0
 #pragma unroll
           for (int i = 0; i < N; ++i) {
-            const float eq = exp2_(y[i]), ep = exp2_(x[i]);
+            const float eq = exp2_(y[i]), ep = exp2_(x[i]), d = fmaf(eq, back, -ep);
             bent += ep == 0.0f ? 0.0f : ep * (x[i] - y[i]);
-            g[i] = fmaf(eq, back, -ep) * scale;
-            flat += g[i];
+            flat += d;
+            g[i] = d * scale;
           }
         } else {
 #pragma unroll
           for (int i = 0; i < N; ++i) {
-            const float eq = exp2_(y[i]), ep = exp2_(x[i]);
+            const float eq = exp2_(y[i]), ep = exp2_(x[i]), d = fmaf(eq, back, -ep);
             bent = fmaf(ep, x[i] - y[i], bent);
-            g[i] = fmaf(eq, back, -ep) * scale;
-            flat += g[i];
+            flat += d;
+            g[i] = d * scale;
           }
         }
+        sum += fmaf(kLn2, bent, flat);
         if (grad) store_vec<true>(grad + at, make_vec<S>(g));
       },
       [&](uint32_t at, float a, float b) {
         const float y = fmaf(a, c, -r), x = fmaf(b, c, -p.r);
-        const float eq = exp2_(y), ep = exp2_(x);
-        bent += ep == 0.0f ? 0.0f : ep * (x - y);
-        const float g = fmaf(eq, back, -ep) * scale;
-        flat += g;
-        if (grad) grad[at] = from_f32<S>(g);
+        const float eq = exp2_(y), ep = exp2_(x), d = fmaf(eq, back, -ep);
+        sum += fmaf(kLn2, ep == 0.0f ? 0.0f : ep * (x - y), d);
+        if (grad) grad[at] = from_f32<S>(d * scale);
       });
-  // log2 p - log2 q = X - Y + off, and the p add up to 1
-  const float mine = flat * temperature + weight * kLn2 * (bent / p.z);
-  const float all = reduce_group<THREADS / 64>(mine, Sum(), slots);
-  return row.lo == 0 ? all + weight * kLn2 * off : all;
+  // What is missing: log2 p - log2 q is X - Y + off, and `back` is rounded.  The p and the q add up
+  // to 1 each, so that is ln 2 off + (2^-off - back) = 1 - back.
+  const float all = reduce_group<THREADS / 64>(weight * (sum / p.z), Sum(), slots);
+  return row.lo == 0 ? fmaf(weight, 1.0f - back, all) : all;
 }
 
 // The same from the sums with exact differences.

@@ -135,7 +135,7 @@ def _work(workspace, nbytes: int, x: torch.Tensor):
     if nbytes < 0:
         raise ValueError("bad shape")
     if workspace is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+        return x.new_empty(nbytes, dtype=torch.uint8)
     if (workspace.device != x.device or not workspace.is_contiguous()
             or workspace.numel() * workspace.element_size() < nbytes):
         raise ValueError("workspace must be a contiguous tensor of at least %d bytes on %s"
