@@ -6,6 +6,8 @@
 // the three steps.  The backward pass keeps, next to the row, its share of the column sums
 // (dweight, dbias) in registers over all the rows that a workgroup takes, leaves them as one
 // partial row per workgroup in the workspace, and a second launch adds those in a fixed order.
+#include <type_traits>
+
 #include "train_common.h"
 
 namespace train {
@@ -47,17 +49,29 @@ constexpr int kVec = 16 / sizeof(T);
 template <typename T>
 constexpr int kUnits = 8 / kVec<T>;
 
-// The columns of a held row: known to be in 8 .. MOST, so that offsets take 32 bits.
-template <int MOST>
-__device__ __forceinline__ uint32_t held_cols(int cols) {
-  __builtin_assume(cols >= 8 && cols <= MOST);
-  return (uint32_t)cols;
-}
-// Which row of the workgroup's this thread is at, as a scalar.
-template <int TPR>
-__device__ __forceinline__ uint32_t wave_of() {
-  return TPR == 64 ? __builtin_amdgcn_readfirstlane(threadIdx.x / TPR) : 0u;
-}
+// A lane's vector of a row of `cols` elements that is held: where it is, and where it is loaded
+// from.  No load depends on a condition (the compiler can then count the loads in flight, and wait
+// for the first of them alone): a vector past the row's end, or cut by it, is loaded from the last
+// N elements, and settled when it is used.
+template <int N, End E>
+struct Place {
+  uint32_t at, from;
+  __device__ __forceinline__ Place(uint32_t at_, uint32_t cols)
+      : at(at_), from(E == kFull || at_ < cols - N ? at_ : cols - N) {}
+  template <typename T>
+  __device__ __forceinline__ Vec<T, N> load(const T* row) const {
+    return load_vec<N>(row + from);
+  }
+  // zeros past the row's end (kCut; with kWhole a vector is in the row or not: see in())
+  template <typename T>
+  __device__ __forceinline__ void settle(Vec<T, N>& v) const {
+    if (E == kCut && at != from) v = at - from < N ? shift(v, (int)(at - from)) : zero_vec<T, N>();
+  }
+  __device__ __forceinline__ bool in(uint32_t cols) const { return E == kFull || at < cols; }
+  __device__ __forceinline__ bool in(uint32_t cols, int i) const {
+    return E == kFull || (E == kWhole ? at < cols : at + i < cols);
+  }
+};
 
 // A value that the whole wavefront wants from memory that no kernel in flight writes, through the
 // scalar cache.
@@ -67,86 +81,120 @@ __device__ __forceinline__ float scalar_load(const float* p) {
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
-// One row: TPR lanes hold K vectors each.  With TPR == 64 a workgroup takes 4 rows at a time.
-template <typename T, typename W, int TPR, int K, End E>
-__global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void forward_kernel(const Forward a) {
-  constexpr int N = kVec<T>, WAVES = TPR / 64, ROWS = TPR == 64 ? 4 : 1;
-  __shared__ float slots[2][WAVES];
-  __shared__ uint32_t top[TPR == 64 ? 4 : WAVES];
-  const uint32_t lane = threadIdx.x % TPR, cols = held_cols<TPR * K * N>(a.cols);
+// Rows of up to 512 columns take a wavefront each (WAVE), longer ones a workgroup; a lane holds K
+// vectors, and where that is eight elements (HOLD) also its weights for all the rows that it comes
+// by (8192 x 4097 bf16 83 us, 100 if they are read for each; 8192 x 4096 f32 47.5 and 51.2).  Rows of
+// bf16 that fill the workgroup, without a residual, are an exception that only the measurement
+// explains: 26.9 us for 8192 x 4096 with the weights held, 22.8 without.
+template <typename T, typename W, int THREADS, int K, End E, bool WAVE, bool HOLD>
+__global__ __launch_bounds__(THREADS) void forward_kernel(const Forward a) {
+  constexpr int N = kVec<T>;
+  __shared__ float slots[2][2][16];
+  __shared__ uint32_t top[16];
+  const uint32_t waves = blockDim.x / 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const uint32_t lane = WAVE ? threadIdx.x % 64 : threadIdx.x, lanes = WAVE ? 64 : blockDim.x;
+  const uint32_t cols = a.cols;
   const float inv = 1.0f / (float)a.cols;
+  auto vector = [&](const void* v, int k) {
+    const Place<N, E> at((k * lanes + lane) * N, cols);
+    Vec<W, N> r = v ? at.load((const W*)v) : zero_vec<W, N>();
+    at.settle(r);
+    return r;
+  };
+  Vec<W, N> weight[HOLD ? K : 1], bias[HOLD ? K : 1];
+#pragma unroll
+  for (int k = 0; k < (HOLD ? K : 0); ++k) weight[k] = vector(a.weight, k), bias[k] = vector(a.bias, k);
+  if (!WAVE) {
+    if (threadIdx.x < 64) ((float*)slots)[threadIdx.x] = 0.0f;      // those of wavefronts not there
+    if (threadIdx.x < 16) top[threadIdx.x] = 0u;
+    __syncthreads();
+  }
+  // over the row; the slots of two rows in turn
+  auto total = [&](float v, float* part) {
+    v = reduce64(v, Sum());
+    if (WAVE) return v;
+    if ((threadIdx.x & 63) == 0) part[wave] = v;
+    lds_barrier();
+    return reduce16(part[threadIdx.x % 16], Sum());
+  };
   uint32_t most = 0;
-  for (int64_t row = (int64_t)blockIdx.x * ROWS + wave_of<TPR>(); row < a.rows;
-       row += (int64_t)gridDim.x * ROWS) {
+  int turn = 0;
+  const int64_t step = (int64_t)gridDim.x * (WAVE ? waves : 1);
+  for (int64_t row = (int64_t)blockIdx.x * (WAVE ? waves : 1) + (WAVE ? wave : 0); row < a.rows;
+       row += step, turn ^= 1) {
     const T* x = (const T*)a.x + row * a.x_stride;
+    Vec<T, N> q[K];
     float v[K][N];
-    float sum = 0.0f;
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const Vec<T, N> q = load_vec<N, E>(x, (k * TPR + lane) * N, cols);
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[k][i] = q[i];
-    }
+    for (int k = 0; k < K; ++k) q[k] = Place<N, E>((k * lanes + lane) * N, cols).load(x);
     if (a.residual) {
       const T* r = (const T*)a.residual + row * a.residual_stride;
-      T* h = (T*)a.h + row * a.cols;
+      T* h = (T*)a.h + row * cols;
+      Vec<T, N> p[K];
+#pragma unroll
+      for (int k = 0; k < K; ++k) p[k] = Place<N, E>((k * lanes + lane) * N, cols).load(r);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        const uint32_t at = (k * TPR + lane) * N;
-        const Vec<T, N> q = load_vec<N, E>(r, at, cols);
+        const Place<N, E> at((k * lanes + lane) * N, cols);
+        at.settle(q[k]);
+        at.settle(p[k]);
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[k][i] += q[i];
-        const Vec<T, N> s = make_vec<T>(v[k]);
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[k][i] = s[i];
-        store_vec<E, true>(h, at, cols, s);
+        for (int i = 0; i < N; ++i) v[k][i] = q[k][i] + p[k][i];
+        q[k] = make_vec<T>(v[k]);
+        store_vec<E, true>(h, at.at, cols, q[k]);
       }
+    } else {
+#pragma unroll
+      for (int k = 0; k < K; ++k) Place<N, E>((k * lanes + lane) * N, cols).settle(q[k]);
     }
-    float mean = 0.0f;
-    if (a.center) {
+    float mean = 0.0f, sum = 0.0f, sq = 0.0f;
 #pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int i = 0; i < N; ++i) sum += v[k][i];
-      mean = reduce_group<WAVES>(sum, Sum(), slots[0]) * inv;
-    }
-    float sq = 0.0f;
-#pragma unroll
-    for (int k = 0; k < K; ++k)
+    for (int k = 0; k < K; ++k) {
+      const Place<N, E> at((k * lanes + lane) * N, cols);
+      float part = 0.0f;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const float d = (k * TPR + lane) * N + i < cols ? v[k][i] - mean : 0.0f;
-        sq += d * d;
+        v[k][i] = q[k][i];
+        part += v[k][i];
       }
-    const float var = reduce_group<WAVES>(sq, Sum(), slots[1]) * inv;
-    const float rstd = 1.0f / sqrtf(var + a.eps);
+      sum += at.in(cols) ? part : 0.0f;
+    }
+    if (a.center) mean = total(sum, slots[turn][0]) * inv;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const Place<N, E> at((k * lanes + lane) * N, cols);
+      float part = 0.0f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        v[k][i] -= mean;
+        const float d = E != kCut || at.in(cols, i) ? v[k][i] : 0.0f;
+        part = fmaf(d, d, part);
+      }
+      sq += at.in(cols) ? part : 0.0f;
+    }
+    const float rstd = 1.0f / sqrtf(total(sq, slots[turn][1]) * inv + a.eps);
     if (lane == 0) {
       a.rstd[row] = rstd;
       if (a.center) a.mean[row] = mean;
     }
-    T* y = (T*)a.y + row * a.cols;
+    T* y = (T*)a.y + row * cols;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const uint32_t at = (k * TPR + lane) * N;
-      const Vec<W, N> w = load_vec<N, E>((const W*)a.weight, at, cols);
+      const Place<N, E> at((k * lanes + lane) * N, cols);
+      const Vec<W, N> w = HOLD ? weight[HOLD ? k : 0] : vector(a.weight, k);
+      const Vec<W, N> b = HOLD ? bias[HOLD ? k : 0] : vector(a.bias, k);
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[k][i] = (v[k][i] - mean) * rstd * w[i];
-      if (a.bias) {
-        const Vec<W, N> b = load_vec<N, E>((const W*)a.bias, at, cols);
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[k][i] += b[i];
-      }
+      for (int i = 0; i < N; ++i) v[k][i] = fmaf(v[k][i] * rstd, w[i], b[i]);
       const Vec<T, N> out = make_vec<T>(v[k]);
-      store_vec<E, true>(y, at, cols, out);
+      store_vec<E, true>(y, at.at, cols, out);
       if (a.amax) {
 #pragma unroll
         for (int i = 0; i < N; ++i)
-          if (at + i < cols) most = max(most, abs_bits(out[i]));
+          if (at.in(cols, i)) most = max(most, abs_bits(out[i]));
       }
     }
-    if (WAVES > 1) __syncthreads();     // the slots are free for the next row
   }
-  if (a.amax) publish_amax<(TPR == 64 ? 4 : WAVES)>(most, a.amax, top);
+  if (a.amax) publish_amax<WAVE ? THREADS / 64 : 16>(most, a.amax, top);
 }
 
 // Rows longer than the registers hold (and those under 8 columns): three passes over the row.
@@ -220,7 +268,7 @@ template <typename T, typename W, int THREADS, int K, End E>
 __global__ __launch_bounds__(THREADS) void backward_wave_kernel(const Backward a) {
   constexpr int N = kVec<T>, WAVES = THREADS / 64;
   __shared__ float part[WAVES][64 * N];
-  const uint32_t lane = threadIdx.x % 64, cols = held_cols<64 * K * N>(a.cols);
+  const uint32_t lane = threadIdx.x % 64, cols = a.cols;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const float inv = 1.0f / (float)a.cols;
   float dw[K][N], db[K][N];
@@ -295,52 +343,69 @@ __global__ __launch_bounds__(THREADS) void backward_wave_kernel(const Backward a
   }
 }
 
-// Rows of a multiple of 512 columns: a workgroup of cols / (K * N) threads takes one row at a time
-// and loads the next one meanwhile.  Nothing may stand between those loads and their use a row
-// later that waits for vector memory in order: the weights lie in shared memory, the
-// statistics come through the scalar cache, and no load or store depends on a condition, so that
-// the compiler can count them.
-template <typename T, typename W, int K, bool RES>
-__global__ __launch_bounds__(1024) void backward_full_kernel(const Backward a) {
+// Longer rows: a workgroup takes one at a time, K vectors a lane, and loads the next one meanwhile
+// (AHEAD).  Nothing may stand between those loads and their use a row later that waits for vector
+// memory in order, or that the compiler cannot count: the weights lie in shared memory, the
+// statistics come through the scalar cache, and no load or store depends on a condition.  Where the
+// row does not fill the workgroup (not FULL), a vector past the row's end, or cut by it, is the last
+// N elements instead.  Its lane then computes and writes what its neighbours do, the same
+// bits, and its weights are zero in the row's sums for the elements that are not its own.
+template <typename T, typename W, int K, bool FULL, bool RES>
+__global__ __launch_bounds__(1024) void backward_kernel(const Backward a) {
   constexpr int N = kVec<T>;
+  constexpr bool AHEAD = K * N == 8 || sizeof(T) == 2;      // there are registers for two rows
   __shared__ float slots[2][2][16];
   extern __shared__ __align__(16) char dynamic[];
   Vec<W, N>* const weight = (Vec<W, N>*)dynamic + threadIdx.x;       // [K][threads], by vectors
-  const uint32_t threads = blockDim.x, at = threadIdx.x * N;
-  const int64_t cols = (int64_t)threads * (K * N);
+  const uint32_t threads = blockDim.x, cols = a.cols;
   const float inv = 1.0f / (float)a.cols;
+  auto own = [&](int k) { return (k * threads + threadIdx.x) * N; };        // the vector's place
+  auto from = [&](int k) { return FULL || own(k) < cols - N ? own(k) : cols - N; };
   float dw[K][N], db[K][N];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    weight[k * threads] = load_vec<N>((const W*)a.weight + k * threads * N + at);
+    weight[k * threads] = load_vec<N>((const W*)a.weight + from(k));
 #pragma unroll
     for (int i = 0; i < N; ++i) dw[k][i] = db[k][i] = 0.0f;
   }
   if (threadIdx.x < 64) ((float*)slots)[threadIdx.x] = 0.0f;         // those of wavefronts not there
   __syncthreads();
-  const int64_t step = gridDim.x;
-  const int64_t last = a.rows - 1;
+  const int64_t step = gridDim.x, last = a.rows - 1;
   Vec<T, N> dy[K], h[K], dy2[K], h2[K], res[K];
   auto load = [&](const void* base, int64_t row, Vec<T, N> (&v)[K]) {
-    const T* p = (const T*)base + row * cols;
 #pragma unroll
-    for (int k = 0; k < K; ++k) v[k] = load_vec<N>(p + (k * threads * N + at));
+    for (int k = 0; k < K; ++k) v[k] = load_vec<N>((const T*)base + row * cols + from(k));
   };
-  load(a.dy, blockIdx.x, dy2);
-  load(a.h, blockIdx.x, h2);
+  if (AHEAD) {
+    load(a.dy, blockIdx.x, dy2);
+    load(a.h, blockIdx.x, h2);
+  }
   int turn = 0;
   for (int64_t row = blockIdx.x; row <= last; row += step, turn ^= 1) {
+    if (AHEAD) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) dy[k] = dy2[k], h[k] = h2[k];
-    if (RES) load(a.dres, row, res);
-    const int64_t ahead = row + step <= last ? row + step : last;     // one too many at the end
-    load(a.dy, ahead, dy2);
-    load(a.h, ahead, h2);
+      for (int k = 0; k < K; ++k) dy[k] = dy2[k], h[k] = h2[k];
+    } else {
+      load(a.dy, row, dy);
+      load(a.h, row, h);
+    }
+    if (RES && AHEAD) load(a.dres, row, res);
+    if (AHEAD) {
+      const int64_t next = row + step <= last ? row + step : last;   // one too many at the end
+      load(a.dy, next, dy2);
+      load(a.h, next, h2);
+    }
     const float mean = a.mean ? scalar_load(a.mean + row) : 0.0f, rstd = scalar_load(a.rstd + row);
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const Vec<W, N> w = weight[k * threads];
+      Vec<W, N> w = weight[k * threads];
+      if (!FULL && own(k) != from(k)) {        // zero before its own elements
+        float f[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) f[i] = i < (int)(own(k) - from(k)) ? 0.0f : w[i];
+        w = make_vec<W>(f);
+      }
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const float xh = (h[k][i] - mean) * rstd, d = dy[k][i], g = d * w[i];
@@ -350,6 +415,12 @@ __global__ __launch_bounds__(1024) void backward_full_kernel(const Backward a) {
         db[k][i] += d;
         asm volatile("" : "+v"(s1), "+v"(s2), "+v"(dw[k][i]), "+v"(db[k][i]));   // here, not later
       }
+    }
+    // dres is here before anyone writes, who may write over it and into another lane's vector
+    if (RES && !FULL) {
+      static_assert(AHEAD || FULL, "");
+#pragma unroll
+      for (int k = 0; k < K; ++k) opaque(res[k], s2);
     }
     // the slots of two rows in turn: one barrier per row is enough
     s1 = reduce64(s1, Sum());
@@ -370,132 +441,29 @@ __global__ __launch_bounds__(1024) void backward_full_kernel(const Backward a) {
       opaque(dy[k], c2);      // unpacked again from here: the floats need not live across the sums
       opaque(h[k], c2);
       const Vec<W, N> w = weight[k * threads];
+      if (RES && !AHEAD) res[k] = load_vec<N>((const T*)a.dres + row * cols + from(k));
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         d[i] = fmaf(mean - h[k][i], c2, fmaf(dy[k][i] * w[i], rstd, -c1));
         if (RES) d[i] += res[k][i];
       }
-      store_vec<true>(dx + (k * threads * N + at), make_vec<T>(d));
+      store_vec<true>(dx + from(k), make_vec<T>(d));
     }
   }
   float* out = a.partial + (int64_t)blockIdx.x * a.sums * cols;
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    store_vec(out + (k * threads * N + at), make_vec<float>(dw[k]));
-    if (a.sums == 2) store_vec(out + cols + (k * threads * N + at), make_vec<float>(db[k]));
-  }
-}
-
-// Other rows: workgroups of 1024 threads take 1024 / TPR rows at a time, K vectors per lane.
-template <typename T, typename W, int TPR, int K, End E>
-__global__ __launch_bounds__(1024, K * kVec<T> == 8 && sizeof(T) == 2 ? 8 : 4) void backward_kernel(
-    const Backward a) {
-  constexpr int N = kVec<T>, WAVES = TPR / 64, ROWS = 1024 / TPR;
-  __shared__ float slots[2][2][16];
-  extern __shared__ __align__(16) char dynamic[];
-  Vec<W, N>* const weight = (Vec<W, N>*)dynamic;       // [K * TPR], by vectors
-  float* const part = (float*)dynamic;                 // [ROWS][K * TPR * N], once the rows are done
-  const uint32_t lane = threadIdx.x % TPR, cols = held_cols<TPR * K * N>(a.cols);
-  const uint32_t sub = __builtin_amdgcn_readfirstlane(threadIdx.x / TPR);
-  const float inv = 1.0f / (float)a.cols;
-  for (uint32_t j = threadIdx.x; j < K * TPR; j += 1024)
-    weight[j] = load_vec<N, E>((const W*)a.weight, j * N, cols);
-  __syncthreads();
-  float dw[K][N], db[K][N];
-#pragma unroll
   for (int k = 0; k < K; ++k)
-#pragma unroll
-    for (int i = 0; i < N; ++i) dw[k][i] = db[k][i] = 0.0f;
-  Vec<T, N> dy[K], h[K];
-  const int64_t stride = (int64_t)gridDim.x * ROWS;
-  int turn = 0;
-  for (int64_t first = (int64_t)blockIdx.x * ROWS; first < a.rows; first += stride, turn ^= 1) {
-    const int64_t row = first + sub;
-    const bool mine = row < a.rows;
-    if (mine) {
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const uint32_t at = (k * TPR + lane) * N;
-        dy[k] = load_vec<N, E>((const T*)a.dy + row * a.cols, at, cols);
-        h[k] = load_vec<N, E>((const T*)a.h + row * a.cols, at, cols);
-      }
-    }
-    const float mean = a.mean && mine ? scalar_load(a.mean + row) : 0.0f;
-    const float rstd = mine ? scalar_load(a.rstd + row) : 0.0f;
-    float s1 = 0.0f, s2 = 0.0f;
-    if (mine) {
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const Vec<W, N> w = weight[k * TPR + lane];
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const float xh = (h[k][i] - mean) * rstd, d = dy[k][i], g = d * w[i];
-          s1 += g;
-          s2 = fmaf(g, xh, s2);
-          dw[k][i] = fmaf(d, xh, dw[k][i]);
-          db[k][i] += d;
-          asm volatile("" : "+v"(s1), "+v"(s2), "+v"(dw[k][i]), "+v"(db[k][i]));   // here, not later
-        }
-      }
-    }
-    // the slots of two rows in turn: one barrier per row is enough
-    s1 = reduce64(s1, Sum());
-    s2 = reduce64(s2, Sum());
-    if (WAVES > 1) {
-      if ((threadIdx.x & 63) == 0) {
-        slots[turn][0][threadIdx.x >> 6] = s1;
-        slots[turn][1][threadIdx.x >> 6] = s2;
-      }
-      __syncthreads();
-      s1 = reduce_few<WAVES>(slots[turn][0][sub * WAVES + lane % WAVES], Sum());
-      s2 = reduce_few<WAVES>(slots[turn][1][sub * WAVES + lane % WAVES], Sum());
-    }
-    if (mine) {
-      // dx = rstd (g - c1 - xh c2), with both constants times rstd
-      const float c1 = a.mean ? s1 * inv * rstd : 0.0f, c2 = s2 * inv * rstd * rstd;
-#pragma unroll
-      for (int k = 0; k < K; ++k) {
-        const uint32_t at = (k * TPR + lane) * N;
-        float d[N];
-        opaque(dy[k], c2);    // unpacked again from here: the floats need not live across the sums
-        opaque(h[k], c2);
-        const Vec<W, N> w = weight[k * TPR + lane];
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          d[i] = fmaf(mean - h[k][i], c2, fmaf(dy[k][i] * w[i], rstd, -c1));
-        }
-        if (a.dres) {
-          const Vec<T, N> r = load_vec<N, E>((const T*)a.dres + row * a.cols, at, cols);
-#pragma unroll
-          for (int i = 0; i < N; ++i) d[i] += r[i];
-        }
-        store_vec<E, true>((T*)a.dx + row * a.cols, at, cols, make_vec<T>(d));
-      }
-    }
-  }
-  // the rows' sums, added in their order
-  float* out = a.partial + (int64_t)blockIdx.x * a.sums * a.cols;
-  for (int v = 0; v < a.sums; ++v, out += cols) {
-    if (ROWS > 1) {
-      __syncthreads();
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-          part[(sub * K * TPR + k * TPR + lane) * N + i] = v ? db[k][i] : dw[k][i];
-      __syncthreads();
-      for (uint32_t c = threadIdx.x; c < cols; c += 1024) {
-        float s = part[c];
-#pragma unroll
-        for (int r = 1; r < ROWS; ++r) s += part[r * K * TPR * N + c];
-        out[c] = s;
-      }
+    if (FULL || own(k) == from(k)) {
+      store_vec(out + own(k), make_vec<float>(dw[k]));
+      if (a.sums == 2) store_vec(out + cols + own(k), make_vec<float>(db[k]));
     } else {
 #pragma unroll
-      for (int k = 0; k < K; ++k)
-        store_vec<E>(out, (k * TPR + lane) * N, cols, make_vec<float>(v ? db[k] : dw[k]));
+      for (int i = 0; i < N; ++i)
+        if (i >= (int)(own(k) - from(k))) {
+          out[from(k) + i] = dw[k][i];
+          if (a.sums == 2) out[cols + from(k) + i] = db[k][i];
+        }
     }
-  }
 }
 
 // Rows longer than the registers hold (and those under 8 columns): dx from two passes over the row ...
@@ -588,70 +556,85 @@ __global__ __launch_bounds__(1024) void column_sums_kernel(const float* __restri
 }
 
 // ----------------------------------------------------------------------------------- host
-// Workgroups of `threads` that fill the chip once (2048 threads on each of 256 compute units).
-constexpr int64_t resident(int threads) { return (int64_t)256 * 2048 / threads; }
-
-// Rows of `esize` bytes an element that a workgroup holds.  (Long binary32 rows whose end cuts a
-// vector would need more than 1024 threads' 128 registers in the backward pass.)
-bool held(int64_t cols, int64_t esize) {
-  return cols >= 8 && cols <= (esize == 4 && cols % 4 ? kMaxHeldCols / 2 : kMaxHeldCols);
+// Workgroups of `threads` in the forward pass: 1536 threads on each of 256 compute units, and two
+// workgroups at the least, so that one loads while the other adds up.  More is no faster with a
+// residual (8192 x 4096 bf16 50.0 us, 50.7 for 2048 threads) and worse where the last one does not
+// fit (6144 x 5120: 49.9 us for two of 640 threads, 60.7 for three).
+constexpr int64_t resident(int threads) {
+  return (int64_t)256 * (threads > 768 ? 2 : 1536 / threads);
 }
 
-template <typename T, typename W, int TPR, int K, End E>
-void forward_held(const Forward& a, hipStream_t s) {
-  constexpr int ROWS = TPR == 64 ? 4 : 1;
-  const int64_t groups = (a.rows + ROWS - 1) / ROWS;
-  constexpr int threads = TPR == 64 ? 256 : TPR;
-  const int64_t most = resident(threads);
-  forward_kernel<T, W, TPR, K, E><<<(unsigned)(groups < most ? groups : most), threads, 0, s>>>(a);
+// Rows that a workgroup holds.
+bool held(int64_t cols) { return cols >= 8 && cols <= kMaxHeldCols; }
+
+// Threads for a row with `per` elements each: whole wavefronts.
+int threads_for(int64_t cols, int per) { return (int)((cols + 64 * per - 1) / (64 * per)) * 64; }
+
+// How the end of held rows falls on vectors of N elements, `per` of them in a lane.
+template <int N>
+End end_of(int64_t cols, int per) {
+  return cols % (64 * per) == 0 ? kFull : cols % N == 0 ? kWhole : kCut;
 }
-template <typename T, typename W, End E>
-void forward(const Forward& a, hipStream_t s) {
-  constexpr int k = kUnits<T>;       // of a lane, to hold eight elements
-  if (a.cols <= 512) return forward_held<T, W, 64, k, E>(a, s);
-  if (a.cols <= 1024) return forward_held<T, W, 128, k, E>(a, s);
-  if (a.cols <= 2048) return forward_held<T, W, 256, k, E>(a, s);
-  if (a.cols <= 4096) return forward_held<T, W, 512, k, E>(a, s);
-  if (a.cols <= 8192) return forward_held<T, W, 1024, k, E>(a, s);
-  if constexpr (E == kWhole || sizeof(T) == 2) forward_held<T, W, 512, 4 * k, E>(a, s);
+
+// Calls f(std::integral_constant) for a runtime End.
+template <typename F>
+void with_end(End e, F f) {
+  if (e == kFull) f(std::integral_constant<End, kFull>());
+  else if (e == kWhole) f(std::integral_constant<End, kWhole>());
+  else f(std::integral_constant<End, kCut>());
 }
+
 template <typename T, typename W>
 void forward(const Forward& a, hipStream_t s) {
-  if (!held(a.cols, sizeof(T))) {
-    const int64_t groups = a.rows < resident(1024) ? a.rows : resident(1024);
-    forward_long_kernel<T, W><<<(unsigned)groups, 1024, 0, s>>>(a);
-  } else if (a.cols % kVec<T>) {
-    forward<T, W, kCut>(a, s);
-  } else {
-    forward<T, W, kWhole>(a, s);
+  constexpr int N = kVec<T>, k = kUnits<T>;
+  const auto grid = [&](int threads, int rows) {
+    const int64_t groups = (a.rows + rows - 1) / rows, most = resident(threads);
+    return (unsigned)(groups < most ? groups : most);
+  };
+  const auto launch = [&](auto kernel, int threads, int rows) {
+    kernel<<<grid(threads, rows), threads, 0, s>>>(a);
+  };
+  if (!held(a.cols)) {
+    launch(forward_long_kernel<T, W>, 1024, 1);
+  } else if (a.cols <= 512) {           // a wavefront; a workgroup of four of them
+    with_end(a.cols == 512 ? kFull : end_of<N>(a.cols, 8) == kCut ? kCut : kWhole, [&](auto e) {
+      launch(forward_kernel<T, W, 256, k, decltype(e)::value, true, true>, 256, 4);
+    });
+  } else if (a.cols <= 8192) {          // eight elements a lane
+    const int threads = threads_for(a.cols, 8);
+    with_end(end_of<N>(a.cols, 8), [&](auto e) {
+      constexpr End E = decltype(e)::value;
+      if (E == kFull && sizeof(T) == 2 && !a.residual)
+        launch(forward_kernel<T, W, 1024, k, E, false, !(E == kFull && sizeof(T) == 2)>, threads, 1);
+      else
+        launch(forward_kernel<T, W, 1024, k, E, false, true>, threads, 1);
+    });
+  } else {                              // thirty-two: 2051 x 14336 bf16 24.5 us, with sixteen 27.7
+    const int threads = threads_for(a.cols, 32);
+    with_end(end_of<N>(a.cols, 32), [&](auto e) {
+      launch(forward_kernel<T, W, 512, 4 * k, decltype(e)::value, false, false>, threads, 1);
+    });
   }
 }
 
 // Rows that a workgroup of the backward pass takes at a time, and the most workgroups: they fill
 // the chip once, and are also the partial rows of the column sums.
-// Rows of backward_full_kernel (binary32 ones over 8192 would not fit its registers).
-bool backward_full_cols(int64_t cols, int64_t esize) {
-  return cols > 512 && cols <= (esize == 4 ? 8192 : 16384) && cols % (cols <= 8192 ? 512 : 1024) == 0;
-}
-
-
 struct Split {
   int rows, most;
 };
+// Rows that a workgroup of the backward pass holds: long binary32 ones only if they fill it (the
+// others would need more than 1024 threads' 128 registers).
+bool backward_held(int64_t cols, int64_t esize) {
+  return held(cols) && (esize == 2 || cols <= 8192 || cols % 1024 == 0);
+}
 Split backward_split(int64_t cols, int64_t esize, bool dres) {
-  if (!held(cols, esize)) return {1, 256};
-  if (backward_full_cols(cols, esize)) {
-    const int threads = (int)(cols <= 8192 ? cols / 8 : cols / 16);
-    // what a compute unit has in flight: 512 threads with 48 or 64 bytes each, 1024 with 32.  More
-    // is no faster and leaves more partial rows (8192 x 4096 bf16: with dres 52.8 us for 512
-    // threads and 57.8 for 1024, without 53.5 and 43.9).
-    const int fill = esize == 4 || dres ? 512 : 1024;
-    return {1, 256 * (fill > threads ? fill / threads : 1)};
-  }
+  if (!backward_held(cols, esize)) return {1, 256};
   if (cols <= 512) return {16, 512};
-  int threads = 128;
-  while (threads < 1024 && threads * 8 < cols) threads *= 2;
-  return {1024 / threads, cols <= 4096 && esize == 2 ? 512 : 256};
+  // What a compute unit has in flight: 512 threads with 48 or 64 bytes each, 1024 with 32.  More
+  // is no faster and leaves more partial rows (8192 x 4096 bf16: with dres 52.8 us for 512
+  // threads and 57.8 for 1024, without 53.5 and 43.9).
+  const int threads = threads_for(cols, cols <= 8192 ? 8 : 16), fill = esize == 4 || dres ? 512 : 1024;
+  return {1, 256 * (fill > threads ? fill / threads : 1)};
 }
 int backward_groups(int64_t rows, int64_t cols, int64_t esize, bool dres) {
   const Split d = backward_split(cols, esize, dres);
@@ -659,55 +642,35 @@ int backward_groups(int64_t rows, int64_t cols, int64_t esize, bool dres) {
   return (int)(groups < d.most ? groups : d.most);
 }
 
-template <typename T, typename W, int THREADS, int K, End E>
-void backward_wave(const Backward& a, int groups, hipStream_t s) {
-  if (a.cols == 64 * K * kVec<T>) backward_wave_kernel<T, W, THREADS, K, kFull><<<groups, THREADS, 0, s>>>(a);
-  else backward_wave_kernel<T, W, THREADS, K, E><<<groups, THREADS, 0, s>>>(a);
-}
-template <typename T, typename W, int TPR, int K, End E>
-void backward_rows(const Backward& a, int groups, hipStream_t s) {
-  constexpr int weights = TPR * K * kVec<T> * sizeof(W), sums = 1024 * K * kVec<T> * 4;
-  constexpr int bytes = TPR < 1024 && sums > weights ? sums : weights;
-  auto kernel = backward_kernel<T, W, TPR, K, E>;
-  if (bytes > kPlainLds)
-    (void)hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  kernel<<<groups, 1024, bytes, s>>>(a);
-}
 template <typename T, typename W, int K>
-void backward_full(const Backward& a, int groups, hipStream_t s) {
-  constexpr int most = 1024 * K * kVec<T> * sizeof(W);
-  auto kernel = a.dres ? backward_full_kernel<T, W, K, true> : backward_full_kernel<T, W, K, false>;
-  const int threads = a.cols / (K * kVec<T>), bytes = a.cols * (int)sizeof(W);
+void backward_held(const Backward& a, int groups, hipStream_t s) {
+  constexpr int per = K * kVec<T>, most = 1024 * per * sizeof(W);
+  const bool full = a.cols % (64 * per) == 0;
+  auto kernel = a.dres ? backward_kernel<T, W, K, true, true> : backward_kernel<T, W, K, true, false>;
+  if constexpr (per == 8 || sizeof(T) == 2)
+    if (!full)
+      kernel = a.dres ? backward_kernel<T, W, K, false, true> : backward_kernel<T, W, K, false, false>;
+  const int threads = threads_for(a.cols, per), bytes = threads * per * (int)sizeof(W);
   if (most > kPlainLds && bytes > kPlainLds)
     (void)hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, most);
   kernel<<<groups, threads, bytes, s>>>(a);
 }
-template <typename T, typename W, End E>
-void backward(const Backward& a, int groups, hipStream_t s) {
-  constexpr int k = kUnits<T>;
-  constexpr bool half = sizeof(T) == 2;
-  if (backward_full_cols(a.cols, sizeof(T))) {
-    if (a.cols <= 8192) return backward_full<T, W, k>(a, groups, s);
-    if constexpr (half) return backward_full<T, W, 2 * k>(a, groups, s);
-  }
-  if (a.cols <= 512) backward_wave<T, W, 1024, k, E>(a, groups, s);
-  else if (a.cols <= 1024) backward_rows<T, W, 128, k, E>(a, groups, s);
-  else if (a.cols <= 2048) backward_rows<T, W, 256, k, E>(a, groups, s);
-  else if (a.cols <= 4096) backward_rows<T, W, 512, k, E>(a, groups, s);
-  else if (a.cols <= 8192) backward_rows<T, W, 1024, k, E>(a, groups, s);
-  else if constexpr (E == kWhole || half) backward_rows<T, W, 1024, 2 * k, E>(a, groups, s);
-}
 template <typename T, typename W>
 void backward(const Backward& a, int groups, void* dweight, void* dbias, hipStream_t s) {
+  constexpr int N = kVec<T>, k = kUnits<T>;
   if (groups == 0) {
-  } else if (!held(a.cols, sizeof(T))) {
+  } else if (!backward_held(a.cols, sizeof(T))) {
     const dim3 grid((unsigned)((a.cols + 2047) / 2048), (unsigned)groups);
     backward_long_columns_kernel<T><<<grid, 256, 0, s>>>(a);
     backward_long_kernel<T, W><<<(unsigned)(a.rows < 512 ? a.rows : 512), 1024, 0, s>>>(a);
-  } else if (a.cols % kVec<T>) {
-    backward<T, W, kCut>(a, groups, s);
+  } else if (a.cols <= 512) {
+    with_end(a.cols == 512 ? kFull : end_of<N>(a.cols, 8) == kCut ? kCut : kWhole, [&](auto e) {
+      backward_wave_kernel<T, W, 1024, k, decltype(e)::value><<<groups, 1024, 0, s>>>(a);
+    });
+  } else if (a.cols <= 8192) {
+    backward_held<T, W, k>(a, groups, s);
   } else {
-    backward<T, W, kWhole>(a, groups, s);
+    backward_held<T, W, 2 * k>(a, groups, s);
   }
   const dim3 grid((unsigned)((a.cols + 63) / 64), dbias ? 2 : 1);
   column_sums_kernel<W><<<grid, 1024, 0, s>>>(a.partial, groups, a.cols, (W*)dweight, (W*)dbias);
