@@ -24,14 +24,18 @@
 // more workgroups share a compute unit the better their passes overlap, so a row gets as few
 // threads as can hold it: 256 (4 workgroups a compute unit) to 16384 bf16 logits, 512 (2) to
 // 32768, or 49152 with shared memory; and 512 up to twice that, the rest being read again, before
-// 1024 (1), which hold 98304.  bf16, us per call: 8192 x 32000 270 with 512 threads, 437 with 1024;
-// 4096 x 60000 330 and 383, 98000 534 and 556, 128000 686 and 660.  Without holding anything,
-// 4096 x 128000 took 805 us with one workgroup a compute unit and 985 with two, whose rows
-// together pass the last-level cache: the second reading is what costs, not the exponentials.
-// Loads and stores bypass the caches (660 against 692 us; the rest of a long row, which is read
-// again, does not).  Rows of an odd length start at odd addresses and take longer (4096 x 127999:
-// 827 us); starting each at a 16-byte boundary (707 us) would let a row's last bits depend on
-// where it lies.
+// 1024 (1), which hold 98304, or with 88 registers per thread 122880, where the row has as many.
+// bf16, us per call: 8192 x 32000 270 with 512 threads, 437 with 1024; 4096 x 60000 330 and 383,
+// 98000 534 and 556, 128000 686 and 649; 88 registers 110000 594 and 577 with 64, 128000 649 and
+// 657, 200192 1050 and 1120.  Without holding anything, 4096 x 128000 took 805 us with one
+// workgroup a compute unit and 985 with two, whose rows together pass the last-level cache: the
+// second reading is what costs, not the exponentials.  Loads and stores bypass the caches (660
+// against 692 us; the rest of a long row, which is read again, does not).  Rows of an odd length
+// start at odd addresses and take longer (4096 x 127999: 827 us); starting each at a 16-byte
+// boundary (707 us) would let a row's last bits depend on where it lies.
+//
+// What bounds it is the memory: 4096 x 128000 bf16 reads and writes 3146 MB in 649 us, 4.85 TB/s,
+// where a copy of that size runs at 4.8.
 //
 // With fewer rows than compute units, a row is split over several workgroups in two launches:
 // partial statistics, then gradient and partial losses, which the last workgroup of a row adds
@@ -440,9 +444,10 @@ void launch_rows(const Distill& a, hipStream_t stream) {
 
 template <typename S, typename T>
 void launch(const Distill& a, hipStream_t stream) {
-  // units that a thread holds: 64 registers, and of 1024 threads 128 KB of shared memory
+  // units that a thread holds: 64 registers, and of 1024 threads 128 KB of shared memory; 88
+  // registers for rows that fill them (shorter ones would wait for loads of nothing)
   constexpr int unit = kUnit<S, T>, bytes = unit * (sizeof(S) + sizeof(T));
-  constexpr int regs = 256 / bytes, lds = 128 / bytes;
+  constexpr int regs = 256 / bytes, lds = 128 / bytes, more = 352 / bytes;
   if (a.splits > 1) {
     const dim3 grid((unsigned)a.splits, (unsigned)a.rows);
     split_stats_kernel<S, T><<<grid, kThreads, 0, stream>>>(a);
@@ -453,8 +458,10 @@ void launch(const Distill& a, hipStream_t stream) {
     launch_rows<S, T, 512, regs, 0>(a, stream);
   } else if (a.vocab <= 2 * 512 * unit * (regs + lds)) {
     launch_rows<S, T, 512, regs, lds>(a, stream);
-  } else {
+  } else if (a.vocab <= 1024 * unit * (more + lds)) {
     launch_rows<S, T, 1024, regs, lds>(a, stream);
+  } else {
+    launch_rows<S, T, 1024, more, lds>(a, stream);
   }
 }
 

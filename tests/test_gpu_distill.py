@@ -46,7 +46,8 @@ def logits(rows, vocab, S, T, seed=0, near=0.3, size=2.5):
 
 def reference(s, t, w, T):
     """loss, gradient, and the tolerances of both."""
-    s, t = s.double() / T, t.double() / T
+    # less the row's largest: next to 1e38, 64 bits have no room for the logarithm of the sum
+    s, t = ((x.double() - x.double().amax(1, keepdim=True)) / T for x in (s, t))
     w = torch.ones(s.shape[0], dtype=torch.float64, device="cuda") if w is None else w.double()
     ls, lt = s.logsumexp(1, keepdim=True), t.logsumexp(1, keepdim=True)
     lq, lp = s - ls, t - lt
@@ -287,3 +288,22 @@ def test_refusals(nv):
             (nv.NVFP4Error, lambda: nv.distill_loss(s, t, grad=t))):
         with pytest.raises(err):
             call()
+
+
+@pytest.mark.parametrize("S,T", [(BF, BF), (F, F), (BF, F), (F, BF)], ids=str)
+@pytest.mark.parametrize("vocab", [9001, 20003, 40008, 70001, 100003, 150001])
+def test_rows_of_every_held_length(nv, vocab, S, T):
+    """One workgroup to a row, with what it holds of the row filled, passed, and cut: from rows in
+    registers alone to ones of which a part is read again.  Also the rows that are done with exact
+    differences, at these lengths."""
+    say("[distill]", 192, vocab, S, T)
+    s, t = logits(192, vocab, S, T)
+    s[7, ::5] = -INF
+    t[7, ::5] = -INF
+    s[8] = torch.finfo(S).min
+    w = torch.rand(192, generator=torch.Generator("cuda").manual_seed(3), device="cuda") + 0.1
+    w[::2] = 0
+    w[8] = 1
+    loss, grad = check(nv, s, t, w, 0.7)
+    again, same = nv.distill_loss(s, t, w, temperature=0.7, grad=s)
+    assert torch.equal(again, loss) and torch.equal(same, grad)
