@@ -74,11 +74,12 @@ constexpr float kSlack = 16.0f;      // how far (in powers of two) entries may p
 template <typename S, typename T>
 constexpr int kUnit = sizeof(S) == 4 && sizeof(T) == 4 ? 4 : 8;
 // sum 2^(fma(x, c, -r)).  An empty one has r = the lowest finite value and sum 0; an entry of
-// -inf adds 0 to any.  `m` is an entry with r = c m (an r that overflows makes the sum useless:
-// see good()).
+// -inf adds 0 to any.  r is c times some entry, rounded (one that overflows makes the sum useless:
+// see good()); m is the largest entry.
 struct Stat {
-  float r, z;
+  float r, z, m;
   __device__ __forceinline__ void join(Stat o) {
+    m = fmaxf(m, o.m);
     const float top = fmaxf(r, o.r);
     z = z * exp2_(r - top) + o.z * exp2_(o.r - top);
     r = top;
@@ -88,6 +89,7 @@ struct Stat {
     float top = v[0];
 #pragma unroll
     for (int i = 1; i < N; ++i) top = fmaxf(top, v[i]);
+    m = fmaxf(m, top);
     top *= c;
     if (top > r + kSlack) {
       z *= exp2_(r - top);
@@ -109,7 +111,7 @@ struct Exact {
   }
 };
 
-// Both sums over a workgroup of WAVES wavefronts; every thread gets them.
+// r and z of both over a workgroup of WAVES wavefronts; every thread gets them.
 template <int WAVES>
 __device__ __forceinline__ void join_group(Stat& q, Stat& p, float (*slots)[4]) {
   const float rq = reduce64(q.r, Max()), rp = reduce64(p.r, Max());
@@ -214,11 +216,11 @@ struct Row {
 template <int THREADS, typename R>
 __device__ __forceinline__ void row_stats(R& row, void* lds, float c, Stat& q, Stat& p,
                                           float (*slots)[4]) {
-  q = p = Stat{kLowest, 0.0f};
+  q = p = Stat{kLowest, 0.0f, kLowest};
   row.load(lds, [&](const auto& a, const auto& b) { q.add(a, c), p.add(b, c); },
            [&](float a, float b) {
-             if (a != -INFINITY) q.join(Stat{a * c, 1.0f});
-             if (b != -INFINITY) p.join(Stat{b * c, 1.0f});
+             if (a != -INFINITY) q.join(Stat{a * c, 1.0f, a});
+             if (b != -INFINITY) p.join(Stat{b * c, 1.0f, b});
            });
   join_group<THREADS / 64>(q, p, slots);
 }
@@ -350,11 +352,18 @@ __global__ __launch_bounds__(THREADS) void row_kernel(const Distill a) {
   if (threadIdx.x == 0) a.loss[row] = loss;
 }
 
-// What a split of a row leaves for both of its logits: r and z of Stat, m and z of Exact (where
-// the fast sum is good, Exact has its value: c m = r but for r's rounding).
+// What a split of a row leaves for both of its logits: r and z of Stat, m and z of Exact, since
+// another split of the row can be one that the fast form has no sum of.
 struct Split {
   float r, z, m, e;
 };
+
+// A good sum, and the same over 2^((x - m) c): times 2^(r - c m), of which 2^(c m - r) is the
+// largest term of the sum (in halves: it may have no reciprocal).
+__device__ __forceinline__ Exact to_exact(Stat s, float m, float c) {
+  const float half = exp2_(-0.5f * fmaf(m, c, -s.r));
+  return Exact{m, s.z * half * half};
+}
 
 template <typename S, typename T>
 __global__ __launch_bounds__(kThreads) void split_stats_kernel(const Distill a) {
@@ -368,9 +377,12 @@ __global__ __launch_bounds__(kThreads) void split_stats_kernel(const Distill a) 
   Stat q, p;
   Row<S, T, kThreads, 0, 0> r(s, t, lo, hi);
   row_stats<kThreads>(r, nullptr, a.c, q, p, slots);
-  Exact eq{q.r / a.c, q.z}, ep{p.r / a.c, p.z};
-  if (!q.good()) eq = row_exact<kThreads>(s, lo, hi, a.c, sums);
-  if (!p.good()) ep = row_exact<kThreads>(t, lo, hi, a.c, sums);
+  const float mq = reduce_group<kThreads / 64>(q.m, Max(), sums);
+  __syncthreads();
+  const float mp = reduce_group<kThreads / 64>(p.m, Max(), sums);
+  __syncthreads();
+  const Exact eq = q.good() ? to_exact(q, mq, a.c) : row_exact<kThreads>(s, lo, hi, a.c, sums);
+  const Exact ep = p.good() ? to_exact(p, mp, a.c) : row_exact<kThreads>(t, lo, hi, a.c, sums);
   if (threadIdx.x == 0) {
     Split* out = (Split*)a.stats + (row * a.splits + blockIdx.x) * 2;
     out[0] = Split{q.r, q.z, eq.m, eq.z};
@@ -393,11 +405,11 @@ __global__ __launch_bounds__(kThreads) void split_grad_kernel(const Distill a) {
   const S* s = (const S*)a.student + row * a.student_stride;
   const T* t = (const T*)a.teacher + row * a.teacher_stride;
   const Split* in = (const Split*)a.stats + row * a.splits * 2;
-  Stat q{in[0].r, in[0].z}, p{in[1].r, in[1].z};
+  Stat q{in[0].r, in[0].z, 0.0f}, p{in[1].r, in[1].z, 0.0f};
   Exact eq{in[0].m, in[0].e}, ep{in[1].m, in[1].e};
   for (int i = 1; i < a.splits; ++i) {
-    q.join(Stat{in[2 * i].r, in[2 * i].z});
-    p.join(Stat{in[2 * i + 1].r, in[2 * i + 1].z});
+    q.join(Stat{in[2 * i].r, in[2 * i].z, 0.0f});
+    p.join(Stat{in[2 * i + 1].r, in[2 * i + 1].z, 0.0f});
     eq.join(Exact{in[2 * i].m, in[2 * i].e}, a.c);
     ep.join(Exact{in[2 * i + 1].m, in[2 * i + 1].e}, a.c);
   }

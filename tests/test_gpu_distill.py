@@ -307,3 +307,21 @@ def test_rows_of_every_held_length(nv, vocab, S, T):
     loss, grad = check(nv, s, t, w, 0.7)
     again, same = nv.distill_loss(s, t, w, temperature=0.7, grad=s)
     assert torch.equal(again, loss) and torch.equal(same, grad)
+
+
+@pytest.mark.parametrize("rows,vocab", [(1, 32769), (3, 50011), (100, 40009), (127, 33000)])
+def test_rows_of_several_workgroups(nv, rows, vocab):
+    """Few long rows, which several workgroups share, and the same rows among many, which have one
+    each: both hold to the definition."""
+    for S, T in ((BF, BF), (F, F), (BF, F)):
+        s, t = logits(rows, vocab, S, T, near=0.01)
+        check(nv, s, t)
+        many = [torch.cat([x, x[:1].expand(128 - rows, vocab)]).contiguous() for x in (s, t)]
+        check(nv, *many)
+        s, t = logits(rows, vocab, S, T, near=5.0, size=1000.0)
+        check(nv, s, t)
+        s[0] = torch.finfo(S).min
+        check(nv, s, t)
+    if rows < 100:
+        test_strides_offsets_and_in_place(nv, max(rows, 2), vocab)
+    test_gradient_against_differences(nv, vocab)
