@@ -19,7 +19,7 @@
 // Where c x overflows (rows of the lowest finite value; logits near the largest) the fast form
 // has no sum; such a row is done again with (x - max) c, which keeps their differences.
 //
-// With rows for every compute unit a workgroup takes a row and holds what it can of it between
+// With rows for the compute units a workgroup takes a row and holds what it can of it between
 // the passes: 64 registers per thread, and up to 128 KB of a compute unit's shared memory.  The
 // more workgroups share a compute unit the better their passes overlap, so a row gets as few
 // threads as can hold it: 256 (4 workgroups a compute unit) to 16384 bf16 logits, 512 (2) to
@@ -37,7 +37,7 @@
 // What bounds it is the memory: 4096 x 128000 bf16 reads and writes 3146 MB in 649 us, 4.85 TB/s,
 // where a copy of that size runs at 4.8.
 //
-// With fewer rows than compute units, a row is split over several workgroups in two launches:
+// Where the rows are few and long, a row is split over several workgroups in two launches:
 // partial statistics, then gradient and partial losses, which the last workgroup of a row adds
 // in order.
 #include "train_common.h"
@@ -435,11 +435,14 @@ __global__ __launch_bounds__(kThreads) void split_grad_kernel(const Distill a) {
 // Places within a row fit 32 bits, their bytes and those of a whole split past them too.
 constexpr int64_t kMaxVocab = int64_t(1) << 28;
 
-// Workgroups per row: one where there are rows for the 256 compute units, else enough for
-// them, each with two vectors per thread at the least.
+// Workgroups per row: few rows that are long enough to be worth two launches get as many as the
+// 256 compute units have room for at one each, and two units per thread.  bf16, us, one workgroup
+// and several: 3 x 32000 9.6 and 11.6, 8 x 40000 11.8 and 11.2, 8 x 64000 19.3 and 11.9, 8 x 128000
+// 30.0 and 14.0, 64 x 64000 20.0 and 16.7, 100 x 64000 20.7 and 19.5, 100 x 256000 67 and 52, 127 x
+// 64000 21.5 and 22.7, 127 x 256000 69 and 67.
 int splits_of(int64_t rows, int64_t vocab) {
-  if (rows <= 0 || rows >= 192) return 1;
-  const int64_t want = (256 + rows - 1) / rows, most = (vocab + 16383) / 16384;
+  if (rows <= 0 || rows > 100 || vocab <= 32768) return 1;
+  const int64_t want = 256 / rows, most = (vocab + 16383) / 16384;
   return (int)(want < most ? want : most);
 }
 
