@@ -17,7 +17,8 @@
  *
  * Ownership, ordering, errors: as in nvfp4_amax.h.  Pointers are device pointers owned by the
  * caller unless marked as host memory; the library allocates nothing and keeps no state; all
- * work is enqueued on `stream` and the calls return at once and may be captured in a HIP graph.
+ * work is enqueued on `stream` and the calls return at once and may be captured in a HIP graph
+ * (which replays the numbers given by the host, such as AdamW's step, as they were).
  * Tensors need the alignment of their element type only.  Argument errors come back before
  * anything is enqueued and leave the outputs untouched.  Results depend on the arguments alone
  * (no atomics whose order matters): the same call gives the same bits on the same device.
@@ -55,7 +56,7 @@ const char* nvfp4_train_status_str(nvfp4_status status);
  * h may equal x or residual where that is contiguous, and y may equal x, where no h is written
  * in its place; any other overlap with an output is rejected.
  * out_amax (may be NULL): float [1], max |y| over all rows as nvfp4_amax defines it (0 for no
- * rows).  rows >= 0, cols >= 1, eps >= 0.  One launch, two with out_amax. */
+ * rows).  rows >= 0, 1 <= cols <= 2^30, eps >= 0.  One launch, two with out_amax. */
 nvfp4_status nvfp4_layernorm_forward(const void* x, int64_t x_stride, const void* residual,
                                      int64_t residual_stride, const void* weight,
                                      const void* bias, int64_t rows, int64_t cols,
@@ -71,7 +72,8 @@ nvfp4_status nvfp4_layernorm_forward(const void* x, int64_t x_stride, const void
  * dy, h, dres (may be NULL: the gradient that reaches h past the norm) [rows][cols] of `type`,
  * dx [rows][cols]; all contiguous.  dx may equal dy or dres.  dx is the gradient of x and of the
  * residual alike.  workspace: nvfp4_layernorm_backward_workspace(...) bytes, 16-byte aligned, any
- * content.  rows == 0 gives dweight = dbias = 0.  Two launches. */
+ * content.  rows == 0 gives dweight = dbias = 0.  Two launches; three where a row is more than a
+ * workgroup holds (16384 columns; 8192 binary32 ones that are no multiple of 1024). */
 int64_t nvfp4_layernorm_backward_workspace(int64_t rows, int64_t cols);
 nvfp4_status nvfp4_layernorm_backward(const void* dy, const void* h, const void* weight,
                                       const float* mean, const float* rstd, const void* dres,
@@ -94,7 +96,8 @@ nvfp4_status nvfp4_layernorm_backward(const void* dy, const void* h, const void*
  * grad_stride, or NULL (loss only).  grad may equal student (same stride).  temperature > 0, and 1 / T
  * finite.
  * workspace: nvfp4_distill_loss_workspace(...) bytes, 16-byte aligned, any content (may be NULL
- * where that is 0).  rows >= 0, vocab >= 1.  One launch; two for few rows. */
+ * where that is 0).  rows >= 0, 1 <= vocab <= 2^28.  One launch; two for few long rows, which several
+ * workgroups share. */
 int64_t nvfp4_distill_loss_workspace(int64_t rows, int64_t vocab);
 nvfp4_status nvfp4_distill_loss(const void* student, int64_t student_stride, const void* teacher,
                                 int64_t teacher_stride, const float* weight, int64_t rows,

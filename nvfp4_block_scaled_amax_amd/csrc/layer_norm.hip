@@ -1,11 +1,14 @@
 // Layer norm forward and backward for gfx950 (include/nvfp4_train.h defines the operation).
 //
-// A row is held in registers by one wavefront (up to 1024 columns) or one workgroup (up to
-// 16384), eight consecutive elements per lane and step, so that x is read once: the mean and then
-// the centred sum of squares come from the registers.  Longer rows are read again for each of
-// the three steps.  The backward pass keeps, next to the row, its share of the column sums
-// (dweight, dbias) in registers over all the rows that a workgroup takes, leaves them as one
-// partial row per workgroup in the workspace, and a second launch adds those in a fixed order.
+// Both directions move bytes and little else: the forward pass reads x (and the residual) and
+// writes y (and h) once, the backward pass reads dy and h (and dres) and writes dx once.  So a row
+// is held in registers while its sums are made: up to 512 columns by 16, 32 or 64 lanes of a
+// wavefront, eight elements each; up to 16384 by one workgroup of as many wavefronts as the row
+// fills.  The variance is the mean square of what is held less the mean (not E[x^2] - mean^2, which
+// cancels).  Longer rows are read again for each step.  The backward pass keeps, next to the row, its
+// share of the column sums (dweight, dbias) in registers over all the rows that a workgroup
+// takes, leaves them as one partial row per workgroup in the workspace, and a second launch adds
+// those in a fixed order.  Loads are 16 bytes a lane, at any alignment of the element.
 #include <type_traits>
 
 #include "train_common.h"
@@ -52,14 +55,15 @@ constexpr int kUnits = 8 / kVec<T>;
 // A lane's vector of a row of `cols` elements that is held: where it is, and where it is loaded
 // from.  No load depends on a condition (the compiler can then count the loads in flight, and wait
 // for the first of them alone): a vector past the row's end, or cut by it, is loaded from the last
-// N elements, and settled when it is used.
+// N elements, and settled when it is used.  (Rows that may have fewer than N, kAny, do without.)
 template <int N, End E>
 struct Place {
-  uint32_t at, from;
+  uint32_t at, from, end;
   __device__ __forceinline__ Place(uint32_t at_, uint32_t cols)
-      : at(at_), from(E == kFull || at_ < cols - N ? at_ : cols - N) {}
+      : at(at_), from(E == kFull || E == kAny || at_ < cols - N ? at_ : cols - N), end(cols) {}
   template <typename T>
   __device__ __forceinline__ Vec<T, N> load(const T* row) const {
+    if (E == kAny) return load_vec<N, E>(row, at, end);
     return load_vec<N>(row + from);
   }
   // zeros past the row's end (kCut; with kWhole a vector is in the row or not: see in())
@@ -79,20 +83,37 @@ __device__ __forceinline__ float scalar_load(const float* p) {
   return *(const __attribute__((address_space(4))) float*)(uintptr_t)p;
 }
 
+// The sum over groups of LANES lanes, to every lane.
+template <int LANES>
+__device__ __forceinline__ float sum_lanes(float v) {
+  if (LANES == 64) return reduce64(v, Sum());
+  v = reduce16(v, Sum());
+  if (LANES == 32) v += __shfl_xor(v, 16, 32);
+  return v;
+}
+
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
 
-// Rows of up to 512 columns take a wavefront each (WAVE), longer ones a workgroup; a lane holds K
-// vectors, and where that is eight elements (HOLD) also its weights for all the rows that it comes
-// by (8192 x 4097 bf16 83 us, 100 if they are read for each; 8192 x 4096 f32 47.5 and 51.2).  Rows of
-// bf16 that fill the workgroup, without a residual, are an exception that only the measurement
-// explains: 26.9 us for 8192 x 4096 with the weights held, 22.8 without.
-template <typename T, typename W, int THREADS, int K, End E, bool WAVE, bool HOLD>
+// y = (h - mean) rstd weight + bias.  Rows of up to 512 columns take a wavefront each, those of up
+// to 256 and 128 a half and a quarter of one (LANES; 262144 x 128 bf16 26.8 us, 52.4 with a wavefront
+// each); longer ones a workgroup (LANES == 0).  A lane holds K vectors, and where that is eight
+// elements (HOLD) also its weights for all the rows that it comes by (8192 x 4097 bf16 83 us, 100
+// if they are read for each; 8192 x 4096 f32 47.5 and 51.2).  Rows of bf16 that fill the workgroup,
+// without a residual, are an exception that only the measurement explains: 26.9 us for
+// 8192 x 4096 with the weights held, 23.3 without.
+//
+// The memory bounds it: 8192 x 4096 bf16 with residual and h 49.5 us (268 MB, 5.4 TB/s; a copy of
+// that size 5.4), without 23.3 (134 MB, half of it in the last-level cache), f32 47.5; 65536 x 512
+// bf16 27.2 us, 4.9 TB/s.  An odd width costs bf16 rows the alignment of every other one
+// (8192 x 4097: 30.6 us).  One row is the launch: 2.6 us of kernel.
+template <typename T, typename W, int THREADS, int K, End E, int LANES, bool HOLD>
 __global__ __launch_bounds__(THREADS) void forward_kernel(const Forward a) {
-  constexpr int N = kVec<T>;
+  constexpr int N = kVec<T>, ROWS = LANES ? THREADS / (LANES ? LANES : 1) : 1;    // at a time
   __shared__ float slots[2][2][16];
   __shared__ uint32_t top[16];
-  const uint32_t waves = blockDim.x / 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-  const uint32_t lane = WAVE ? threadIdx.x % 64 : threadIdx.x, lanes = WAVE ? 64 : blockDim.x;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const uint32_t lanes = LANES ? LANES : blockDim.x, lane = LANES ? threadIdx.x % lanes : threadIdx.x;
+  const uint32_t first = LANES == 64 ? wave : LANES ? threadIdx.x / lanes : 0;
   const uint32_t cols = a.cols;
   const float inv = 1.0f / (float)a.cols;
   auto vector = [&](const void* v, int k) {
@@ -104,24 +125,23 @@ __global__ __launch_bounds__(THREADS) void forward_kernel(const Forward a) {
   Vec<W, N> weight[HOLD ? K : 1], bias[HOLD ? K : 1];
 #pragma unroll
   for (int k = 0; k < (HOLD ? K : 0); ++k) weight[k] = vector(a.weight, k), bias[k] = vector(a.bias, k);
-  if (!WAVE) {
+  if (!LANES) {
     if (threadIdx.x < 64) ((float*)slots)[threadIdx.x] = 0.0f;      // those of wavefronts not there
     if (threadIdx.x < 16) top[threadIdx.x] = 0u;
     __syncthreads();
   }
   // over the row; the slots of two rows in turn
   auto total = [&](float v, float* part) {
+    if (LANES) return sum_lanes<LANES ? LANES : 64>(v);
     v = reduce64(v, Sum());
-    if (WAVE) return v;
     if ((threadIdx.x & 63) == 0) part[wave] = v;
     lds_barrier();
     return reduce16(part[threadIdx.x % 16], Sum());
   };
   uint32_t most = 0;
   int turn = 0;
-  const int64_t step = (int64_t)gridDim.x * (WAVE ? waves : 1);
-  for (int64_t row = (int64_t)blockIdx.x * (WAVE ? waves : 1) + (WAVE ? wave : 0); row < a.rows;
-       row += step, turn ^= 1) {
+  const int64_t step = (int64_t)gridDim.x * ROWS;
+  for (int64_t row = (int64_t)blockIdx.x * ROWS + first; row < a.rows; row += step, turn ^= 1) {
     const T* x = (const T*)a.x + row * a.x_stride;
     Vec<T, N> q[K];
     float v[K][N];
@@ -167,7 +187,7 @@ __global__ __launch_bounds__(THREADS) void forward_kernel(const Forward a) {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         v[k][i] -= mean;
-        const float d = E != kCut || at.in(cols, i) ? v[k][i] : 0.0f;
+        const float d = E < kCut || at.in(cols, i) ? v[k][i] : 0.0f;
         part = fmaf(d, d, part);
       }
       sq += at.in(cols) ? part : 0.0f;
@@ -194,10 +214,11 @@ __global__ __launch_bounds__(THREADS) void forward_kernel(const Forward a) {
       }
     }
   }
-  if (a.amax) publish_amax<WAVE ? THREADS / 64 : 16>(most, a.amax, top);
+  if (a.amax) publish_amax<LANES ? THREADS / 64 : 16>(most, a.amax, top);
 }
 
-// Rows longer than the registers hold (and those under 8 columns): three passes over the row.
+// Rows longer than the registers hold: three passes over the row, of which the caches serve some
+// (1024 x 32768 bf16 49.5 us, f32 77: 2.7 and 3.5 TB/s of one read and one write).
 template <typename T, typename W>
 __global__ __launch_bounds__(1024) void forward_long_kernel(const Forward a) {
   __shared__ float slots[2][16];
@@ -262,26 +283,28 @@ __global__ __launch_bounds__(1024) void forward_long_kernel(const Forward a) {
   if (a.amax) publish_amax<16>(most, a.amax, top);
 }
 
-// A row in a wavefront: K vectors per lane.  Each wavefront goes its own way to the end, where the
-// workgroup adds their column sums in order.
-template <typename T, typename W, int THREADS, int K, End E>
+// A row in a wavefront or a part of it: K vectors per lane.  Each group of LANES goes its own way
+// to the end, where the workgroup adds their column sums in order.  Bound by the memory, at two
+// workgroups a compute unit: 65536 x 512 bf16 42 us, 262144 x 128 42.6 (86 with a wavefront for
+// each row), 4.8 TB/s with the column sums' launch.
+template <typename T, typename W, int THREADS, int K, End E, int LANES>
 __global__ __launch_bounds__(THREADS) void backward_wave_kernel(const Backward a) {
-  constexpr int N = kVec<T>, WAVES = THREADS / 64;
-  __shared__ float part[WAVES][64 * N];
-  const uint32_t lane = threadIdx.x % 64, cols = a.cols;
-  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  constexpr int N = kVec<T>, ROWS = THREADS / LANES;
+  __shared__ float part[ROWS][LANES * N];
+  const uint32_t lane = threadIdx.x % LANES, cols = a.cols;
+  const uint32_t first = LANES == 64 ? __builtin_amdgcn_readfirstlane(threadIdx.x / 64) : threadIdx.x / LANES;
   const float inv = 1.0f / (float)a.cols;
   float dw[K][N], db[K][N];
 #pragma unroll
   for (int k = 0; k < K; ++k)
 #pragma unroll
     for (int i = 0; i < N; ++i) dw[k][i] = db[k][i] = 0.0f;
-  for (int64_t row = (int64_t)blockIdx.x * WAVES + wave; row < a.rows;
-       row += (int64_t)gridDim.x * WAVES) {
+  for (int64_t row = (int64_t)blockIdx.x * ROWS + first; row < a.rows;
+       row += (int64_t)gridDim.x * ROWS) {
     Vec<T, N> dy[K], h[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const uint32_t at = (k * 64 + lane) * N;
+      const uint32_t at = (k * LANES + lane) * N;
       dy[k] = load_vec<N, E>((const T*)a.dy + row * a.cols, at, cols);
       h[k] = load_vec<N, E>((const T*)a.h + row * a.cols, at, cols);
     }
@@ -289,7 +312,7 @@ __global__ __launch_bounds__(THREADS) void backward_wave_kernel(const Backward a
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      uint32_t at = (k * 64 + lane) * N;
+      uint32_t at = (k * LANES + lane) * N;
       asm volatile("" : "+v"(at));       // read again for each row: not worth registers
       const Vec<W, N> w = load_vec<N, E>((const W*)a.weight, at, cols);
 #pragma unroll
@@ -303,11 +326,11 @@ __global__ __launch_bounds__(THREADS) void backward_wave_kernel(const Backward a
       }
     }
     // dx = rstd (g - c1 - xh c2), with both constants times rstd
-    const float c1 = a.mean ? reduce64(s1, Sum()) * inv * rstd : 0.0f;
-    const float c2 = reduce64(s2, Sum()) * inv * rstd * rstd;
+    const float c1 = a.mean ? sum_lanes<LANES>(s1) * inv * rstd : 0.0f;
+    const float c2 = sum_lanes<LANES>(s2) * inv * rstd * rstd;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      uint32_t at = (k * 64 + lane) * N;
+      uint32_t at = (k * LANES + lane) * N;
       opaque(at, c2);
       opaque(dy[k], c2);  // unpacked again from here: the floats need not live across the sums
       opaque(h[k], c2);
@@ -330,13 +353,13 @@ __global__ __launch_bounds__(THREADS) void backward_wave_kernel(const Backward a
 #pragma unroll
     for (int k = 0; k < K; ++k) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) part[wave][lane * N + i] = v ? db[k][i] : dw[k][i];
+      for (int i = 0; i < N; ++i) part[first][lane * N + i] = v ? db[k][i] : dw[k][i];
       __syncthreads();
-      for (uint32_t c = threadIdx.x; c < 64 * N; c += THREADS) {
+      for (uint32_t c = threadIdx.x; c < LANES * N; c += THREADS) {
         float s = part[0][c];
 #pragma unroll
-        for (int r = 1; r < WAVES; ++r) s += part[r][c];
-        if (k * 64 * N + c < cols) out[k * 64 * N + c] = s;
+        for (int r = 1; r < ROWS; ++r) s += part[r][c];
+        if (k * LANES * N + c < cols) out[k * LANES * N + c] = s;
       }
       __syncthreads();
     }
@@ -350,6 +373,10 @@ __global__ __launch_bounds__(THREADS) void backward_wave_kernel(const Backward a
 // row does not fill the workgroup (not FULL), a vector past the row's end, or cut by it, is the last
 // N elements instead.  Its lane then computes and writes what its neighbours do, the same
 // bits, and its weights are zero in the row's sums for the elements that are not its own.
+//
+// Bound by the memory: 8192 x 4096 bf16 with dres 50.3 us (268 MB, 5.3 TB/s), without 39 (5.2), and
+// the column sums' launch.  2051 x 14336 bf16 takes 38 us (4.6 TB/s): 256 workgroups of 896 threads,
+// of which three take a ninth row.
 template <typename T, typename W, int K, bool FULL, bool RES>
 __global__ __launch_bounds__(1024) void backward_kernel(const Backward a) {
   constexpr int N = kVec<T>;
@@ -466,7 +493,8 @@ __global__ __launch_bounds__(1024) void backward_kernel(const Backward a) {
     }
 }
 
-// Rows longer than the registers hold (and those under 8 columns): dx from two passes over the row ...
+// Rows longer than the registers hold: dx from two passes over the row (with the column sums, which
+// read dy and h a third time, 1024 x 32768 bf16 102 us, f32 180) ...
 template <typename T, typename W>
 __global__ __launch_bounds__(1024) void backward_long_kernel(const Backward a) {
   __shared__ float slots[2][16];
@@ -531,7 +559,8 @@ __global__ __launch_bounds__(256) void backward_long_columns_kernel(const Backwa
 }
 
 // dweight (y == 0) and dbias (y == 1): a lane adds a column, the 16 wavefronts of a workgroup
-// take every 16th partial row, and their sums are added in order.
+// take every 16th partial row, and their sums are added in order.  Short: 512 partial rows of both
+// sums of 4096 columns 4.6 us, 256 of one of 14336 4.6, 64 of 256 columns 2.5, most of it the launch.
 template <typename W>
 __global__ __launch_bounds__(1024) void column_sums_kernel(const float* __restrict__ partial,
                                                            int groups, int cols, W* dweight,
@@ -565,7 +594,7 @@ constexpr int64_t resident(int threads) {
 }
 
 // Rows that a workgroup holds.
-bool held(int64_t cols) { return cols >= 8 && cols <= kMaxHeldCols; }
+bool held(int64_t cols) { return cols <= kMaxHeldCols; }
 
 // Threads for a row with `per` elements each: whole wavefronts.
 int threads_for(int64_t cols, int per) { return (int)((cols + 64 * per - 1) / (64 * per)) * 64; }
@@ -576,12 +605,27 @@ End end_of(int64_t cols, int per) {
   return cols % (64 * per) == 0 ? kFull : cols % N == 0 ? kWhole : kCut;
 }
 
+// Lanes of a wavefront for a row of up to 512 columns: eight elements each.
+int lanes_for(int64_t cols) { return cols <= 128 ? 16 : cols <= 256 ? 32 : 64; }
+
 // Calls f(std::integral_constant) for a runtime End.
 template <typename F>
 void with_end(End e, F f) {
   if (e == kFull) f(std::integral_constant<End, kFull>());
   else if (e == kWhole) f(std::integral_constant<End, kWhole>());
   else f(std::integral_constant<End, kCut>());
+}
+
+// Calls f(lanes, end) for a row of up to 512 columns in vectors of N elements.
+template <int N, typename F>
+void with_lanes(int64_t cols, F f) {
+  const int lanes = lanes_for(cols);
+  if (cols < 8) return f(std::integral_constant<int, 16>(), std::integral_constant<End, kAny>());
+  with_end(cols == lanes * 8 ? kFull : cols % N == 0 ? kWhole : kCut, [&](auto e) {
+    if (lanes == 16) f(std::integral_constant<int, 16>(), e);
+    else if (lanes == 32) f(std::integral_constant<int, 32>(), e);
+    else f(std::integral_constant<int, 64>(), e);
+  });
 }
 
 template <typename T, typename W>
@@ -596,23 +640,24 @@ void forward(const Forward& a, hipStream_t s) {
   };
   if (!held(a.cols)) {
     launch(forward_long_kernel<T, W>, 1024, 1);
-  } else if (a.cols <= 512) {           // a wavefront; a workgroup of four of them
-    with_end(a.cols == 512 ? kFull : end_of<N>(a.cols, 8) == kCut ? kCut : kWhole, [&](auto e) {
-      launch(forward_kernel<T, W, 256, k, decltype(e)::value, true, true>, 256, 4);
+  } else if (a.cols <= 512) {           // a wavefront or part of one; a workgroup of four of them
+    with_lanes<N>(a.cols, [&](auto lanes, auto e) {
+      constexpr int L = decltype(lanes)::value;
+      launch(forward_kernel<T, W, 256, k, decltype(e)::value, L, true>, 256, 256 / L);
     });
   } else if (a.cols <= 8192) {          // eight elements a lane
     const int threads = threads_for(a.cols, 8);
     with_end(end_of<N>(a.cols, 8), [&](auto e) {
       constexpr End E = decltype(e)::value;
       if (E == kFull && sizeof(T) == 2 && !a.residual)
-        launch(forward_kernel<T, W, 1024, k, E, false, !(E == kFull && sizeof(T) == 2)>, threads, 1);
+        launch(forward_kernel<T, W, 1024, k, E, 0, !(E == kFull && sizeof(T) == 2)>, threads, 1);
       else
-        launch(forward_kernel<T, W, 1024, k, E, false, true>, threads, 1);
+        launch(forward_kernel<T, W, 1024, k, E, 0, true>, threads, 1);
     });
   } else {                              // thirty-two: 2051 x 14336 bf16 24.5 us, with sixteen 27.7
     const int threads = threads_for(a.cols, 32);
     with_end(end_of<N>(a.cols, 32), [&](auto e) {
-      launch(forward_kernel<T, W, 512, 4 * k, decltype(e)::value, false, false>, threads, 1);
+      launch(forward_kernel<T, W, 512, 4 * k, decltype(e)::value, 0, false>, threads, 1);
     });
   }
 }
@@ -629,7 +674,7 @@ bool backward_held(int64_t cols, int64_t esize) {
 }
 Split backward_split(int64_t cols, int64_t esize, bool dres) {
   if (!backward_held(cols, esize)) return {1, 256};
-  if (cols <= 512) return {16, 512};
+  if (cols <= 512) return {1024 / lanes_for(cols), 512};
   // What a compute unit has in flight: 512 threads with 48 or 64 bytes each, 1024 with 32.  More
   // is no faster and leaves more partial rows (8192 x 4096 bf16: with dres 52.8 us for 512
   // threads and 57.8 for 1024, without 53.5 and 43.9).
@@ -664,8 +709,9 @@ void backward(const Backward& a, int groups, void* dweight, void* dbias, hipStre
     backward_long_columns_kernel<T><<<grid, 256, 0, s>>>(a);
     backward_long_kernel<T, W><<<(unsigned)(a.rows < 512 ? a.rows : 512), 1024, 0, s>>>(a);
   } else if (a.cols <= 512) {
-    with_end(a.cols == 512 ? kFull : end_of<N>(a.cols, 8) == kCut ? kCut : kWhole, [&](auto e) {
-      backward_wave_kernel<T, W, 1024, k, decltype(e)::value><<<groups, 1024, 0, s>>>(a);
+    with_lanes<N>(a.cols, [&](auto lanes, auto e) {
+      backward_wave_kernel<T, W, 1024, k, decltype(e)::value, decltype(lanes)::value>
+          <<<groups, 1024, 0, s>>>(a);
     });
   } else if (a.cols <= 8192) {
     backward_held<T, W, k>(a, groups, s);

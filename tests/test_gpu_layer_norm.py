@@ -359,3 +359,27 @@ def test_refusals(nv):
             (nv.NVFP4Error, lambda: nv.layer_norm_backward(x, r, w, m, m, dx=r))):
         with pytest.raises(err):
             call()
+
+
+@pytest.mark.parametrize("T,W", [(BF, BF), (BF, F), (F, F), (F, BF)], ids=str)
+@pytest.mark.parametrize("cols", [3, 6, 60, 100, 127, 128, 129, 200, 252, 256, 257])
+def test_several_rows_to_a_wavefront(nv, cols, T, W):
+    """Rows of a head's width and less, more of them than the workgroups take at a time, their
+    number odd; in place, and with strides."""
+    for rows in (1, 19, 40013):
+        say("[norm] narrow", rows, cols, T, W)
+        x, r, w, b, gen = inputs(rows, cols, T, W)
+        y, h, mean, rstd = check_forward(nv, x, r, w, b, True)
+        a = r.clone()
+        again = nv.layer_norm(x, w, b, residual=a, h=a)
+        assert torch.equal(again[0], y) and torch.equal(a, h)
+        wide = torch.full((rows, cols + 5), 9.0, device="cuda", dtype=T)
+        wide[:, :cols] = x
+        check_forward(nv, wide[:, :cols], None, w, None, False)
+        dy = (0.01 * randn(gen, rows, cols)).to(T)
+        dres = (0.01 * r.float()).to(T)
+        dx, dw, db = check_backward(nv, dy, h, w, mean, rstd, dres)
+        a = dy.clone()
+        again = nv.layer_norm_backward(a, h, w, mean, rstd, dres=dres, dx=a)
+        assert torch.equal(again[0], dx) and torch.equal(again[1], dw) and torch.equal(again[2], db)
+        check_backward(nv, dy, h, w, None, rstd, None, bias=False)
