@@ -252,8 +252,8 @@ class AdamWPlan:
     params, master, exp_avg, exp_avg_sq, avg_scale, sq_scale are lists of tensors (None for a
     kind that is not there); a checkpoint saves and restores their contents.  With 8-bit states
     exp_avg holds E4M3 codes of m / avg_scale and exp_avg_sq those of sqrt(v) / sq_scale, one
-    scale per 128 elements.  The tensors' memory is read at each step, so `p.data = ...` is
-    noticed; their number, sizes and types are the plan's."""
+    scale per 128 elements.  The tensors' addresses are read at each step, so `p.data = ...` is
+    noticed, and refused where the number, the sizes or the types are no longer the plan's."""
 
     KINDS = ("params", "exp_avg", "exp_avg_sq", "master", "avg_scale", "sq_scale")
 
@@ -273,23 +273,16 @@ class AdamWPlan:
         if master is not None and self.dtype != torch.bfloat16:
             raise ValueError("a master copy goes with bfloat16 parameters only")
         blocks = [-(-n // ADAMW_BLOCK) for n in self.numels]
-        for kind, sizes, dtype in (("params", self.numels, self.dtype), ("exp_avg", self.numels, state),
-                                   ("exp_avg_sq", self.numels, state),
-                                   ("master", self.numels, torch.float32),
-                                   ("avg_scale", blocks, torch.float32),
-                                   ("sq_scale", blocks, torch.float32)):
-            tensors = getattr(self, kind)
-            if tensors is None:
-                continue
-            if len(tensors) != len(params):
-                raise ValueError("%s: %d tensors for %d parameters" % (kind, len(tensors), len(params)))
-            for t, n in zip(tensors, sizes):
-                self._look(kind, t, n, dtype)
         # nvfp4_adamw_tensor, an entry a row
         self._table = np.zeros((len(params), 8), np.int64)
         self._table[:, 7] = self.numels
-        self._columns = [(0, params), (2, exp_avg), (3, exp_avg_sq)]
-        self._columns += [(k, v) for k, v in ((4, master), (5, avg_scale), (6, sq_scale)) if v is not None]
+        self._at = {}                   # the addresses in it: tensors that are elsewhere are checked
+        self._columns = [(k, kind, sizes, dtype) for k, kind, sizes, dtype in (
+            (0, "params", self.numels, self.dtype), (2, "exp_avg", self.numels, state),
+            (3, "exp_avg_sq", self.numels, state), (4, "master", self.numels, torch.float32),
+            (5, "avg_scale", blocks, torch.float32), (6, "sq_scale", blocks, torch.float32))
+            if getattr(self, kind) is not None]
+        self._fill()
 
     def _look(self, kind, t, numel, dtype):
         if t.dtype != dtype:
@@ -300,13 +293,22 @@ class AdamWPlan:
             raise ValueError("%s must be contiguous, with %d elements, got %s"
                              % (kind, numel, tuple(t.shape)))
 
+    def _fill(self):
+        for k, kind, sizes, dtype in self._columns:
+            tensors = getattr(self, kind)
+            now = [t.data_ptr() for t in tensors]
+            if now != self._at.get(k):
+                if len(tensors) != len(sizes):
+                    raise ValueError("%s: %d tensors for %d parameters" % (kind, len(tensors), len(sizes)))
+                for t, n in zip(tensors, sizes):
+                    self._look(kind, t, n, dtype)
+                self._table[:, k] = self._at[k] = now
+
     def table(self, grads) -> np.ndarray:
         """The entries of nvfp4_adamw_tensor for these gradients."""
-        rows = self._table
-        for k, tensors in self._columns:
-            rows[:, k] = [t.data_ptr() for t in tensors]
-        rows[:, 1] = [g.data_ptr() for g in grads]
-        return rows
+        self._fill()
+        self._table[:, 1] = [g.data_ptr() for g in grads]
+        return self._table
 
 
 def adamw_plan(params, exp_avg=None, exp_avg_sq=None, *, master=None, avg_scale=None,

@@ -464,3 +464,27 @@ def test_refusals(nv):
             (nv.NVFP4Error, lambda: nv.adamw_step(plan, [p], **ok))):
         with pytest.raises(err):
             call()
+
+
+def test_parameters_that_moved(nv):
+    """New memory of the same size is taken; of another size, type or number it is refused."""
+    params = [torch.nn.Parameter(torch.ones(n, device="cuda")) for n in (300, 40)]
+    plan = nv.adamw_plan(params)
+    grads = [torch.ones_like(p) for p in params]
+    old = params[0].data
+    params[0].data = torch.full((300,), 5.0, device="cuda")
+    nv.adamw_step(plan, grads, step=1, lr=0.5, weight_decay=0.0)
+    assert (old == 1).all() and ((params[0] - 4.5).abs() < 1e-5).all() and ((params[1] - 0.5).abs() < 1e-5).all()
+    params[1].data = torch.ones(39, device="cuda")
+    for _ in range(2):
+        with pytest.raises(ValueError, match="params"):
+            nv.adamw_step(plan, grads, step=2, lr=0.5)
+    params[1].data = torch.ones(40, device="cuda")
+    plan.exp_avg[0] = torch.zeros(300, device="cuda", dtype=torch.bfloat16)
+    with pytest.raises(TypeError, match="exp_avg"):
+        nv.adamw_step(plan, grads, step=2, lr=0.5)
+    plan.exp_avg[0] = torch.zeros(300, device="cuda")
+    plan.exp_avg.pop()
+    with pytest.raises(ValueError, match="exp_avg"):
+        nv.adamw_step(plan, grads, step=2, lr=0.5)
+    assert ((params[0] - 4.5).abs() < 1e-5).all() and (params[1] == 1).all()
