@@ -568,19 +568,22 @@ __global__ __launch_bounds__(1024) void column_sums_kernel(const float* __restri
   __shared__ float part[16][64];
   W* out = blockIdx.y ? dbias : dweight;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
-  float s = 0.0f;
-  if (c < cols) {
-    const float* p = partial + (int64_t)blockIdx.y * cols + c;
+  for (int64_t first = (int64_t)blockIdx.x * 64; first < cols; first += (int64_t)gridDim.x * 64) {
+    const int64_t c = first + lane;
+    float s = 0.0f;
+    if (c < cols) {
+      const float* p = partial + (int64_t)blockIdx.y * cols + c;
 #pragma unroll 16
-    for (int g = wave; g < groups; g += 16) s += p[(int64_t)g * gridDim.y * cols];
-  }
-  part[wave][lane] = s;
-  __syncthreads();
-  if (wave == 0 && c < cols) {
+      for (int g = wave; g < groups; g += 16) s += p[(int64_t)g * gridDim.y * cols];
+    }
+    part[wave][lane] = s;
+    __syncthreads();
+    if (wave == 0 && c < cols) {
 #pragma unroll
-    for (int i = 1; i < 16; ++i) s += part[i][lane];
-    out[c] = from_f32<W>(s);
+      for (int i = 1; i < 16; ++i) s += part[i][lane];
+      out[c] = from_f32<W>(s);
+    }
+    __syncthreads();
   }
 }
 
@@ -718,7 +721,8 @@ void backward(const Backward& a, int groups, void* dweight, void* dbias, hipStre
   } else {
     backward_held<T, W, 2 * k>(a, groups, s);
   }
-  const dim3 grid((unsigned)((a.cols + 63) / 64), dbias ? 2 : 1);
+  const int64_t columns = ((int64_t)a.cols + 63) / 64, most = 1 << 20;    // threads stay below 2^32
+  const dim3 grid((unsigned)(columns < most ? columns : most), dbias ? 2 : 1);
   column_sums_kernel<W><<<grid, 1024, 0, s>>>(a.partial, groups, a.cols, (W*)dweight, (W*)dbias);
 }
 

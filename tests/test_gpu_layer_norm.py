@@ -383,3 +383,19 @@ def test_several_rows_to_a_wavefront(nv, cols, T, W):
         again = nv.layer_norm_backward(a, h, w, mean, rstd, dres=dres, dx=a)
         assert torch.equal(again[0], dx) and torch.equal(again[1], dw) and torch.equal(again[2], db)
         check_backward(nv, dy, h, w, None, rstd, None, bias=False)
+
+
+def test_backward_of_a_row_past_a_launch(nv):
+    """A row with more columns than one launch has threads for their sums (2^32 / 16)."""
+    cols = (1 << 28) + 9
+    gen = torch.Generator("cuda").manual_seed(8)
+    h, dy = (torch.randn(1, cols, generator=gen, device="cuda", dtype=BF) for _ in range(2))
+    w = torch.ones(cols, device="cuda", dtype=BF)
+    mean, rstd = torch.full((1,), 0.25, device="cuda"), torch.full((1,), 0.5, device="cuda")
+    dx, dw, db = nv.layer_norm_backward(dy, h, w, mean, rstd)
+    assert torch.equal(db, dy[0])
+    for at in (0, (1 << 26) - 5, (1 << 28) - 100, cols - 50):
+        part = slice(at, min(at + 1000, cols))
+        want = dy[0, part].double() * (h[0, part].double() - 0.25) * 0.5
+        near(dw[part], want, (HALF[BF] + 4 * U) * want.abs() * (1 + HALF[BF])
+             + dy[0, part].double().abs() * h[0, part].double().abs() * U + 1e-40, "dweight")
