@@ -488,3 +488,40 @@ def test_parameters_that_moved(nv):
     with pytest.raises(ValueError, match="exp_avg"):
         nv.adamw_step(plan, grads, step=2, lr=0.5)
     assert ((params[0] - 4.5).abs() < 1e-5).all() and (params[1] == 1).all()
+
+
+def test_a_tensor_past_32_bits(nv):
+    """Elements past 2^32 are updated as they would be by themselves; the random bits do not repeat
+    there."""
+    n, size = (1 << 32) + 5000, 5000
+    gen = torch.Generator("cuda").manual_seed(6)
+    places = (0, (1 << 31) - 77, (1 << 32) - 2048, n - size)
+    grad = torch.randn(size, generator=gen, device="cuda").to(BF)
+    g = torch.zeros(n, device="cuda", dtype=BF)
+    for at in places:
+        g[at:at + size] = grad
+    args = dict(step=3, lr=0.01, weight_decay=0.0)
+    p = torch.ones(n, device="cuda")
+    plan = nv.adamw_plan([p])
+    nv.adamw_step(plan, [g], **args)
+    few = torch.ones(size, device="cuda")
+    want = nv.adamw_plan([few])
+    nv.adamw_step(want, [grad], **args)
+    # the last place begins within the one before it, which ends there
+    first = {at: min([b - at for b in places if b > at] + [size]) for at in places}
+    for at, m in first.items():
+        assert torch.equal(p[at:at + m], few[:m]) and torch.equal(plan.exp_avg[0][at:at + m], want.exp_avg[0][:m])
+    assert (p[size:1 << 20] == 1).all() and (p[1 << 31:][size:1 << 20] == 1).all()
+    del p, plan
+    torch.cuda.empty_cache()
+    p = torch.ones(n, device="cuda", dtype=BF)
+    plan = nv.adamw_plan([p], state="e4m3")
+    nv.adamw_step(plan, [g], **args)
+    for at, m in first.items():
+        got, exact = p[at:at + m].float(), few[:m]
+        assert ((got - exact).abs() <= 2.0 ** -7).all() and (got != 1).any()
+    tail = p[n - size:]
+    alone = torch.ones(size, device="cuda", dtype=BF)
+    nv.adamw_step(nv.adamw_plan([alone], state="e4m3"), [grad], **args)
+    assert not torch.equal(tail, alone) and not torch.equal(p[:size], tail)
+    assert torch.equal(p[:first[0]], alone[:first[0]])

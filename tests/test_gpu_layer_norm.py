@@ -399,3 +399,31 @@ def test_backward_of_a_row_past_a_launch(nv):
         want = dy[0, part].double() * (h[0, part].double() - 0.25) * 0.5
         near(dw[part], want, (HALF[BF] + 4 * U) * want.abs() * (1 + HALF[BF])
              + dy[0, part].double().abs() * h[0, part].double().abs() * U + 1e-40, "dweight")
+
+
+def test_offsets_past_32_bits(nv):
+    """More than 2^31 elements: the last rows are what they are by themselves, and the column sums
+    have their part."""
+    for rows, cols in ((131080, 16384), (8388700, 257)):
+        say("[norm] offsets", rows, cols)
+        gen = torch.Generator("cuda").manual_seed(4)
+        x = torch.zeros(rows, cols, device="cuda", dtype=BF)
+        last = randn(gen, 40, cols).to(BF)
+        x[-40:] = last
+        w, b = randn(gen, cols), randn(gen, cols)
+        y, _, mean, rstd = nv.layer_norm(x, w, b)
+        y2, _, mean2, rstd2 = nv.layer_norm(last, w, b)
+        assert torch.equal(y[-40:], y2) and torch.equal(mean[-40:], mean2) and torch.equal(rstd[-40:], rstd2)
+        assert torch.equal(y[:9], b.to(BF).expand(9, cols)) and torch.equal(y[-49:-40], y[:9])
+        dy = y.zero_()
+        dy[-40:] = randn(gen, 40, cols).to(BF)
+        few = dy[-40:].clone()
+        dx, dw, db = nv.layer_norm_backward(dy, x, w, mean, rstd)
+        want, want_w, want_b, _, xh, _, _ = backward_reference(few, last, w, mean2, rstd2, None)
+        dx2, _, _ = check_backward(nv, few, last, w, mean2, rstd2, None)
+        assert torch.equal(dx[-40:], dx2) and not dx[:9].any() and not dx[-49:-40].any()
+        lever = (few.double().abs() * rstd2.double()[:, None] * last.double().abs() * U).sum(0)
+        near(dw, want_w, 104 * U * (few.double() * xh).abs().sum(0) + lever + U * want_w.abs() + 1e-40, "dweight")
+        near(db, want_b, 104 * U * few.double().abs().sum(0) + U * want_b.abs() + 1e-40, "dbias")
+        del x, y, dy, dx
+        torch.cuda.empty_cache()
