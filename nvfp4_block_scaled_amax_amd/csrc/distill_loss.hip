@@ -16,8 +16,9 @@
 // that q's normalization brings into both its parts cancels to second order: the loss of a
 // student near its teacher keeps its precision.
 //
-// Where c x overflows (rows of the lowest finite value; logits near the largest) the fast form
-// has no sum; such a row is done again with (x - max) c, which keeps their differences.
+// Where c x is 2^14 or more (logits of 11000, a temperature of 1/100; rows of the lowest finite value,
+// where it overflows) the fast form has too few bits for what lies between R and log2 Z, or no sum;
+// such a row is done again with (x - max) c, which keeps the differences, in four readings.
 //
 // With rows for the compute units a workgroup takes a row and holds what it can of it between
 // the passes: 64 registers per thread, and up to 128 KB of a compute unit's shared memory.  The
@@ -74,8 +75,7 @@ constexpr float kSlack = 16.0f;      // how far (in powers of two) entries may p
 template <typename S, typename T>
 constexpr int kUnit = sizeof(S) == 4 && sizeof(T) == 4 ? 4 : 8;
 // sum 2^(fma(x, c, -r)).  An empty one has r = the lowest finite value and sum 0; an entry of
-// -inf adds 0 to any.  r is c times some entry, rounded (one that overflows makes the sum useless:
-// see good()); m is the largest entry.
+// -inf adds 0 to any.  r is c times some entry, rounded; m is the largest entry.
 struct Stat {
   float r, z, m;
   __device__ __forceinline__ void join(Stat o) {
@@ -98,8 +98,19 @@ struct Stat {
 #pragma unroll
     for (int i = 0; i < N; ++i) z += exp2_(fmaf(v[i], c, -r));
   }
-  __device__ __forceinline__ bool good() const { return z > 0.0f && z < INFINITY; }
+  // Whether the fast form can go on from here: z is a number that a ratio has room for (a row's is
+  // between 2^-1 and 2^16 times its length while r is small), and r is so small that log2 of a ratio
+  // added to it is rounded by 2^-11 at the most, whose square row_grad leaves out.
+  __device__ __forceinline__ bool good() const {
+    return z > 0x1p-60f && z < 0x1p60f && fabsf(r) < 16384.0f;
+  }
 };
+
+// One entry: its term is 1 but for what r is rounded by (0 for one near the lowest value).
+__device__ __forceinline__ Stat single(float x, float c) {
+  const float r = fmaxf(x * c, kLowest);
+  return Stat{r, exp2_(fmaf(x, c, -r)), x};
+}
 
 // The same with exact differences: max x, and sum 2^((x - max) c).
 struct Exact {
@@ -219,8 +230,8 @@ __device__ __forceinline__ void row_stats(R& row, void* lds, float c, Stat& q, S
   q = p = Stat{kLowest, 0.0f, kLowest};
   row.load(lds, [&](const auto& a, const auto& b) { q.add(a, c), p.add(b, c); },
            [&](float a, float b) {
-             if (a != -INFINITY) q.join(Stat{a * c, 1.0f, a});
-             if (b != -INFINITY) p.join(Stat{b * c, 1.0f, b});
+             if (a != -INFINITY) q.join(single(a, c));
+             if (b != -INFINITY) p.join(single(b, c));
            });
   join_group<THREADS / 64>(q, p, slots);
 }
@@ -252,7 +263,7 @@ __device__ __forceinline__ float row_grad(R& row, void* lds, S* grad, float c, f
   const float by = log2f(q.z / p.z), r = q.r + by;
   const float part = r - q.r, off = (q.r - (r - part)) + (by - part);
   const float scale = weight / (temperature * p.z);
-  const float back = 1.0f - off * kLn2;       // 2^-off
+  const float back = 1.0f - off * kLn2;       // 2^-off: |off| <= 2^-11, see good()
   // Zp sum of (q - p) + ln 2 p (X - Y): both parts of a unit meet before they are added to the
   // others, because their sums over the row are far larger than the loss
   float sum = 0.0f;

@@ -325,3 +325,18 @@ def test_rows_of_several_workgroups(nv, rows, vocab):
     if rows < 100:
         test_strides_offsets_and_in_place(nv, max(rows, 2), vocab)
     test_gradient_against_differences(nv, vocab)
+
+
+@pytest.mark.parametrize("rows,vocab", [(3, 5), (200, 2000), (2, 40000)])
+def test_large_logits(nv, rows, vocab):
+    """Logits (over T) so large that a 32-bit exponent has few bits left, or none, for the logarithm
+    of the sum."""
+    for S, T in ((F, F), (BF, F), (BF, BF)):
+        for size, temp in ((100.0, 0.01), (100.0, 0.001), (2e4, 1.0), (1e6, 1.0), (1e10, 1.0), (1e30, 3.0)):
+            say("[distill] large", rows, vocab, S, T, size, temp)
+            s, t = logits(rows, vocab, S, T, near=0.3, size=size)
+            s[0, 1] = t[0, 1] = s[0, 0]           # shared largest entries, in some rows
+            s[0, 2], t[0, 2] = s[0, 0], s[0, 0]
+            check(nv, s, t, T=temp)
+            check(nv, t.to(S), t, T=temp)
+            check(nv, s * 0.0, t, T=temp)
