@@ -106,8 +106,8 @@ nvfp4_status nvfp4_distill_loss(const void* student, int64_t student_stride, con
                                 void* workspace, hipStream_t stream);
 
 /* One AdamW step over many tensors, in place.  Per element, in binary32 with one rounding per
- * operation as written (the quotient within 2 ulp; with 8-bit states sqrt(v) within 1 ulp where
- * 0 < v < 2^-96):
+ * operation as written (the quotient within 2 ulp where its divisor is within 2^-126 .. 2^126; with
+ * 8-bit states sqrt(v) within 1 ulp where 0 < v < 2^-96):
  *   g = grad * grad_scale[0]                  (grad_scale: device float, NULL = no factor)
  *   m = m * beta1 + g * (1 - beta1)
  *   v = v * beta2 + (g * g) * (1 - beta2)
