@@ -285,8 +285,9 @@ __global__ __launch_bounds__(1024) void forward_long_kernel(const Forward a) {
 
 // A row in a wavefront or a part of it: K vectors per lane.  Each group of LANES goes its own way
 // to the end, where the workgroup adds their column sums in order.  Bound by the memory, at two
-// workgroups a compute unit: 65536 x 512 bf16 42 us, 262144 x 128 42.6 (86 with a wavefront for
-// each row), 4.8 TB/s with the column sums' launch.
+// workgroups a compute unit: 65536 x 512 bf16 42 us, 262144 x 128 42.4 (86 with a wavefront for
+// each row), 4.8 TB/s with the column sums' launch; 262144 x 512 150 (5.4), and 164 with half as
+// many threads.
 template <typename T, typename W, int THREADS, int K, End E, int LANES>
 __global__ __launch_bounds__(THREADS) void backward_wave_kernel(const Backward a) {
   constexpr int N = kVec<T>, ROWS = THREADS / LANES;
@@ -675,18 +676,26 @@ struct Split {
 bool backward_held(int64_t cols, int64_t esize) {
   return held(cols) && (esize == 2 || cols <= 8192 || cols % 1024 == 0);
 }
+// Rows that a wavefront takes by itself: one vector a lane, or two of bf16 (16384 x 1024 22.7 us,
+// 28.7 with a workgroup each; 2048 x 1024 8.0 and 11.2; but 65536 x 1024 84 and 82).  binary32 would
+// take four (16384 x 1024 with dres 58 us, and 55), and bf16 of 2048 columns, too (46 and 45).
+bool backward_wave(int64_t cols, int64_t esize) { return cols <= 512 || (esize == 2 && cols <= 1024); }
 Split backward_split(int64_t cols, int64_t esize, bool dres) {
   if (!backward_held(cols, esize)) return {1, 256};
   if (cols <= 512) return {1024 / lanes_for(cols), 512};
+  if (backward_wave(cols, esize)) return {8, 512};
   // What a compute unit has in flight: 512 threads with 48 or 64 bytes each, 1024 with 32.  More
   // is no faster and leaves more partial rows (8192 x 4096 bf16: with dres 52.8 us for 512
   // threads and 57.8 for 1024, without 53.5 and 43.9).
   const int threads = threads_for(cols, cols <= 8192 ? 8 : 16), fill = esize == 4 || dres ? 512 : 1024;
   return {1, 256 * (fill > threads ? fill / threads : 1)};
 }
+// A workgroup for each compute unit, then four rows at the least to a partial row (bf16, 2048
+// columns: 1024 rows 10.7 us, 14.0 with a workgroup for each of them; 2051 rows 13.5 and 16.1).
 int backward_groups(int64_t rows, int64_t cols, int64_t esize, bool dres) {
   const Split d = backward_split(cols, esize, dres);
-  const int64_t groups = (rows + d.rows - 1) / d.rows;
+  const int64_t all = (rows + d.rows - 1) / d.rows, few = (rows + 3) / 4 > 256 ? (rows + 3) / 4 : 256;
+  const int64_t groups = all < few ? all : few;
   return (int)(groups < d.most ? groups : d.most);
 }
 
@@ -716,6 +725,11 @@ void backward(const Backward& a, int groups, void* dweight, void* dbias, hipStre
       backward_wave_kernel<T, W, 1024, k, decltype(e)::value, decltype(lanes)::value>
           <<<groups, 1024, 0, s>>>(a);
     });
+  } else if (backward_wave(a.cols, sizeof(T))) {
+    if constexpr (sizeof(T) == 2)
+      with_end(a.cols == 1024 ? kFull : a.cols % N == 0 ? kWhole : kCut, [&](auto e) {
+        backward_wave_kernel<T, W, 512, 2 * k, decltype(e)::value, 64><<<groups, 512, 0, s>>>(a);
+      });
   } else if (a.cols <= 8192) {
     backward_held<T, W, k>(a, groups, s);
   } else {

@@ -427,3 +427,21 @@ def test_offsets_past_32_bits(nv):
         near(db, want_b, 104 * U * few.double().abs().sum(0) + U * want_b.abs() + 1e-40, "dbias")
         del x, y, dy, dx
         torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("T,W", [(BF, BF), (BF, F), (F, F), (F, BF)], ids=str)
+@pytest.mark.parametrize("cols", [513, 520, 777, 1016, 1023, 1024, 1025])
+def test_backward_of_rows_about_a_wavefronts_length(nv, cols, T, W):
+    """Few rows, some hundred, and more than the workgroups take at a time; in place."""
+    for rows in (1, 19, 300, 9001):
+        h, dres, w, _, gen = inputs(rows, cols, T, W)
+        dy = (0.01 * randn(gen, rows, cols)).to(T)
+        dres = (0.01 * dres.float()).to(T)
+        _, mean, rstd = forward_reference(h, w, None, 1e-5, True)
+        mean, rstd = mean[:, 0].float(), rstd[:, 0].float()
+        check_backward(nv, dy, h, w, None, rstd, None, bias=False)
+        dx, dw, db = check_backward(nv, dy, h, w, mean, rstd, dres)
+        for target in ("dy", "dres"):
+            a, c = dy.clone(), dres.clone()
+            got = nv.layer_norm_backward(a, h, w, mean, rstd, dres=c, dx=a if target == "dy" else c)
+            assert torch.equal(got[0], dx) and torch.equal(got[1], dw) and torch.equal(got[2], db)
