@@ -24,7 +24,10 @@
 // With rows for the compute units a workgroup takes a row and holds what it can of it between
 // the passes: 64 registers per thread, and up to 128 KB of a compute unit's shared memory.  The
 // more workgroups share a compute unit the better their passes overlap, so a row gets as few
-// threads as can hold it: 256 (4 workgroups a compute unit) to 16384 bf16 logits, 512 (2) to
+// threads as can hold it, and no more registers than it fills, since what is loaded past its end
+// is not free (8192 x 1000 bf16 14.3 us with 128 threads of one vector each, 19.5 with 256, 31 with
+// 256 of eight; 8192 x 6000 52 with four vectors, 58 with eight; 4000 x 8191 with four 43, 59 with eight):
+// 128 threads to 1024 bf16 logits, 256 (4 workgroups a compute unit) to 16384, 512 (2) to
 // 32768, or 49152 with shared memory; and 512 up to twice that, the rest being read again, before
 // 1024 (1), which hold 98304, or with 88 registers per thread 122880, where the row has as many.
 // bf16, us per call: 8192 x 32000 270 with 512 threads, 437 with 1024; 4096 x 60000 330 and 383,
@@ -165,11 +168,13 @@ struct Row {
   __device__ __forceinline__ uint32_t place(int k) const {
     return lo + (k * THREADS + threadIdx.x) * N;
   }
-  // where a vector past the row's end is loaded from: its first one (unused, but no branch
-  // stands between the loads)
-  __device__ __forceinline__ uint32_t inside(int k) const {
+  // where a vector is loaded from: one past the row's end from its beginning, at a 16-byte boundary
+  // (unused, but no branch stands between the loads; 2000 x 17001 bf16 53 us, 62 from odd addresses)
+  template <typename V>
+  __device__ __forceinline__ uint32_t inside(const V* row, int k) const {
     const uint32_t at = place(k);
-    return at < whole ? at : lo;
+    const uint32_t even = lo + (uint32_t)(-(intptr_t)(row + lo) & 15) / sizeof(V);
+    return at < whole ? at : even + N <= hi ? even : lo;
   }
   static __device__ __forceinline__ VS* lds_a(void* lds, int k) {
     return (VS*)lds + k * THREADS + threadIdx.x;
@@ -184,13 +189,13 @@ struct Row {
     if (lo < whole) {
 #pragma unroll
       for (int k = 0; k < REGS; ++k) {
-        a[k] = load_vec<N, true>(s + inside(k));
-        b[k] = load_vec<N, true>(t + inside(k));
+        a[k] = load_vec<N, true>(s + inside(s, k));
+        b[k] = load_vec<N, true>(t + inside(t, k));
       }
 #pragma unroll
       for (int k = 0; k < LDS; ++k) {
-        const VS x = load_vec<N, true>(s + inside(REGS + k));
-        const VT y = load_vec<N, true>(t + inside(REGS + k));
+        const VS x = load_vec<N, true>(s + inside(s, REGS + k));
+        const VT y = load_vec<N, true>(t + inside(t, REGS + k));
         *lds_a(lds, k) = x;
         *lds_b(lds, k) = y;
         if (place(REGS + k) < whole) f(x, y);
@@ -479,6 +484,14 @@ void launch(const Distill& a, hipStream_t stream) {
     const dim3 grid((unsigned)a.splits, (unsigned)a.rows);
     split_stats_kernel<S, T><<<grid, kThreads, 0, stream>>>(a);
     split_grad_kernel<S, T><<<grid, kThreads, 0, stream>>>(a);
+  } else if (a.vocab <= 128 * unit) {
+    launch_rows<S, T, 128, 1, 0>(a, stream);
+  } else if (a.vocab <= 256 * unit) {
+    launch_rows<S, T, 256, 1, 0>(a, stream);
+  } else if (a.vocab <= 256 * unit * 2) {
+    launch_rows<S, T, 256, 2, 0>(a, stream);
+  } else if (a.vocab <= 256 * unit * 4) {
+    launch_rows<S, T, 256, 4, 0>(a, stream);
   } else if (a.vocab <= 256 * unit * regs) {
     launch_rows<S, T, 256, regs, 0>(a, stream);
   } else if (a.vocab <= 512 * unit * regs) {

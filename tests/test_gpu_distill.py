@@ -340,3 +340,20 @@ def test_large_logits(nv, rows, vocab):
             check(nv, s, t, T=temp)
             check(nv, t.to(S), t, T=temp)
             check(nv, s * 0.0, t, T=temp)
+
+
+@pytest.mark.parametrize("S,T", [(BF, BF), (F, F), (BF, F), (F, BF)], ids=str)
+@pytest.mark.parametrize("vocab", [11, 512, 513, 1001, 1024, 1025, 2047, 2049, 3001, 4096, 4097, 6007, 8192, 8193])
+def test_short_rows(nv, vocab, S, T):
+    """Every number of vectors that a thread may hold, filled and not, rows beginning anywhere."""
+    say("[distill] short", vocab, S, T)
+    s, t = logits(130, vocab, S, T)
+    w = torch.rand(130, generator=torch.Generator("cuda").manual_seed(3), device="cuda")
+    w[::7] = 0
+    loss, grad = check(nv, s, t, w, 1.5)
+    buf = torch.zeros(130 * (vocab + 1) + 1, device="cuda", dtype=S)
+    view = buf[1:].view(130, vocab + 1)[:, :vocab]
+    view.copy_(s)
+    again, same = nv.distill_loss(view, t, w, temperature=1.5, grad=view)
+    assert torch.equal(again, loss) and torch.equal(same, grad)
+    assert not buf[vocab + 1::vocab + 1].any() and buf[0] == 0
