@@ -67,7 +67,7 @@ def _call(name: str, x: torch.Tensor, *args):
     """The entry point `name` on x's device and its current stream; raises on an error status.
     (A call of a few microseconds: the device is only switched where it has to be.)"""
     fn, dev = getattr(lib(), name), x.get_device()
-    if dev == torch.cuda.current_device():
+    if dev == torch._C._cuda_getDevice():
         status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
@@ -112,17 +112,17 @@ def _like(t: torch.Tensor, shape, dtypes, x: torch.Tensor, what: str):
 
 
 def _vector(t: torch.Tensor, shape, dtypes, x: torch.Tensor, what: str):
-    _like(t, shape, dtypes, x, what)
-    if not t.is_contiguous():
+    """The same, and that it is contiguous.  (One condition: it is what small calls wait for.)"""
+    if not (t.shape == shape and t.dtype in dtypes and t.is_contiguous()
+            and t.get_device() == x.get_device()):
+        _like(t, shape, dtypes, x, what)
         raise ValueError("%s must be contiguous" % what)
 
 
 def _out(t, shape, dtype, x: torch.Tensor) -> torch.Tensor:
-    """The caller's output, checked, or a new one.  (empty_like of a contiguous tensor takes a
-    third of empty's time.)"""
+    """The caller's output, checked, or a new one.  (The callers make those that are like a contiguous
+    tensor with torch.empty_like, in two thirds of the time.)"""
     if t is None:
-        if x.dtype == dtype and x.shape == shape and x.is_contiguous():
-            return torch.empty_like(x)
         return x.new_empty(shape, dtype=dtype)
     if t.shape != shape or t.dtype != dtype or not t.is_contiguous() or t.device != x.device:
         raise ValueError("output must be a contiguous %s tensor of shape %s on %s"
@@ -167,12 +167,15 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor = None,
     if residual is not None:
         _like(residual, shape, (dtype,), x, "residual")
         rs = _rows(residual, shape, "residual")
-        h = _out(h, shape, dtype, x)
+        h = torch.empty_like(x) if h is None and xs == cols else _out(h, shape, dtype, x)
     elif h is not None:
         raise ValueError("h is an output of the residual form only")
-    y = _out(y, shape, dtype, x)
+    y = torch.empty_like(x) if y is None and xs == cols else _out(y, shape, dtype, x)
     rstd = _out(rstd, lead, torch.float32, x)
-    mean = _out(mean, lead, torch.float32, rstd) if center else None
+    if center:
+        mean = torch.empty_like(rstd) if mean is None else _out(mean, lead, torch.float32, x)
+    else:
+        mean = None
     if amax is not None:
         _vector(amax, (1,), _F32, x, "amax")
     _call("nvfp4_layernorm_forward", x, x.data_ptr(), xs, _ptr(residual), rs, weight.data_ptr(),
@@ -203,9 +206,12 @@ def layer_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor,
     if mean is not None:
         _vector(mean, lead, _F32, dy, "mean")
     rows, wtype = rstd.numel(), weight.dtype
-    dx = _out(dx, shape, dtype, dy)
-    dweight = _out(dweight, shape[-1:], wtype, weight)
-    dbias = _out(dbias, shape[-1:], wtype, weight) if bias else None
+    dx = torch.empty_like(dy) if dx is None else _out(dx, shape, dtype, dy)
+    dweight = torch.empty_like(weight) if dweight is None else _out(dweight, shape[-1:], wtype, dy)
+    if bias:
+        dbias = torch.empty_like(weight) if dbias is None else _out(dbias, shape[-1:], wtype, dy)
+    else:
+        dbias = None
     ws = _work(workspace, lib().nvfp4_layernorm_backward_workspace(rows, cols), dy)
     _call("nvfp4_layernorm_backward", dy, dy.data_ptr(), h.data_ptr(), weight.data_ptr(), _ptr(mean),
           rstd.data_ptr(), _ptr(dres), rows, cols, kind, TYPES[wtype], dx.data_ptr(),
@@ -228,7 +234,9 @@ def distill_loss(student: torch.Tensor, teacher: torch.Tensor, weight: torch.Ten
     ts = _rows(teacher, shape, "teacher")
     if weight is not None:
         _vector(weight, lead, _F32, student, "weight")
-    loss = _out(loss, lead, torch.float32, student if weight is None else weight)
+    if loss is None and weight is not None:
+        loss = torch.empty_like(weight)
+    loss = _out(loss, lead, torch.float32, student)
     gs = vocab
     if grad is not None:
         if not want_grad:
@@ -236,7 +244,7 @@ def distill_loss(student: torch.Tensor, teacher: torch.Tensor, weight: torch.Ten
         _like(grad, shape, (student.dtype,), student, "grad")
         gs = _rows(grad, shape, "grad")
     elif want_grad:
-        grad = _out(None, shape, student.dtype, student)
+        grad = torch.empty_like(student) if ss == vocab else _out(None, shape, student.dtype, student)
     rows = loss.numel()
     need = lib().nvfp4_distill_loss_workspace(rows, vocab)
     ws = _work(workspace, need, student) if need else None
