@@ -236,7 +236,8 @@ def distill_loss(student: torch.Tensor, teacher: torch.Tensor, weight: torch.Ten
         _vector(weight, lead, _F32, student, "weight")
     if loss is None and weight is not None:
         loss = torch.empty_like(weight)
-    loss = _out(loss, lead, torch.float32, student)
+    else:
+        loss = _out(loss, lead, torch.float32, student)
     gs = vocab
     if grad is not None:
         if not want_grad:
