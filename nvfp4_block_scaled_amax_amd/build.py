@@ -38,10 +38,15 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found (ROCm is required to build the HIP library)")
 
 
-def flags() -> list:
+def compile_flags() -> list:
     return ["--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC",
             "-ffp-contract=off", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
             "-fvisibility=hidden", "-Wall", "-I" + INCLUDE]
+
+
+def flags() -> list:
+    """To compile and link a library of one source."""
+    return compile_flags() + ["-shared"]
 
 
 def scratch_users(report: str) -> list:
@@ -59,7 +64,7 @@ def scratch_users(report: str) -> list:
 
 def compile_source(src: str, obj: str) -> tuple:
     """hipcc -c of one source: (its command, its return code, its output lines)."""
-    cmd = [hipcc()] + flags() + ["-Rpass-analysis=kernel-resource-usage", "-c", "-o", obj, src]
+    cmd = [hipcc()] + compile_flags() + ["-Rpass-analysis=kernel-resource-usage", "-c", "-o", obj, src]
     res = subprocess.run(cmd, capture_output=True, text=True)
     return cmd, res.returncode, (res.stdout + res.stderr).splitlines()
 

@@ -214,3 +214,15 @@ def test_c_program_compiles_links_and_runs(tmp_path, L):
     r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0, r.stdout + r.stderr
     assert "c consumer ok" in r.stdout
+
+
+def test_a_library_of_one_source_links():
+    """flags() compile and link a shared library by themselves (tests/hw is built with them)."""
+    import tempfile
+    from nvfp4_block_scaled_amax_amd import build
+    with tempfile.TemporaryDirectory() as work:
+        src, lib = os.path.join(work, "one.hip"), os.path.join(work, "one.so")
+        with open(src, "w") as f:
+            f.write('extern "C" __attribute__((visibility("default"))) int one() { return 1; }\n')
+        subprocess.run([build.hipcc()] + build.flags() + ["-o", lib, src], check=True, capture_output=True)
+        assert ctypes.CDLL(lib).one() == 1
