@@ -3,8 +3,8 @@
 // Both directions move bytes and little else: the forward pass reads x (and the residual) and
 // writes y (and h) once, the backward pass reads dy and h (and dres) and writes dx once.  So a row
 // is held in registers while its sums are made: up to 512 columns by 16, 32 or 64 lanes of a
-// wavefront, eight elements each; up to 16384 by one workgroup of as many wavefronts as the row
-// fills.  The variance is the mean square of what is held less the mean (not E[x^2] - mean^2, which
+// wavefront, eight elements each (in the backward pass up to 1024 of bf16, sixteen each); up to
+// 16384 by one workgroup of as many wavefronts as the row fills.  The variance is the mean square of what is held less the mean (not E[x^2] - mean^2, which
 // cancels).  Longer rows are read again for each step.  The backward pass keeps, next to the row, its
 // share of the column sums (dweight, dbias) in registers over all the rows that a workgroup
 // takes, leaves them as one partial row per workgroup in the workspace, and a second launch adds
@@ -97,10 +97,10 @@ __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v
 // y = (h - mean) rstd weight + bias.  Rows of up to 512 columns take a wavefront each, those of up
 // to 256 and 128 a half and a quarter of one (LANES; 262144 x 128 bf16 26.8 us, 52.4 with a wavefront
 // each); longer ones a workgroup (LANES == 0).  A lane holds K vectors, and where that is eight
-// elements (HOLD) also its weights for all the rows that it comes by (8192 x 4097 bf16 83 us, 100
-// if they are read for each; 8192 x 4096 f32 47.5 and 51.2).  Rows of bf16 that fill the workgroup,
-// without a residual, are an exception that only the measurement explains: 26.9 us for
-// 8192 x 4096 with the weights held, 23.3 without.
+// elements (HOLD) also its weights for all the rows that it comes by (bf16, 8192 x 4097 30.5 us, 41.0 if
+// they are read for each; 8192 x 4104 with residual 49.9 and 57.0; f32 the same).  Rows of bf16 that
+// fill the workgroup, without a residual, are an exception that only the measurement explains:
+// 8192 x 4096 27.4 us with the weights held, 24.1 without, 4096 x 8192 27.1 and 22.9.
 //
 // The memory bounds it: 8192 x 4096 bf16 with residual and h 49.5 us (268 MB, 5.4 TB/s; a copy of
 // that size 5.4), without 23.3 (134 MB, half of it in the last-level cache), f32 47.5; 65536 x 512
