@@ -255,14 +255,39 @@ def distill_loss(student: torch.Tensor, teacher: torch.Tensor, weight: torch.Ten
     return loss, grad
 
 
+class _Seen:
+    """Tensors that were checked, to be recognized at the next step: the same sizes, strides, types and
+    devices in the same order.  (An address does not tell: a view of a tensor, and what is put into its
+    freed memory, begin where it did.)  torch compares a whole list in one call, 3 us for 72 tensors, where
+    their attributes take 11 one by one; what it does not recognize is checked again in full."""
+
+    def __init__(self):
+        self._guards = None
+
+    def keep(self, tensors) -> None:
+        try:
+            self._guards = torch._C._dynamo.guards.TensorGuards(
+                *tensors, dynamic_dims_sizes=[list(t.shape) for t in tensors],
+                dynamic_dims_strides=[list(t.stride()) for t in tensors])
+        except (AttributeError, TypeError):         # not in this torch, or not for these tensors
+            self._guards = None
+
+    def again(self, tensors) -> bool:
+        try:
+            return self._guards is not None and self._guards.check(*tensors)
+        except TypeError:                           # another number of them
+            return False
+
+
 class AdamWPlan:
     """Parameters and their optimizer state, checked once: what adamw_step updates in place.
 
     params, master, exp_avg, exp_avg_sq, avg_scale, sq_scale are lists of tensors (None for a
     kind that is not there); a checkpoint saves and restores their contents.  With 8-bit states
     exp_avg holds E4M3 codes of m / avg_scale and exp_avg_sq those of sqrt(v) / sq_scale, one
-    scale per 128 elements.  The tensors' addresses are read at each step, so `p.data = ...` is
-    noticed, and refused where the number, the sizes or the types are no longer the plan's."""
+    scale per 128 elements.  The tensors are looked at again at each step, so `p.data = ...` is
+    noticed, and refused where the number, the sizes, the types or the device are no longer the plan's
+    or a tensor is not contiguous."""
 
     KINDS = ("params", "exp_avg", "exp_avg_sq", "master", "avg_scale", "sq_scale")
 
@@ -285,7 +310,8 @@ class AdamWPlan:
         # nvfp4_adamw_tensor, an entry a row
         self._table = np.zeros((len(params), 8), np.int64)
         self._table[:, 7] = self.numels
-        self._at = {}                   # the addresses in it: tensors that are elsewhere are checked
+        self._at = {}                   # the addresses in it
+        self._seen, self._seen_grads = _Seen(), _Seen()
         self._columns = [(k, kind, sizes, dtype) for k, kind, sizes, dtype in (
             (0, "params", self.numels, self.dtype), (2, "exp_avg", self.numels, state),
             (3, "exp_avg_sq", self.numels, state), (4, "master", self.numels, torch.float32),
@@ -303,15 +329,30 @@ class AdamWPlan:
                              % (kind, numel, tuple(t.shape)))
 
     def _fill(self):
-        for k, kind, sizes, dtype in self._columns:
-            tensors = getattr(self, kind)
-            now = [t.data_ptr() for t in tensors]
-            if now != self._at.get(k):
+        lists = [getattr(self, kind) for _, kind, _, _ in self._columns]
+        flat = [t for tensors in lists for t in tensors]
+        alike = all(len(tensors) == len(self.numels) for tensors in lists)
+        if not (alike and self._seen.again(flat)):
+            for (_, kind, sizes, dtype), tensors in zip(self._columns, lists):
                 if len(tensors) != len(sizes):
                     raise ValueError("%s: %d tensors for %d parameters" % (kind, len(tensors), len(sizes)))
                 for t, n in zip(tensors, sizes):
                     self._look(kind, t, n, dtype)
+            self._seen.keep(flat)
+        for (k, _, _, _), tensors in zip(self._columns, lists):
+            now = [t.data_ptr() for t in tensors]
+            if now != self._at.get(k):
                 self._table[:, k] = self._at[k] = now
+
+    def _look_grads(self, grads) -> int:
+        """The gradients' type, all of them checked."""
+        gtype = grads[0].dtype
+        kind = _type(grads[0], "gradients")
+        if not self._seen_grads.again(grads):
+            for g, n in zip(grads, self.numels):
+                self._look("grads", g, n, gtype)
+            self._seen_grads.keep(grads)
+        return kind
 
     def table(self, grads) -> np.ndarray:
         """The entries of nvfp4_adamw_tensor for these gradients."""
@@ -367,12 +408,7 @@ def adamw_step(plan: AdamWPlan, grads, *, step: int, lr: float, betas=(0.9, 0.99
     grads = list(grads)
     if len(grads) != len(plan.params):
         raise ValueError("%d gradients for %d parameters" % (len(grads), len(plan.params)))
-    gtype = grads[0].dtype
-    kind = _type(grads[0], "gradients")
-    dev = plan.device.index
-    for g, n in zip(grads, plan.numels):
-        if g.dtype != gtype or g.get_device() != dev or g.numel() != n or not g.is_contiguous():
-            plan._look("grads", g, n, gtype)          # says which
+    kind = plan._look_grads(grads)
     like = plan.params[0]
     if grad_scale is not None:
         _vector(grad_scale, (1,), _F32, like, "grad_scale")

@@ -525,3 +525,45 @@ def test_a_tensor_past_32_bits(nv):
     nv.adamw_step(nv.adamw_plan([alone], state="e4m3"), [grad], **args)
     assert not torch.equal(tail, alone) and not torch.equal(p[:size], tail)
     assert torch.equal(p[:first[0]], alone[:first[0]])
+
+
+def test_parameters_that_changed_where_they_are(nv):
+    """A view of a tensor at its own address, of another size, order or type, is refused for every kind
+    of tensor, as are such gradients; the step leaves everything as it was."""
+    for ptype, state, master in ((F, "f32", None), (BF, "f32", True), (BF, "e4m3", None)):
+        params = [torch.nn.Parameter(torch.ones(40, 40, device="cuda", dtype=ptype)) for _ in range(3)]
+        plan = nv.adamw_plan(params, state=state, master=master)
+        grads = [torch.ones(40, 40, device="cuda") for _ in params]
+        nv.adamw_step(plan, grads, step=1, lr=0.5)
+        lists = {k: getattr(plan, k) for k in plan.KINDS if getattr(plan, k) is not None}
+        was = [t.detach().clone() for v in lists.values() for t in v]
+        for kind, tensors in {**lists, "grads": grads}.items():
+            whole = tensors[1].data
+            others = [(whole[:2] if whole.dim() > 1 else whole[:5], ValueError)]
+            if whole.dim() > 1:
+                others.append((whole.t(), ValueError))
+            half = whole.view(torch.float16 if whole.dtype != E8 else torch.uint8).flatten()[:whole.numel()]
+            others.append((half.view(whole.shape), TypeError))
+            for other, error in others:
+                assert other.data_ptr() == whole.data_ptr()
+                if kind == "params" and other.dtype == whole.dtype:
+                    tensors[1].data = other
+                else:
+                    keep = tensors[1]
+                    tensors[1] = other
+                for _ in range(2):
+                    with pytest.raises(error, match=kind):
+                        nv.adamw_step(plan, grads, step=2, lr=0.5)
+                if kind == "params" and other.dtype == whole.dtype:
+                    tensors[1].data = whole
+                else:
+                    tensors[1] = keep
+        torch.cuda.synchronize()
+        assert all(torch.equal(t.view(torch.uint8), w.view(torch.uint8))
+                   for t, w in zip((t.detach() for v in lists.values() for t in v), was))
+        # what is alike but elsewhere, or of another shape, is taken
+        params[1].data = params[1].data.clone().view(1600)
+        params[2].data = params[2].data.view(20, 80)
+        nv.adamw_step(plan, grads, step=2, lr=0.5)
+        assert torch.equal(params[0].view(-1), params[1]) and torch.equal(params[0].view(-1), params[2].view(-1)) \
+            or (ptype == BF and master is None)

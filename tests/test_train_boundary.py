@@ -226,3 +226,80 @@ def test_a_library_of_one_source_links():
             f.write('extern "C" __attribute__((visibility("default"))) int one() { return 1; }\n')
         subprocess.run([build.hipcc()] + build.flags() + ["-o", lib, src], check=True, capture_output=True)
         assert ctypes.CDLL(lib).one() == 1
+
+
+class OnTheGpu:
+    """What an AdamWPlan looks at of a GPU tensor."""
+
+    def __init__(self, numel, dtype=torch.float32, at=A, contiguous=True, device=0):
+        self.dtype, self.shape, self.is_cuda = dtype, (numel,), device >= 0
+        self.device = torch.device("cuda", device) if device >= 0 else torch.device("cpu")
+        self._numel, self._at, self._contiguous = numel, at, contiguous
+
+    def numel(self):
+        return self._numel
+
+    def data_ptr(self):
+        return self._at
+
+    def is_contiguous(self):
+        return self._contiguous
+
+    def get_device(self):
+        return self.device.index if self.is_cuda else -1
+
+
+PLAN = {"params": (torch.bfloat16, 1600), "exp_avg": (torch.float8_e4m3fn, 1600),
+        "exp_avg_sq": (torch.float8_e4m3fn, 1600), "master": (torch.float32, 1600),
+        "avg_scale": (torch.float32, 13), "sq_scale": (torch.float32, 13)}
+
+
+@pytest.mark.parametrize("change,error", [
+    (dict(numel=12), ValueError), (dict(numel=3000), ValueError), (dict(dtype=torch.float16), TypeError),
+    (dict(contiguous=False), ValueError), (dict(device=1), ValueError), (dict(device=-1), ValueError)])
+@pytest.mark.parametrize("kind", list(PLAN))
+def test_a_plan_refuses_tensors_that_changed_where_they_are(kind, change, error):
+    """A tensor of another size, type, order or device at the address that the plan knows (a view of
+    it; memory that was freed and taken again) is refused at the next step, before anything is
+    enqueued; one that is the same but for its address is taken."""
+    lists = {k: [OnTheGpu(n, dtype, B + 0x100000 * i + 0x10000 * j) for j in range(3)]
+             for i, (k, (dtype, n)) in enumerate(PLAN.items())}
+    plan = train.AdamWPlan(**lists)
+    grads = [OnTheGpu(1600, torch.bfloat16, G + 0x10000 * j) for j in range(3)]
+    table = plan.table(grads).copy()
+    assert (table == plan.table(grads)).all()
+    dtype, n = PLAN[kind]
+    held = lists[kind][1]
+    lists[kind][1] = OnTheGpu(**{**dict(numel=n, dtype=dtype, at=held.data_ptr()), **change})
+    for _ in range(2):
+        with pytest.raises(error, match=kind):
+            plan.table(grads)
+    lists[kind][1] = OnTheGpu(n, dtype, H)
+    again = plan.table(grads)
+    assert (again != table).sum() == 1 and (again[1] == H).sum() == 1
+    lists[kind][1] = held
+    assert (plan.table(grads) == table).all()
+
+
+def test_tensors_are_recognized_by_more_than_their_addresses():
+    """What was checked once is recognized, also elsewhere in memory; a view of it at the same address
+    with another size, order or type is not, nor is another number of tensors."""
+    seen = train._Seen()
+    ts = [torch.zeros(40, 40), torch.nn.Parameter(torch.zeros(300)), torch.zeros(7, dtype=torch.bfloat16)]
+    assert not seen.again(ts)
+    seen.keep(ts)
+    assert seen.again(ts)
+    whole = ts[0].data
+    ts[0].data = whole.clone()
+    assert seen.again(ts)
+    for other in (whole.t(), whole[:2], whole.view(torch.int32), whole.view(torch.bfloat16)[:, :40],
+                  whole.as_strided((40, 40), (1, 1)), whole.to("meta")):
+        assert not seen.again([other] + ts[1:])
+    ts[0].data = whole.t()                    # the same object
+    assert not seen.again(ts)
+    ts[0].data = whole
+    assert not seen.again(ts[:2]) and not seen.again(ts + ts[:1]) and not seen.again(ts[:2] + [None])
+    with torch.no_grad():
+        assert seen.again(ts)
+    seen.keep([object()])                     # nothing that can be compared: never recognized
+    assert not seen.again([object()])
