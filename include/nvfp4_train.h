@@ -106,8 +106,7 @@ nvfp4_status nvfp4_distill_loss(const void* student, int64_t student_stride, con
                                 void* workspace, hipStream_t stream);
 
 /* One AdamW step over many tensors, in place.  Per element, in binary32 with one rounding per
- * operation as written (the quotient within 2 ulp where its divisor is within 2^-126 .. 2^126; with
- * 8-bit states sqrt(v) within 1 ulp where 0 < v < 2^-96):
+ * operation as written (the quotient within 2 ulp where its divisor is within 2^-126 .. 2^126):
  *   g = grad * grad_scale[0]                  (grad_scale: device float, NULL = no factor)
  *   m = m * beta1 + g * (1 - beta1)
  *   v = v * beta2 + (g * g) * (1 - beta2)
@@ -119,7 +118,7 @@ nvfp4_status nvfp4_distill_loss(const void* student, int64_t student_stride, con
  * States: float; or 8 bits, per block of NVFP4_ADAMW_BLOCK consecutive elements of the tensor
  * one float scale = max / 448 and E4M3 codes of m / scale and sqrt(v) / scale.  Codes are rounded
  * stochastically (round-to-nearest would hold v still: beta2 near 1 moves it by less than half
- * a step); sqrt(v) > 0 never becomes 0.  The update of p uses m and v before that rounding.  A block
+ * a step); sqrt(v) > 0 never becomes 0, and an m whose block stays below 2^-100 does.  The update of p uses m and v before that rounding.  A block
  * with a non-finite value reads back as non-finite.
  * Stochastic rounding adds random bits below the kept ones and truncates.  The bits are
  * hash32(element + key) with key = hash32(hash32(hash32(seed) ^ step) ^ tensor index), see

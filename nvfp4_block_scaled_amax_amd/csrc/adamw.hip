@@ -51,15 +51,33 @@ __device__ __forceinline__ float round_e4m3(float y, uint32_t bits) {
   return cut - up;
 }
 
-// sqrt(v), rounded to nearest for 0, inf and v >= 2^-96 (below, where a residual underflows, it may be the
-// neighbour): the hardware's root is within one step, and the residual of the value below and
-// above it tells.  (A NaN residual, of 0 and inf, tells nothing and changes nothing.)
+// sqrt(v) rounded to nearest, for v = 0, inf and v >= 2^-96.  The hardware's root is within one step, and the
+// sign of v - s' s tells on which side of the midpoint between a neighbour s' and s the root lies (Tuckerman's
+// test: Agarwal et al., "New scalar and vector elementary functions for the IBM System/370", 1986).  With
+// s >= 2^-48 the residual is a multiple of 2^-142, so that no sign is lost.  (That of 0 and inf is NaN,
+// tells nothing and changes nothing.)
 __device__ __forceinline__ float root(float v) {
   const float s = __builtin_amdgcn_sqrtf(v);
   const float below = __uint_as_float(__float_as_uint(s) - 1u);
   const float above = __uint_as_float(__float_as_uint(s) + 1u);
   const float r = fmaf(-below, s, v) <= 0.0f ? below : s;
   return fmaf(-above, s, v) > 0.0f ? above : r;
+}
+
+// The same for every v.  The hardware takes a subnormal v for 0; what is below 2^-96 is taken 2^96
+// times, which is exact, in a branch that ordinary second moments do not enter.
+__device__ __forceinline__ void roots(const float (&v)[8], float (&r)[8]) {
+  float least = v[0];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    r[i] = root(v[i]);
+    least = fminf(least, v[i]);
+  }
+  if (least < 0x1p-96f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (v[i] > 0.0f && v[i] < 0x1p-96f) r[i] = root(v[i] * 0x1p96f) * 0x1p-48f;
+  }
 }
 
 // Eight values over 16 lanes to a block scale and eight E4M3 bytes.
@@ -75,12 +93,12 @@ __device__ __forceinline__ u32x2 encode(const float (&x)[8], const uint32_t (&bi
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float s = x[i] * inv;
-    // at the most 448; and for the root, which is divided by, at the least 2^-9 where it is not 0
-    // (the smallest root of all times 2^120 / 448 is far above 448, so that the median is of
-    // 2^-9 and 448, or of 2^-9 and 0)
+    // at the most 448; and for the root, which is divided by, at the least 2^-9 where it is not 0: the
+    // median with 2^-9 and a bound that is 0 for 0, else above 2^-9 and s rounded up (the smallest
+    // root of all, 2^-74.5, over the largest, 2^64, is s = 2^-129.7, and 2^127 times that 2^-2.7)
     if (POSITIVE)
       y[i] = __builtin_amdgcn_fmed3f(round_e4m3(s, bits[i] >> 12), 0.001953125f,
-                                     fminf(s * 0x1p120f, 448.0f));
+                                     fminf(s * 0x1p127f, 448.0f));
     else
       y[i] = copysignf(fminf(round_e4m3(fabsf(s), bits[i] & 0xFFFFFu), 448.0f), s);
   }
@@ -189,9 +207,12 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const Batch a) {
       const float sq = E4M3 ? v[i] * v[i] : v[i];
       m[i] = m[i] * a.beta1 + g * a.rest1;
       v[i] = sq * a.beta2 + (g * g) * a.rest2;
-      low[i] = E4M3 ? root(v[i]) : sqrtf(v[i]);
-      p[i] = p[i] * a.keep - (m[i] * __builtin_amdgcn_rcpf(low[i] * a.root + a.eps)) * a.rate;
+      if (!E4M3) low[i] = sqrtf(v[i]);
     }
+    if (E4M3) roots(v, low);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      p[i] = p[i] * a.keep - (m[i] * __builtin_amdgcn_rcpf(low[i] * a.root + a.eps)) * a.rate;
     if (E4M3) {
       float ms, vs;
       const u32x2 mc = encode<false>(m, bits, ms), vc = encode<true>(low, bits, vs);

@@ -567,3 +567,84 @@ def test_parameters_that_changed_where_they_are(nv):
         nv.adamw_step(plan, grads, step=2, lr=0.5)
         assert torch.equal(params[0].view(-1), params[1]) and torch.equal(params[0].view(-1), params[2].view(-1)) \
             or (ptype == BF and master is None)
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-8])
+@pytest.mark.parametrize("ptype,master", KINDS, ids=["f32", "master", "bf16"])
+def test_second_moments_below_the_normal_numbers(nv, ptype, master, eps):
+    """8-bit states, gradients whose squares are subnormal: blocks of such gradients alone, and beside
+    ordinary ones, and beside one whose square is infinite (its block reads back as not finite).  sqrt(v),
+    the scales and the codes bit for bit as numpy has them, no code of a v > 0 is 0, and the update is
+    the one of binary32 (tolerance as in test_bits)."""
+    t, seed, f = 1, 77, np.float32
+    lr, (b1, b2), wd = ARGS["lr"], ARGS["betas"], ARGS["weight_decay"]
+    gen = torch.Generator("cuda").manual_seed(12)
+    sizes = (1e-18, 3e-20, 5e-21)
+    grads = []
+    for alone in sizes:                    # a tensor for each size: alone, beside 1, beside 4e20, a cut block
+        r = torch.randn(4 * BLOCK + 37, generator=gen, device="cuda", dtype=torch.float64)
+        g = alone * r.sign() * (1 + r.abs())
+        g[BLOCK + 5], g[2 * BLOCK + 9], g[4 * BLOCK:4 * BLOCK + 3] = 1.0, 4e20, 0.0
+        grads.append(g.float())
+    params = [(0.05 * torch.randn(g.numel(), generator=gen, device="cuda")).to(ptype) for g in grads]
+    old = [p.clone() for p in params]
+    plan = nv.adamw_plan(params, state="e4m3", master=True if master else None)
+    nv.adamw_step(plan, grads, step=t, seed=seed, eps=eps, lr=lr, betas=(b1, b2), weight_decay=wd)
+    key = mix(mix(np.uint32(seed)) ^ np.uint32(t))
+    host = lambda x: x.float().cpu().numpy()
+    for k, g in enumerate(map(host, grads)):
+        n = g.size
+        with np.errstate(over="ignore"):
+            m, v = g * f(1 - b1), (g * g) * f(1 - b2)
+        low = np.sqrt(v)
+        assert ((v > 0) == (g != 0)).all() and (v[v > 0].min() < 2.0 ** -126)
+        p0 = host(old[k])
+        with np.errstate(invalid="ignore", divide="ignore"):
+            p = p0 * f(1 - lr * wd) - (m / (low * f(1 / math.sqrt(1 - b2 ** t)) + f(eps))) * f(lr / (1 - b1 ** t))
+        with np.errstate(over="ignore"):
+            bits = mix(np.arange(n, dtype=np.uint32) + mix(key ^ np.uint32(k)))
+        for x, r, codes, scales, positive in (
+                (m, bits & np.uint32(0xFFFFF), plan.exp_avg[k], plan.avg_scale[k], False),
+                (low, bits >> np.uint32(12), plan.exp_avg_sq[k], plan.sq_scale[k], True)):
+            finite = np.ones(n, bool)
+            if positive:
+                finite[2 * BLOCK:3 * BLOCK] = False
+                assert not torch.isfinite(f64(codes, scales)[2 * BLOCK:3 * BLOCK]).any()
+                x = np.where(finite, x, f(1))
+            scale = np.abs(np.pad(x, (0, -n % BLOCK)).reshape(-1, BLOCK)).max(1) * f(1 / 448)
+            held = np.append(finite[::BLOCK][:n // BLOCK], True)
+            assert np.array_equal(host(scales)[held].view(np.uint32), scale[held].view(np.uint32)), (k, positive)
+            y = x * np.repeat(f(1) / scale, BLOCK)[:n]
+            want = np.copysign(e4m3_cut(np.abs(y), r), y)
+            if positive:
+                want = np.where(x > 0, np.maximum(want, f(2.0 ** -9)), want)
+                assert ((host(codes) > 0) == (v > 0))[finite].all()
+            assert np.array_equal(host(codes)[finite], want[finite]), (k, positive)
+        got = host((plan.master or params)[k])
+        live = g != 0 if eps == 0 else np.ones(n, bool)               # 0 / 0 where the gradient is 0
+        off = 2.0 ** -22 * np.abs(p - p0) + 2.0 ** -23 * np.abs(p)
+        if ptype == BF and not master:                               # one of the two bf16 neighbours
+            off = off + 2.0 ** -7 * np.abs(p) + 2.0 ** -133
+        assert (np.abs(got.astype(np.float64) - p)[live] <= off[live]).all(), k
+        assert np.isnan(got[~live]).all()
+
+
+def test_second_moments_beside_the_largest(nv):
+    """The smallest and the largest roots of a block: codes of 2^-9 and 448, and a scale between."""
+    g = torch.full((2 * BLOCK,), 1.8e19, device="cuda")
+    g[1::2], g[BLOCK:] = 1.3e-21, 0.0
+    g[BLOCK + 3] = 1.3e-21
+    v = (g * g) * np.float32(1 - 0.999)
+    assert v[1].item() == 2.0 ** -149
+    for seed in range(4):
+        plan = nv.adamw_plan([torch.zeros(2 * BLOCK, device="cuda")], state="e4m3")
+        nv.adamw_step(plan, [g], step=1, lr=0.125, eps=0.0, weight_decay=0.0, seed=seed)
+        codes = plan.exp_avg_sq[0].float()
+        assert (codes[:BLOCK:2] == 448).all() and (codes[1:BLOCK:2] == 2.0 ** -9).all()
+        assert codes[BLOCK + 3] == 448 and (codes[BLOCK:] > 0).sum() == 1
+        assert plan.sq_scale[0][1].item() == np.float32(2.0 ** -74.5) * np.float32(1 / 448)
+        # m / sqrt(v) with the root of the binary32 v: within 2 ulp of 0.1 g / sqrt(v), corrected
+        live = g != 0
+        p = plan.params[0][live].double()
+        want = -0.125 * (g * np.float32(0.1))[live].double() / v[live].double().sqrt() * math.sqrt(1 - 0.999) / (1 - 0.9)
+        assert ((p - want).abs() <= 2.0 ** -20 * want.abs()).all()
