@@ -88,7 +88,8 @@ nvfp4_status nvfp4_layernorm_backward(const void* dy, const void* h, const void*
  * near its teacher keeps its relative precision.
  *   - A row of weight 0 is not read: loss 0, gradient 0, whatever its logits hold.
  *   - Entries of -inf have probability 0.  p_j = 0 contributes nothing, also where q_j = 0;
- *     p_j > 0 = q_j makes the loss +inf.
+ *     p_j > 0 where the student is -inf makes the loss +inf.  Where the student is a finite value far
+ *     below (the type's lowest) log q_j is that value's, though q_j comes out as 0.
  *   - A row with a NaN, a +inf, or no entry above -inf (in teacher or student) has no
  *     distribution: its loss and its whole gradient are NaN.
  * student, teacher [rows][vocab] of `stype`, `ttype` with row strides in elements (>= vocab);

@@ -259,6 +259,15 @@ __device__ __forceinline__ Exact row_exact(const S* s, uint32_t lo, uint32_t hi,
   return e;
 }
 
+// An entry that the student excludes by a finite value (the type's lowest, -1e36): from X - Y = kFar on,
+// Zp p (X - Y) may overflow where the loss does not, and Y itself does.  There p (log p - log q) is -p s / T,
+// infinite where s is: the rest of X - Y is no part of it in 32 bits.  The sum of the loss is kept
+// kDown times, where Zp p is below 1.
+constexpr float kFar = 0x1p100f, kDown = 0x1p-64f;
+__device__ __forceinline__ float far_part(float ep, float c, float s) {
+  return ep * (c * kLn2) * (-s * kDown);
+}
+
 // The second pass: writes the gradient, returns the workgroup's part of the loss (with the row's
 // weight) to every thread.
 template <int THREADS, typename S, typename R>
@@ -283,14 +292,23 @@ __device__ __forceinline__ float row_grad(R& row, void* lds, S* grad, float c, f
           x[i] = fmaf(b[i], c, -p.r);
           least = fminf(least, fminf(x[i], y[i]));
         }
-        if (least == -INFINITY) {     // log2 p - log2 q counts where p is not 0
+        if (least < -kFar) {          // log2 p - log2 q counts where p is not 0
+          bool far = false;
 #pragma unroll
           for (int i = 0; i < N; ++i) {
             const float eq = exp2_(y[i]), ep = exp2_(x[i]), d = fmaf(eq, back, -ep);
-            bent += ep == 0.0f ? 0.0f : ep * (x[i] - y[i]);
+            const float gap = x[i] - y[i];
+            far |= gap > kFar && ep != 0.0f;
+            bent += ep == 0.0f || gap > kFar ? 0.0f : ep * gap;
             flat += d;
             g[i] = d * scale;
           }
+          if (far)            // seldom: read again (not yet written over), there are no registers for them
+#pragma unroll 1
+            for (int i = 0; i < N; ++i) {
+              const float s = to_f32(row.s[at + i]), x = fmaf(to_f32(row.t[at + i]), c, -p.r);
+              if (exp2_(x) != 0.0f && x - fmaf(s, c, -r) > kFar) sum += far_part(exp2_(x), c, s);
+            }
         } else {
 #pragma unroll
           for (int i = 0; i < N; ++i) {
@@ -300,18 +318,20 @@ __device__ __forceinline__ float row_grad(R& row, void* lds, S* grad, float c, f
             g[i] = d * scale;
           }
         }
-        sum += fmaf(kLn2, bent, flat);
+        sum = fmaf(kDown, fmaf(kLn2, bent, flat), sum);
         if (grad) store_vec<true>(grad + at, make_vec<S>(g));
       },
       [&](uint32_t at, float a, float b) {
         const float y = fmaf(a, c, -r), x = fmaf(b, c, -p.r);
         const float eq = exp2_(y), ep = exp2_(x), d = fmaf(eq, back, -ep);
-        sum += fmaf(kLn2, ep == 0.0f ? 0.0f : ep * (x - y), d);
+        const float gap = x - y;
+        if (ep != 0.0f && gap > kFar) sum += far_part(ep, c, a);
+        sum = fmaf(kDown, fmaf(kLn2, ep == 0.0f || gap > kFar ? 0.0f : ep * gap, d), sum);
         if (grad) grad[at] = from_f32<S>(d * scale);
       });
   // What is missing: log2 p - log2 q is X - Y + off, and `back` is rounded.  The p and the q add up
   // to 1 each, so that is ln 2 off + (2^-off - back) = 1 - back.
-  const float all = reduce_group<THREADS / 64>(weight * (sum / p.z), Sum(), slots);
+  const float all = reduce_group<THREADS / 64>(weight * (sum / (p.z * kDown)), Sum(), slots);
   return row.lo == 0 ? fmaf(weight, 1.0f - back, all) : all;
 }
 
@@ -325,8 +345,10 @@ __device__ __forceinline__ float row_grad_exact(const S* s, const T* t, S* grad,
 #pragma unroll 1
   for (uint32_t at = lo + threadIdx.x; at < hi; at += THREADS) {
     const float y = (to_f32(s[at]) - q.m) * c - lq, x = (to_f32(t[at]) - p.m) * c - lp;
-    const float eq = exp2_(y), ep = exp2_(x);
-    sum += (eq - ep) + (ep == 0.0f ? 0.0f : kLn2 * ep * (x - y));
+    const float eq = exp2_(y), ep = exp2_(x), b = to_f32(s[at]);
+    // (top - s in halves: it may be up to twice the largest number)
+    const float bent = y < -kFar ? ep * (0.5f * q.m - 0.5f * b) * (c * kLn2) * 2.0f : kLn2 * ep * (x - y);
+    sum += (eq - ep) + (ep == 0.0f ? 0.0f : bent);
     if (grad) grad[at] = from_f32<S>((eq - ep) * scale);
   }
   return reduce_group<THREADS / 64>(weight * sum, Sum(), slots);

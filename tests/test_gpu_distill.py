@@ -357,3 +357,47 @@ def test_short_rows(nv, vocab, S, T):
     again, same = nv.distill_loss(view, t, w, temperature=1.5, grad=view)
     assert torch.equal(again, loss) and torch.equal(same, grad)
     assert not buf[vocab + 1::vocab + 1].any() and buf[0] == 0
+
+
+@pytest.mark.parametrize("rows,vocab", [(3, 7), (260, 3001), (3, 40000), (130, 60001)])
+def test_a_student_masked_by_a_finite_value(nv, rows, vocab):
+    """The student excludes, by the type's lowest value or another far below all, an entry that the
+    teacher expects: the loss is p (top - mask) / T, a number, not infinity.  Its other parts are no
+    part of it in 32 bits, so it is off by the error of p (in the header) and 8 roundings."""
+    gen = torch.Generator("cuda").manual_seed(5)
+    for S, T in ((BF, BF), (F, F), (BF, F), (F, BF)):
+        for size, temp, mask in ((2.5, 1.0, None), (2.5, 2.0, None), (2.5, 0.7, None), (2.5, 1.0, -1e36),
+                                 (2.5, 0.01, -1e36), (1e6, 3.0, None), (1e37, 3.0, None)):
+            say("[distill] finite mask", rows, vocab, S, T, size, temp, mask)
+            s, t = logits(rows, vocab, S, T, size=size, near=0.3 * size)
+            top = t.double().amax(1, keepdim=True)
+            p = torch.softmax((t.double() - top) / temp, 1)
+            # expected by the teacher with at most a quarter: no loss passes the largest number
+            at = torch.where(p <= 0.25, p, -1.0).argmax(1)
+            each = torch.arange(rows, device="cuda")
+            if rows > 100:                        # not the rows of even number: they stay as they are
+                each, at = each[1::2], at[1::2]
+            clean = s.clone()
+            s[each, at] = torch.finfo(S).min if mask is None else mask
+            w = torch.rand(rows, generator=gen, device="cuda") + 0.1
+            want, want_grad, tol, tol_grad = reference(s, t, w, temp)
+            d = (s.double().amax(1)[each] - s.double()[each, at]) / temp
+            main = w.double()[each] * p[each, at] * d
+            far = (top[each, 0] - t.double()[each, at]) / temp / math.log(2)
+            logz = torch.log2(torch.exp((t.double() - top) / temp).sum(1))[each]
+            steps = 16 * -(-vocab // 8192) + 64
+            rel = U * (4 + steps + 3 * (far + logz)) + 8 * U
+            loss, grad = nv.distill_loss(s, t, w, temperature=temp)
+            sure = p[each, at] > 2.0 ** -100              # where the teacher's probability is a number
+            off = (loss.double()[each] - main).abs() / main.clamp(min=1e-300)
+            # what is left out of `main`: the rest of the loss
+            rest = (want[each] - main).abs() / main.clamp(min=1e-300)
+            assert (off <= rel + rest)[sure].all(), float((off / (rel + rest))[sure].max())
+            ok = (grad.double() - want_grad).abs() <= (tol_grad * (1 + HALF[S]) + HALF[S] * want_grad.abs()
+                                                       + 2.0 ** -126)
+            assert ok.all()
+            again, same = nv.distill_loss(s, t, w, temperature=temp, grad=s)
+            assert torch.equal(again, loss) and torch.equal(same, grad)
+            if rows > 100:
+                plain = nv.distill_loss(clean, t, w, temperature=temp)
+                assert torch.equal(loss[::2], plain[0][::2]) and torch.equal(grad[::2], plain[1][::2])
