@@ -444,11 +444,14 @@ __global__ __launch_bounds__(1024) void backward_kernel(const Backward a) {
         asm volatile("" : "+v"(s1), "+v"(s2), "+v"(dw[k][i]), "+v"(db[k][i]));   // here, not later
       }
     }
-    // dres is here before anyone writes, who may write over it and into another lane's vector
+    // dres is here before the barrier, behind which another lane may write over it (a vector past the
+    // row's end, or cut by it, is its neighbours').  What is loaded of dy and h is used before the barrier.
     if (RES && !FULL) {
       static_assert(AHEAD || FULL, "");
 #pragma unroll
-      for (int k = 0; k < K; ++k) opaque(res[k], s2);
+      for (int k = 0; k < K; ++k) opaque(res[k], s2);      // as late as can be
+#pragma unroll
+      for (int k = 0; k < K; ++k) arrived(res[k]);
     }
     // the slots of two rows in turn: one barrier per row is enough
     s1 = reduce64(s1, Sum());

@@ -128,6 +128,13 @@ __device__ __forceinline__ void opaque(Vec<T, N>& v, float after) {
 #pragma unroll
   for (int i = 0; i < Vec<T, N>::kWords; ++i) asm("" : "+v"(v.w[i]) : "v"(after));
 }
+// v is in its registers, before anything that follows and has an effect (a barrier, a volatile asm): the
+// others may be moved past these.
+template <typename T, int N>
+__device__ __forceinline__ void arrived(Vec<T, N>& v) {
+#pragma unroll
+  for (int i = 0; i < Vec<T, N>::kWords; ++i) asm volatile("" : "+v"(v.w[i]));
+}
 __device__ __forceinline__ void opaque(uint32_t& v, float after) { asm volatile("" : "+v"(v) : "v"(after)); }
 
 // Elements by..N-1 moved to the front, zeros behind them (by in 1..N-1).

@@ -445,3 +445,22 @@ def test_backward_of_rows_about_a_wavefronts_length(nv, cols, T, W):
             a, c = dy.clone(), dres.clone()
             got = nv.layer_norm_backward(a, h, w, mean, rstd, dres=c, dx=a if target == "dy" else c)
             assert torch.equal(got[0], dx) and torch.equal(got[1], dw) and torch.equal(got[2], db)
+
+
+@pytest.mark.parametrize("T,W", [(BF, BF), (BF, F), (F, F), (F, BF)], ids=str)
+@pytest.mark.parametrize("cols", [1032, 1500, 4099, 4104, 6001, 8191, 8200, 14341, 16383])
+def test_in_place_of_rows_that_do_not_fill_a_workgroup(nv, cols, T, W):
+    """dx over dy and over dres, where a lane past the row's end has its neighbours' elements: more rows
+    than workgroups, the same bits as in memory of their own."""
+    rows = 1203
+    say("[norm] in place", rows, cols, T, W)
+    h, dres, w, _, gen = inputs(rows, cols, T, W)
+    dy = (0.01 * randn(gen, rows, cols)).to(T)
+    _, mean, rstd = forward_reference(h, w, None, 1e-5, True)
+    mean, rstd = mean[:, 0].float(), rstd[:, 0].float()
+    want = nv.layer_norm_backward(dy, h, w, mean, rstd, dres=dres)
+    for target in ("dy", "dres"):
+        for _ in range(3):
+            a, c = dy.clone(), dres.clone()
+            got = nv.layer_norm_backward(a, h, w, mean, rstd, dres=c, dx=a if target == "dy" else c)
+            assert all(torch.equal(p, q) for p, q in zip(got, want)), target
