@@ -346,13 +346,15 @@ class AdamWPlan:
 
     def _look_grads(self, grads) -> int:
         """The gradients' type, all of them checked."""
-        gtype = grads[0].dtype
-        kind = _type(grads[0], "gradients")
         if not self._seen_grads.again(grads):
+            for k, g in enumerate(grads):
+                if g is None:
+                    raise ValueError("gradient %d is None: a plan steps all of its tensors" % k)
+            _type(grads[0], "gradients")
             for g, n in zip(grads, self.numels):
-                self._look("grads", g, n, gtype)
+                self._look("grads", g, n, grads[0].dtype)
             self._seen_grads.keep(grads)
-        return kind
+        return TYPES[grads[0].dtype]
 
     def table(self, grads) -> np.ndarray:
         """The entries of nvfp4_adamw_tensor for these gradients."""
@@ -400,7 +402,8 @@ def adamw_step(plan: AdamWPlan, grads, *, step: int, lr: float, betas=(0.9, 0.99
                amax: torch.Tensor = None, seed: int = 0) -> None:
     """One AdamW step on the plan's tensors, in place.
 
-    grads: one tensor per parameter, all bfloat16 or all float32.  step: 1 for the first.
+    grads: one tensor per parameter (None is refused: a plan steps all of its tensors), all bfloat16
+    or all float32.  step: 1 for the first.
     grad_scale: float32 [1] on the GPU that multiplies the gradients (a clipping coefficient).
     amax: float32 [tensors], receives max |param| as written, for the *_from_amax calls.
     seed: of the stochastic rounding of 8-bit states and of bfloat16 parameters without a master

@@ -303,3 +303,13 @@ def test_tensors_are_recognized_by_more_than_their_addresses():
         assert seen.again(ts)
     seen.keep([object()])                     # nothing that can be compared: never recognized
     assert not seen.again([object()])
+
+
+def test_a_missing_gradient_is_named():
+    """None in the list of gradients (a parameter that the step did not use) is refused by its place."""
+    plan = train.AdamWPlan([OnTheGpu(8, at=A), OnTheGpu(8, at=B)], [OnTheGpu(8, at=C), OnTheGpu(8, at=D)],
+                           [OnTheGpu(8, at=E), OnTheGpu(8, at=F)], None, None, None)
+    g = OnTheGpu(8, at=G)
+    for grads, place in (([None, g], 0), ([g, None], 1)):
+        with pytest.raises(ValueError, match="gradient %d is None" % place):
+            train.adamw_step(plan, grads, step=1, lr=0.1)
