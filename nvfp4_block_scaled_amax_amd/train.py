@@ -12,7 +12,9 @@ computation runs in the library's kernels.
     plan = adamw_plan(params, state="e4m3")
     adamw_step(plan, grads, step=1, lr=1e-4, seed=0)
 
-Tensors are bfloat16 or float32, on one GPU, with a contiguous last dimension.
+Tensors are bfloat16 or float32, on one GPU, with a contiguous last dimension.  No call records
+an autograd graph, whatever `requires_grad` says: results have none, and a training loop passes
+the gradients on itself (examples/qad_step.py) or from a torch.autograd.Function of its own.
 """
 from __future__ import annotations
 
@@ -156,7 +158,8 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor = None,
     weight + bias.  center=False is the root-mean-square norm (mean is None).  mean and rstd
     are float32, one per row, for the backward pass.  amax: float32 [1], receives max |y| for
     fakequant_from_amax / quantize_from_amax.  x and residual may be 2-D with a row stride.
-    y may be x (without residual) and h may be x or residual, where they are contiguous."""
+    y may be x (without residual) and h may be x or residual, where they are contiguous.
+    Outside of autograd: layer_norm_backward is the gradient."""
     shape, dtype = x.shape, x.dtype
     xs, kind = _rows(x, shape, "x"), _type(x, "x")
     lead, cols = shape[:-1], shape[-1]
@@ -226,7 +229,8 @@ def distill_loss(student: torch.Tensor, teacher: torch.Tensor, weight: torch.Ten
     respect to the student's logits -> (loss float32 [...], grad in student's type or None).
 
     Logits are [..., vocab]; 2-D ones may have a row stride.  weight: float32 [...]; rows of
-    weight 0 are not read.  grad may be the student itself (written in place)."""
+    weight 0 are not read.  grad may be the student itself (written in place).  Outside of
+    autograd: loss has no graph, grad is what goes back from it."""
     shape = student.shape
     ss, kind = _rows(student, shape, "student"), _type(student, "student")
     lead, vocab = shape[:-1], shape[-1]
@@ -400,7 +404,7 @@ def adamw_plan(params, exp_avg=None, exp_avg_sq=None, *, master=None, avg_scale=
 def adamw_step(plan: AdamWPlan, grads, *, step: int, lr: float, betas=(0.9, 0.999),
                eps: float = 1e-8, weight_decay: float = 0.01, grad_scale: torch.Tensor = None,
                amax: torch.Tensor = None, seed: int = 0) -> None:
-    """One AdamW step on the plan's tensors, in place.
+    """One AdamW step on the plan's tensors, in place.  (No two of them may share memory.)
 
     grads: one tensor per parameter (None is refused: a plan steps all of its tensors), all bfloat16
     or all float32.  step: 1 for the first.
