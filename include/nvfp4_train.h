@@ -123,7 +123,9 @@ nvfp4_status nvfp4_distill_loss(const void* student, int64_t student_stride, con
  * with a non-finite value reads back as non-finite.
  * Stochastic rounding adds random bits below the kept ones and truncates.  The bits are
  * hash32(element + key) with key = hash32(hash32(hash32(seed) ^ step) ^ tensor index), see
- * csrc/adamw.hip: no state, the same on every run, and different for each step.
+ * csrc/adamw.hip: no state, the same on every run, and different for each step.  One word serves an
+ * element's m (bits 0..19), sqrt(v) (bits 12..31) and bf16 parameter (the upper half of the word times
+ * 0x9E3779B1): each rounding is unbiased by itself, the three are not independent of each other.
  * `tensors`: host array of `count` entries, read before the call returns.  Empty tensors
  * (numel 0) are skipped and may have NULL pointers.  All tensors of a call have one parameter type, gradient
  * type, state kind, and either all or none a master copy.  Different tensors must not overlap
