@@ -33,7 +33,8 @@ struct Batch {
 
 static_assert(sizeof(Batch) <= 4096 && kTable <= 64, "kernel arguments; a lane per entry");
 
-// Two rounds of xor-shift and multiply: every input bit reaches every output bit.
+// Two rounds of xor-shift and multiply: every input bit reaches every output bit.  Shifts and factors are a
+// published set of low bias (C. Wellons, "Prospecting for Hash Functions", 2018, public domain).
 __host__ __device__ __forceinline__ uint32_t hash32(uint32_t h) {
   h ^= h >> 16;
   h *= 0x7FEB352Du;
