@@ -4,11 +4,12 @@
 // writes y (and h) once, the backward pass reads dy and h (and dres) and writes dx once.  So a row
 // is held in registers while its sums are made: up to 512 columns by 16, 32 or 64 lanes of a
 // wavefront, eight elements each (in the backward pass up to 1024 of bf16, sixteen each); up to
-// 16384 by one workgroup of as many wavefronts as the row fills.  The variance is the mean square of what is held less the mean (not E[x^2] - mean^2, which
-// cancels).  Longer rows are read again for each step.  The backward pass keeps, next to the row, its
-// share of the column sums (dweight, dbias) in registers over all the rows that a workgroup
-// takes, leaves them as one partial row per workgroup in the workspace, and a second launch adds
-// those in a fixed order.  Loads are 16 bytes a lane, at any alignment of the element.
+// 16384 by one workgroup of as many wavefronts as the row fills.  The variance is the mean square
+// of what is held less the mean (not E[x^2] - mean^2, which cancels).  Longer rows are read again
+// for each step.  The backward pass keeps, next to the row, its share of the column sums (dweight,
+// dbias) in registers over all the rows that a workgroup takes, leaves them as one partial row per
+// workgroup in the workspace, and a second launch adds those in a fixed order.  Loads are 16
+// bytes a lane, at any alignment of the element.
 #include <type_traits>
 
 #include "train_common.h"
