@@ -464,3 +464,61 @@ def test_in_place_of_rows_that_do_not_fill_a_workgroup(nv, cols, T, W):
             a, c = dy.clone(), dres.clone()
             got = nv.layer_norm_backward(a, h, w, mean, rstd, dres=c, dx=a if target == "dy" else c)
             assert all(torch.equal(p, q) for p, q in zip(got, want)), target
+
+
+class Guarded:
+    """Tensors in memory of their own with 64 bytes around them that nothing may write, starting
+    `skew` elements into it."""
+
+    def __init__(self):
+        self.bufs = []
+
+    def __call__(self, values, skew):
+        esize, n = values.element_size(), values.numel()
+        buf = torch.full((n * esize + 128 + 16,), 0x5A, device="cuda", dtype=torch.uint8)
+        at = 64 + skew * esize
+        self.bufs.append((buf, at, at + n * esize))
+        part = buf[at:at + n * esize].view(values.dtype).view(values.shape)
+        part.copy_(values)
+        return part
+
+    def untouched(self):
+        return all((b[:lo] == 0x5A).all() and (b[hi:] == 0x5A).all() for b, lo, hi in self.bufs)
+
+
+@pytest.mark.parametrize("T,W", [(BF, BF), (BF, F), (F, F), (F, BF)], ids=str)
+@pytest.mark.parametrize("cols", [5, 100, 200, 513, 1023, 1030, 4099, 8200, 12001, 16383, 20001])
+def test_any_start_and_nothing_written_around(nv, cols, T, W):
+    """Every operand of both directions at odd starts, the outputs and a workspace of the exact size
+    with guards around them: the bits of the aligned call, and the guards as they were."""
+    for rows in (1, 6, 301):
+        say("[norm] guards", rows, cols, T, W)
+        x, r, w, b, gen = inputs(rows, cols, T, W)
+        dy = (0.01 * randn(gen, rows, cols)).to(T)
+        stat = torch.zeros(rows, device="cuda")
+        for res in (None, r):
+            for center in (True, False):
+                amax = torch.zeros(1, device="cuda")
+                want = nv.layer_norm(x, w, b, residual=res, center=center, amax=amax)
+                g = Guarded()
+                top = g(torch.zeros(1, device="cuda"), 1)
+                got = nv.layer_norm(
+                    g(x, 1), g(w, 3), g(b, 1), residual=None if res is None else g(res, 3), center=center,
+                    amax=top, y=g(torch.zeros_like(x), 1), h=None if res is None else g(torch.zeros_like(x), 3),
+                    mean=g(stat, 1) if center else None, rstd=g(stat, 3))
+                _, h, mean, rstd = want
+                for p, q in zip(got, want):
+                    assert (p is None and q is None) or torch.equal(p, q)
+                assert torch.equal(top, amax) and g.untouched()
+                want = nv.layer_norm_backward(dy, h, w, mean, rstd, dres=res, bias=center)
+                g = Guarded()
+                work = torch.zeros(nv.lib().nvfp4_layernorm_backward_workspace(rows, cols), device="cuda",
+                                   dtype=torch.uint8)
+                got = nv.layer_norm_backward(
+                    g(dy, 1), g(h, 3), g(w, 1), None if mean is None else g(mean, 1), g(rstd, 3),
+                    dres=None if res is None else g(res, 1), bias=center, dx=g(torch.zeros_like(dy), 3),
+                    dweight=g(torch.zeros_like(w), 1), dbias=g(torch.zeros_like(w), 3) if center else None,
+                    workspace=g(work, 0))
+                for p, q in zip(got, want):
+                    assert (p is None and q is None) or torch.equal(p, q)
+                assert g.untouched()
