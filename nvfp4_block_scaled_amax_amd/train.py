@@ -19,6 +19,7 @@ the gradients on itself (examples/qad_step.py) or from a torch.autograd.Function
 from __future__ import annotations
 
 import ctypes
+from itertools import chain
 
 import numpy as np
 import torch
@@ -334,9 +335,8 @@ class AdamWPlan:
 
     def _fill(self):
         lists = [getattr(self, kind) for _, kind, _, _ in self._columns]
-        flat = [t for tensors in lists for t in tensors]
-        alike = all(len(tensors) == len(self.numels) for tensors in lists)
-        if not (alike and self._seen.again(flat)):
+        flat = list(chain.from_iterable(lists))
+        if set(map(len, lists)) != {len(self.numels)} or not self._seen.again(flat):
             for (_, kind, sizes, dtype), tensors in zip(self._columns, lists):
                 if len(tensors) != len(sizes):
                     raise ValueError("%s: %d tensors for %d parameters" % (kind, len(tensors), len(sizes)))
