@@ -36,11 +36,12 @@
 // workgroup a compute unit and 985 with two, whose rows together pass the last-level cache: the
 // second reading is what costs, not the exponentials.  Loads and stores bypass the caches (660
 // against 692 us; the rest of a long row, which is read again, does not).  Rows of an odd length
-// start at odd addresses and take longer (4096 x 127999: 827 us); starting each at a 16-byte
-// boundary (707 us) would let a row's last bits depend on where it lies.
+// start at odd addresses, where 16-byte accesses are slow (4096 x 127999: 827 us).  Starting each row's units
+// at a 16-byte boundary (707 us) would let its last bits depend on where it lies; loading from the
+// boundary below and shifting words into the same units would not, and is not built.
 //
-// What bounds it is the memory: 4096 x 128000 bf16 reads and writes 3146 MB in 649 us, 4.85 TB/s,
-// where a copy of that size runs at 4.8.
+// What bounds it is the memory: 4096 x 128000 bf16 reads and writes 3146 MB in 647 us, 4.86 TB/s,
+// where a copy of that size runs at 4.8.  Without the gradient 541 us (2097 MB read, 3.9 TB/s).
 //
 // Where the rows are few and long, a row is split over several workgroups in two launches:
 // partial statistics, then gradient and partial losses, which the last workgroup of a row adds

@@ -100,8 +100,10 @@ __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v
 // each); longer ones a workgroup (LANES == 0).  A lane holds K vectors, and where that is eight
 // elements (HOLD) also its weights for all the rows that it comes by (bf16, 8192 x 4097 30.5 us, 41.0 if
 // they are read for each; 8192 x 4104 with residual 49.9 and 57.0; f32 the same).  Rows of bf16 that
-// fill the workgroup, without a residual, are an exception that only the measurement explains:
-// 8192 x 4096 27.4 us with the weights held, 24.1 without, 4096 x 8192 27.1 and 22.9.
+// fill the workgroup, without a residual, are an exception while the tensors are of the last-level
+// cache's size; why has not been shown (us, weights held and read for each row: 16384 x 2048 26.7 and
+// 24.4, 6553 x 5120 30.4 and 26.5, 8192 x 4096 27.2 and 23.4, 4096 x 8192 27.3 and 23.0, 512 x 4096 4.6
+// and 4.8).  For larger ones it is the slower way: 32768 x 4096 100 and 113.
 //
 // The memory bounds it: 8192 x 4096 bf16 with residual and h 49.5 us (268 MB, 5.4 TB/s; a copy of
 // that size 5.4), without 23.3 (134 MB, half of it in the last-level cache), f32 47.5; 65536 x 512
@@ -676,7 +678,8 @@ struct Split {
   int rows, most;
 };
 // Rows that a workgroup of the backward pass holds: long binary32 ones only if they fill it (the
-// others would need more than 1024 threads' 128 registers).
+// others would need more than 1024 threads' 128 registers; read again they take 2048 x 10001 110 us,
+// 12000 123 and 16383 176, where the held 2048 x 12288 takes 67 and 16384 90).
 bool backward_held(int64_t cols, int64_t esize) {
   return held(cols) && (esize == 2 || cols <= 8192 || cols % 1024 == 0);
 }
