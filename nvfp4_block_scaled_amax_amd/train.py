@@ -291,8 +291,8 @@ class AdamWPlan:
     kind that is not there); a checkpoint saves and restores their contents.  With 8-bit states
     exp_avg holds E4M3 codes of m / avg_scale and exp_avg_sq those of sqrt(v) / sq_scale, one
     scale per 128 elements.  The tensors are looked at again at each step, so `p.data = ...` is
-    noticed, and refused where the number, the sizes, the types or the device are no longer the plan's
-    or a tensor is not contiguous."""
+    noticed, and refused where the number, the sizes, the types or the device are no longer the plan's,
+    a tensor is not contiguous or two share memory."""
 
     KINDS = ("params", "exp_avg", "exp_avg_sq", "master", "avg_scale", "sq_scale")
 
@@ -343,10 +343,24 @@ class AdamWPlan:
                 for t, n in zip(tensors, sizes):
                     self._look(kind, t, n, dtype)
             self._seen.keep(flat)
+        moved = {}
         for (k, _, _, _), tensors in zip(self._columns, lists):
             now = [t.data_ptr() for t in tensors]
             if now != self._at.get(k):
+                moved[k] = now
+        if moved:
+            self._look_apart({**self._at, **moved})
+            for k, now in moved.items():
                 self._table[:, k] = self._at[k] = now
+
+    def _look_apart(self, at):
+        """That no two of the tensors at these addresses share memory: a launch writes all of them."""
+        parts = sorted((a, a + n * dtype.itemsize, kind) for k, kind, sizes, dtype in self._columns
+                       for a, n in zip(at[k], sizes) if n)
+        for (_, end, one), (start, _, other) in zip(parts, parts[1:]):
+            if start < end:
+                raise ValueError("%s and %s share memory" % (one, other) if one != other
+                                 else "two tensors of %s share memory" % one)
 
     def _look_grads(self, grads) -> int:
         """The gradients' type, all of them checked."""
@@ -404,7 +418,7 @@ def adamw_plan(params, exp_avg=None, exp_avg_sq=None, *, master=None, avg_scale=
 def adamw_step(plan: AdamWPlan, grads, *, step: int, lr: float, betas=(0.9, 0.999),
                eps: float = 1e-8, weight_decay: float = 0.01, grad_scale: torch.Tensor = None,
                amax: torch.Tensor = None, seed: int = 0) -> None:
-    """One AdamW step on the plan's tensors, in place.  (No two of them may share memory.)
+    """One AdamW step on the plan's tensors, in place.
 
     grads: one tensor per parameter (None is refused: a plan steps all of its tensors), all bfloat16
     or all float32.  step: 1 for the first.

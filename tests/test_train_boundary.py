@@ -313,3 +313,25 @@ def test_a_missing_gradient_is_named():
     for grads, place in (([None, g], 0), ([g, None], 1)):
         with pytest.raises(ValueError, match="gradient %d is None" % place):
             train.adamw_step(plan, grads, step=1, lr=0.1)
+
+
+def test_a_plan_refuses_tensors_that_share_memory():
+    """A parameter listed twice (tied weights), a state that is another's, parts that overlap: the
+    workgroups of one launch would race for them.  Neighbours in one buffer and empty tensors do not."""
+    def plan(params, avg, sq):
+        return train.AdamWPlan(params, avg, sq, None, None, None).table(grads)
+    grads = [OnTheGpu(100, at=G), OnTheGpu(100, at=H)]
+    apart = lambda at: [OnTheGpu(100, at=at), OnTheGpu(100, at=at + 400)]
+    plan(apart(A), apart(B), apart(C))
+    for params, avg, sq in ((apart(A)[:1] * 2, apart(B), apart(C)), (apart(A), apart(B)[:1] * 2, apart(C)),
+                            (apart(A), apart(B), apart(B)), (apart(A), apart(A + 796), apart(C)),
+                            ([OnTheGpu(100, at=A), OnTheGpu(100, at=A + 396)], apart(B), apart(C))):
+        with pytest.raises(ValueError, match="share memory"):
+            plan(params, avg, sq)
+    later = train.AdamWPlan(apart(A), apart(B), apart(C), None, None, None)
+    later.exp_avg[1] = later.exp_avg[0]
+    for _ in range(2):
+        with pytest.raises(ValueError, match="share memory"):
+            later.table(grads)
+    none = [OnTheGpu(0, at=0), OnTheGpu(0, at=0)]
+    train.AdamWPlan(none, none, none, None, None, None)
