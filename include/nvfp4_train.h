@@ -50,6 +50,7 @@ const char* nvfp4_train_status_str(nvfp4_status status);
  *   mean = sum_j h_j / cols                 (0 where center == 0: root-mean-square norm)
  *   rstd = 1 / sqrt(sum_j (h_j - mean)^2 / cols + eps)
  *   y    = round((h - mean) * rstd * weight + bias)
+ * (in binary32: where |h - mean| passes 2^64 the sum of squares is infinite and rstd 0).
  * x, residual [rows][cols] of `type` with row strides in elements (>= cols); h and y [rows][cols]
  * of `type`, contiguous; weight and bias (may be NULL) [cols] of `wtype`; mean (NULL where
  * center == 0) and rstd float [rows].  h is required with residual and must be NULL without.
@@ -117,7 +118,8 @@ nvfp4_status nvfp4_distill_loss(const void* student, int64_t student_stride, con
  * param is it rounded to nearest even; param is not read); or bf16 alone (master NULL), rounded
  * stochastically, because most updates are smaller than half a bf16 step.
  * States: float; or 8 bits, per block of NVFP4_ADAMW_BLOCK consecutive elements of the tensor
- * one float scale = max / 448 and E4M3 codes of m / scale and sqrt(v) / scale.  Codes are rounded
+ * one float scale = max / 448 and E4M3 codes of m / scale and sqrt(v) / scale (v is read back as the binary32 square
+ * of code * scale, 0 where that is below 2^-75).  Codes are rounded
  * stochastically (round-to-nearest would hold v still: beta2 near 1 moves it by less than half
  * a step); sqrt(v) > 0 never becomes 0, and an m whose block stays below 2^-100 does.  The update of p uses m and v before that rounding.  A block
  * with a non-finite value reads back as non-finite.
