@@ -13,7 +13,9 @@ x is a contiguous bf16 CUDA tensor [rows, cols] or [E, rows, cols] (a leading
 expert dimension selects the batched entry points), cols % 16 == 0.
 
 The operators of a distillation step around it (layer norm, distillation loss, AdamW) are in
-``train.py`` and exported here; ``include/nvfp4_train.h`` defines them.
+``train.py`` and exported here; ``include/nvfp4_train.h`` defines them.  Those of a step on the
+model's own answers (packed products of a few rows, log probabilities of tokens, gradient norm) are in
+``answer.py``; ``include/nvfp4_answer.h`` defines them.
 """
 from __future__ import annotations
 
@@ -28,6 +30,8 @@ __all__ = ["quantize", "fakequant", "amax", "quantize_from_amax", "fakequant_fro
            "diag_ws_words", "lib",
            "layer_norm", "layer_norm_backward", "distill_loss", "adamw_plan", "adamw_step",
            "AdamWPlan", "ADAMW_BLOCK",
+           "packed_matvec", "token_logprobs", "token_logprobs_backward", "grad_norm", "clip_grads",
+           "MATVEC_MAX_ROWS", "LOGPROBS_MAX",
            "NVFP4Error", "MODES", "RULES", "STATS", "FUSED_WS_WORDS", "LIB_PATH"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnvfp4_amax.so")
@@ -94,6 +98,7 @@ def lib() -> ctypes.CDLL:
                      "nvfp4_quantize_fused_noalloc"):
             getattr(L, name).restype = i32
         train.bind(L)
+        answer.bind(L)
         _lib = L
     return _lib
 
@@ -361,3 +366,6 @@ def set_fused_wait_limit(polls: int) -> None:
 from . import train  # noqa: E402  (it uses the helpers above)
 from .train import (ADAMW_BLOCK, AdamWPlan, adamw_plan, adamw_step, distill_loss,  # noqa: E402
                     layer_norm, layer_norm_backward)
+from . import answer  # noqa: E402
+from .answer import (LOGPROBS_MAX, MATVEC_MAX_ROWS, clip_grads, grad_norm, packed_matvec,  # noqa: E402
+                     token_logprobs, token_logprobs_backward)

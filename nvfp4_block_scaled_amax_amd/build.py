@@ -24,7 +24,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 SOURCES = [os.path.join(CSRC, f) for f in ("nvfp4_amax.hip", "layer_norm.hip", "distill_loss.hip",
-                                           "adamw.hip")]
+                                           "adamw.hip", "packed_matvec.hip", "token_logprobs.hip",
+                                           "grad_norm.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libnvfp4_amax.so")
 ARCH = os.environ.get("NVFP4_OFFLOAD_ARCH", "gfx950")
