@@ -23,10 +23,9 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef u32x4 u32x4_a8 __attribute__((aligned(8)));
 typedef u32x2 u32x2_a8 __attribute__((aligned(8)));
-typedef uint16_t u16_a1 __attribute__((aligned(1)));
 
 constexpr int kMaxRows = NVFP4_MATVEC_MAX_ROWS;
-constexpr int kStepK = 128;                 // elements of a weight row that a wavefront takes at a time
+constexpr int kUnit = 512;                  // elements of 16 weight rows that a wavefront takes at a time
 
 struct Matvec {
   const uint16_t* x;        // bf16; binary32 rows are three each
@@ -38,11 +37,22 @@ struct Matvec {
   int64_t x_stride, rows, cols;
   int out_rows, picks, experts, group;      // tokens * picks; 1 or 3 rows of x per token
   int wide, f32;                            // 64-bit indices; binary32 y
+  int lds;                                  // bytes of shared memory for x
+  int deal;                                 // log2 of the wavefronts that deal a tile's units among them
 };
 
+// Eight codes as bf16.
+__device__ __forceinline__ bf16x8 decode8(uint32_t w) {
+  u32x4 r;
+#define PAIR(SEL) \
+  r[SEL] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, SEL));
+  PAIR(0) PAIR(1) PAIR(2) PAIR(3)
+#undef PAIR
+  return __builtin_bit_cast(bf16x8, r);
+}
 // Eight codes times their scale, as bf16: the low half of each product is zero.
 __device__ __forceinline__ bf16x8 decode8(uint32_t w, float scale) {
-  uint32_t r[4];
+  u32x4 r;
 #define PAIR(SEL)                                                              \
   {                                                                            \
     const f32x2 v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, SEL);    \
@@ -51,26 +61,35 @@ __device__ __forceinline__ bf16x8 decode8(uint32_t w, float scale) {
   }
   PAIR(0) PAIR(1) PAIR(2) PAIR(3)
 #undef PAIR
-  const u32x4 v = {r[0], r[1], r[2], r[3]};
-  return __builtin_bit_cast(bf16x8, v);
+  return __builtin_bit_cast(bf16x8, r);
+}
+// Scales 2 `pair` and 2 `pair` + 1 of eight bytes.
+__device__ __forceinline__ f32x2 scales_of(u32x2 bytes, int pair) {
+  const int w = (int)bytes[pair >> 1];
+  return pair & 1 ? __builtin_amdgcn_cvt_pk_f32_fp8(w, true) : __builtin_amdgcn_cvt_pk_f32_fp8(w, false);
 }
 
-template <int RT, int MT>
-struct Stage {
-  u32x4 code[RT];
-  uint32_t scale[RT];
-  u32x4 x[MT][4];
+// What a lane holds of a unit: 128 elements of a weight row, and the scales that it needs.
+template <int S>
+struct Unit {
+  u32x4 code[4];
+  u32x2 scale[S];
 };
 
-template <int RT, int MT, int W, int DEPTH, bool EXPERT>
+// SHORT: rows of less than a unit.
+template <bool FEW, int MT, int W, int DEPTH, bool EXPERT, bool SHORT>
 __global__ __launch_bounds__(W * 64) void matvec_kernel(const Matvec a) {
-  __shared__ float part[W][RT * MT][256];
+  constexpr int kCols = FEW ? 4 : 16;                // of a tile
+  constexpr int S = FEW ? 4 : 1;
+  extern __shared__ __align__(16) char held[];       // x, then the wavefronts' sums
   __shared__ uint16_t list[EXPERT ? kMaxRows : 1];
-  __shared__ int counts[2];
-  const int lane = threadIdx.x & 63;
+  __shared__ int counts[2], x_row[EXPERT ? 64 : 1];
+  __shared__ u32x4 zeros[FEW ? 16 : 1];
+  const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int deal = 1 << a.deal, wr = wave >> a.deal, wk = wave & (deal - 1);
   const int e = EXPERT ? blockIdx.y : 0;
-  const int64_t row0 = (int64_t)blockIdx.x * (RT * 16);
+  const int64_t row0 = (int64_t)blockIdx.x * (W * 16 >> a.deal);      // the workgroup's first weight row
   int count = a.out_rows;
   if (EXPERT) {
     // the rows that go to this expert, in order; behind the end those that go nowhere (expert 0's
@@ -95,127 +114,249 @@ __global__ __launch_bounds__(W * 64) void matvec_kernel(const Matvec a) {
     count = counts[0];
     for (int i = 0; i < counts[1]; ++i) {
       const int64_t m = list[kMaxRows - 1 - i];
-      for (int64_t j = row0 + threadIdx.x; j < row0 + RT * 16 && j < a.rows; j += W * 64) {
+      for (int64_t j = row0 + threadIdx.x; j < row0 + (W * 16 >> a.deal) && j < a.rows; j += W * 64) {
         if (a.f32) ((float*)a.y)[m * a.rows + j] = 0.0f;
         else ((uint16_t*)a.y)[m * a.rows + j] = 0;
       }
     }
     if (count == 0) return;
   }
-  const float alpha = a.alpha[e];
-  const int g = lane >> 4;
-  // this lane's weight rows (the last one again past the end: what comes of it is not stored)
-  const uint8_t* code[RT];
-  const uint8_t* scale[RT];
+  if (FEW && threadIdx.x < 16) zeros[threadIdx.x] = u32x4{0u, 0u, 0u, 0u};
+  // Units of a row.  What is left behind the whole ones is a unit that ends with the row: x is zero
+  // where it overlaps the one before.
+  const int cols = (int)a.cols, full = cols / kUnit, all = (cols + kUnit - 1) / kUnit;
+  const auto start = [&](int unit) { return SHORT ? 0 : unit < full ? unit * kUnit : cols - kUnit; };
+  // the tile's first weight row, this lane's row in it, and the rows of its scales (the last one again
+  // past the end: what comes of it is not stored)
+  const int64_t row_t = row0 + wr * 16 < a.rows ? row0 + wr * 16 : a.rows - 1;
+  const int rows_t = (int)(a.rows - row_t < 16 ? a.rows - row_t : 16);
+  const int64_t first_row = (int64_t)e * a.rows + row_t;
+  const uint8_t* code = a.codes + first_row * (a.cols / 2);
+  const uint8_t* scale = a.scales + first_row * (a.cols / 16);
+  const uint32_t code_at = (uint32_t)min(c, rows_t - 1) * (uint32_t)(cols / 2) + g * 64;
+  uint32_t scale_at[S];
 #pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    const int64_t row = row0 + r * 16 + (lane & 15);
-    const int64_t at = (int64_t)e * a.rows + (row < a.rows ? row : a.rows - 1);
-    code[r] = a.codes + at * (a.cols / 2) + g * 16;
-    scale[r] = a.scales + at * (a.cols / 16) + g * 2;
-  }
-  const int full = (int)(a.cols / kStepK);
-  const int per_pass = MT * 16 / a.group;
+  for (int i = 0; i < S; ++i)
+    scale_at[i] = (uint32_t)min(FEW ? g * 4 + i : c, rows_t - 1) * (uint32_t)(cols / 16) + (FEW ? c & 3 : g) * 8;
+  // A unit past this wavefront's last one is 64 bytes of its first, read by every lane: no branch stands
+  // between loads and the waits can count them.
+  const auto load = [&](Unit<S>& u, int unit) {
+    const int at = unit < all ? start(unit) : 0;
+    const uint32_t there = unit < all ? ~0u : 0u;
+    const uint8_t* codes = code + at / 2;
+    const uint8_t* scales = scale + at / 16;
+    if constexpr (!SHORT) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) u.code[q] = *(const u32x4_a8*)(codes + (code_at & there) + q * 16);
+#pragma unroll
+      for (int i = 0; i < S; ++i) u.scale[i] = *(const u32x2_a1*)(scales + (scale_at[i] & there));
+    } else {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int k = cols - g * 128 - q * 32;
+        u.code[q] = u32x4{0u, 0u, 0u, 0u};
+        if (k >= 32) {
+          u.code[q] = *(const u32x4_a8*)(codes + code_at + q * 16);
+        } else if (k >= 16) {
+          const u32x2 v = *(const u32x2_a8*)(codes + code_at + q * 16);
+          u.code[q][0] = v[0], u.code[q][1] = v[1];
+        }
+      }
+      const int n = cols / 16 - (FEW ? c & 3 : g) * 8;       // scales that are there
+#pragma unroll
+      for (int i = 0; i < S; ++i) {
+        u.scale[i] = u32x2{0u, 0u};
+        if (n >= 8) {
+          u.scale[i] = *(const u32x2_a1*)(scales + scale_at[i]);
+        } else if (n > 0) {
+          uint32_t b[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) b[k] = scales[scale_at[i] + min(k, n - 1)];
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (k < n) u.scale[i][k >> 2] |= b[k] << (8 * (k & 3));
+        }
+      }
+    }
+  };
+  // columns of which a turn of all wavefronts fits: at least a.group of them
+  const int turn = kUnit * deal * DEPTH;
+  const int per_pass = min(MT * kCols, a.lds / (turn * 2 + 16)) / a.group;
   for (int first = 0; first < count; first += per_pass) {
-    const int here = min(per_pass, count - first);
-    const uint16_t* x[MT];
-#pragma unroll
-    for (int c = 0; c < MT; ++c) {
-      const int col = min(c * 16 + (lane & 15), here * a.group - 1);
-      const int i = first + col / a.group;
-      const int token = (EXPERT ? (int)list[i] : i) / a.picks;
-      x[c] = a.x + (int64_t)(token * a.group + col % a.group) * a.x_stride + g * 32;
+    const int here = min(per_pass, count - first), wide = here * a.group;
+    // x: all of it, or as many elements of each column as fit, a multiple of a turn
+    const int fit = (a.lds / wide - 16) / 2, chunk = (fit >= all * kUnit ? all * kUnit : fit / turn * turn) / kUnit;
+    const int pitch = chunk * (kUnit * 2) + 16;
+    if (EXPERT) {
+      for (int col = threadIdx.x; col < wide; col += W * 64)
+        x_row[col] = list[first + col / a.group] / a.picks * a.group + col % a.group;
+      __syncthreads();
     }
-    f32x4 acc[RT][MT];
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-      for (int c = 0; c < MT; ++c) acc[r][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
-    const auto load = [&](Stage<RT, MT>& s, int step) {
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        s.code[r] = *(const u32x4_a8*)(code[r] + (int64_t)step * (kStepK / 2));
-        s.scale[r] = *(const u16_a1*)(scale[r] + (int64_t)step * (kStepK / 16));
-      }
-#pragma unroll
-      for (int c = 0; c < MT; ++c)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          s.x[c][i] = *(const u32x4_a2*)(x[c] + (int64_t)step * kStepK + i * 8);
+    // A wavefront stages units of columns: with `beside` wavefronts to a column it takes every beside-th
+    // unit of every (W / beside)-th column, kAhead at a time.  The first ones are asked for before the
+    // weights: loads come back in order.
+    constexpr int kAhead = FEW ? 4 : 8;
+    const int beside = 31 - __builtin_clz(min(chunk, W)), col_step = W >> beside;
+    struct Place {
+      int col, unit;
     };
-    const auto add = [&](const Stage<RT, MT>& s) {
+    const Place begin = {wave >> beside, wave & ((1 << beside) - 1)};
+    const auto after = [&](Place p) {
+      p.col += col_step;
+      if (p.col >= wide) {
+        p.col = begin.col;
+        p.unit += 1 << beside;
+      }
+      return p;
+    };
+    u32x4 v[kAhead];
+    // (a place past the last one is the last one again, and no branch stands between the loads)
+    const auto fetch = [&](int from, Place p) {
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        const float lo = __builtin_amdgcn_cvt_f32_fp8((int)s.scale[r], 0);
-        const float hi = __builtin_amdgcn_cvt_f32_fp8((int)s.scale[r], 1);
+      for (int k = 0; k < kAhead; ++k) {
+        const int col = min(p.col, wide - 1), unit = min(from + min(p.unit, chunk - 1), all - 1);
+        const int at = start(unit) + lane * 8;
+        const int64_t row = EXPERT ? __builtin_amdgcn_readfirstlane(x_row[col]) : first * a.group + col;
+        const uint16_t* x = a.x + row * a.x_stride;
+        v[k] = *(const u32x4_a2*)(x + (uint32_t)(SHORT ? min(at, cols - 8) : at));
+        const bool fresh = SHORT ? at < cols : at >= unit * kUnit;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[k][i] = fresh ? v[k][i] : 0u;
+        p = after(p);
+      }
+    };
+    const auto put = [&](Place p) {
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int col = min(p.col, wide - 1), unit = min(p.unit, chunk - 1);
+        *(u32x4*)(held + col * pitch + unit * (kUnit * 2) + lane * 16) = v[k];
+        p = after(p);
+      }
+      return p;
+    };
+    fetch(0, begin);
+    Unit<S> s[DEPTH];
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) load(s[d], wk + d * deal);
+    f32x4 acc[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    // the lane's column of x: of FEW, four columns a tile, four lanes each; the lanes of group g take the
+    // column's elements of group g, the others zeros
+    const char* xs[MT];
+    int live[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const int col = m * kCols + (FEW ? c >> 2 : c);
+      live[m] = !FEW || ((c & 3) == g && col < wide) ? -1 : 0;
+      xs[m] = live[m] ? held + min(col, wide - 1) * pitch + g * 256 : (const char*)zeros;
+    }
+    const auto add = [&](const Unit<S>& u, int unit) {        // unit: in the chunk
+      const char* from[MT];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) from[m] = xs[m] + ((unit * (kUnit * 2)) & live[m]);
+      f32x4 last[MT];                                // of FEW: the products of the block before
+      f32x2 by[4];                                   // and the scales of two blocks
+      const auto take = [&](int block) {
+        if (!(block & 1))
+#pragma unroll
+          for (int i = 0; i < 4; ++i) by[i] = scales_of(u.scale[i % S], block >> 1);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[m][i] = fmaf(last[m][i], by[i][block & 1], acc[m][i]);
+          // (the sums stay here: moved down behind the loop's branch they would keep every block's products)
+          asm volatile("" : "+v"(acc[m]));
+        }
+      };
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        u32x4 x[MT][4];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[m][i] = *(const u32x4*)(from[m] + q * 64 + i * 16);
+        if constexpr (FEW) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const bf16x8 w0 = decode8(u.code[q][2 * h]), w1 = decode8(u.code[q][2 * h + 1]);
+            f32x4 d[MT];
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+              d[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w0, __builtin_bit_cast(bf16x8, x[m][2 * h]), zero, 0,
+                                                             0, 0);
+              d[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w1, __builtin_bit_cast(bf16x8, x[m][2 * h + 1]), d[m],
+                                                             0, 0, 0);
+            }
+            if (q + h) take(2 * q + h - 1);          // while this block's products are under way
+#pragma unroll
+            for (int m = 0; m < MT; ++m) last[m] = d[m];
+            __builtin_amdgcn_sched_barrier(0);
+          }
+          if (q == 3) take(7);
+        } else {
+          const f32x2 by = scales_of(u.scale[0], q);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const bf16x8 w = decode8(u.code[q][i], by[i >> 1]);
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+              acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8, x[m][i]), acc[m],
+                                                               0, 0, 0);
+          }
+        }
+      }
+    };
+    int t = wk;
+    for (int from = 0; from < all; from += chunk) {
+      if (first || from) __syncthreads();            // the chunk before, or the last pass' sums, is read
+      if (from) fetch(from, begin);
+      for (Place p = put(begin); p.unit < chunk;) {
+        fetch(from, p);
+        p = put(p);
+      }
+      lds_barrier();
+      const int until = min(from + chunk, all);
+      while (t < until) {
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) {
+          add(s[d], t - from);
+          load(s[d], t + DEPTH * deal);
+          t += deal;
+          if (t >= until) break;
+        }
+      }
+    }
+    __syncthreads();                                 // x is read
+    // [wave][column][16 rows of the tile]
+    float* part = (float*)held;
+    constexpr int kPart = MT * kCols * 16;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      f32x4 v = acc[m];
+      if constexpr (FEW) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const bf16x8 w = decode8(s.code[r][i], i < 2 ? lo : hi);
-#pragma unroll
-          for (int c = 0; c < MT; ++c)
-            acc[r][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                w, __builtin_bit_cast(bf16x8, s.x[c][i]), acc[r][c], 0, 0, 0);
+          v[i] += dpp<0xB1>(v[i]);                   // the four lanes of a column
+          v[i] += dpp<0x4E>(v[i]);
         }
-      }
-    };
-    Stage<RT, MT> s[DEPTH];
-#pragma unroll
-    for (int d = 0; d < DEPTH; ++d)
-      if (wave + d * W < full) load(s[d], wave + d * W);
-    for (int step = wave; step < full; step += DEPTH * W) {
-#pragma unroll
-      for (int d = 0; d < DEPTH; ++d) {
-        if (step + d * W < full) {
-          add(s[d]);
-          if (step + (d + DEPTH) * W < full) load(s[d], step + (d + DEPTH) * W);
-        }
+        if ((c & 3) == 0) *(f32x4*)(part + wave * kPart + (m * 4 + (c >> 2)) * 16 + g * 4) = v;
+      } else {
+        *(f32x4*)(part + wave * kPart + (m * 16 + c) * 16 + g * 4) = v;
       }
     }
-    // what is left of the rows: up to 112 elements, blocks of 16 whole
-    const int left = (int)(a.cols - (int64_t)full * kStepK) - g * 32;
-    if (full * (int64_t)kStepK < a.cols && full % W == wave) {
-      Stage<RT, MT> t;
-      const int64_t step = full;
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        t.code[r] = u32x4{0u, 0u, 0u, 0u};
-        t.scale[r] = 0u;
-        if (left >= 16) {
-          const u32x2 v = *(const u32x2_a8*)(code[r] + step * (kStepK / 2));
-          t.code[r][0] = v[0], t.code[r][1] = v[1];
-          t.scale[r] = scale[r][step * (kStepK / 16)];
-        }
-        if (left >= 32) {
-          const u32x2 v = *(const u32x2_a8*)(code[r] + step * (kStepK / 2) + 8);
-          t.code[r][2] = v[0], t.code[r][3] = v[1];
-          t.scale[r] |= (uint32_t)scale[r][step * (kStepK / 16) + 1] << 8;
-        }
-      }
-#pragma unroll
-      for (int c = 0; c < MT; ++c)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          t.x[c][i] = u32x4{0u, 0u, 0u, 0u};
-          if (left >= i * 8 + 8) t.x[c][i] = *(const u32x4_a2*)(x[c] + step * kStepK + i * 8);
-        }
-      add(t);
-    }
-    if (first) __syncthreads();               // the last pass' sums are read
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-      for (int c = 0; c < MT; ++c) *(f32x4*)&part[wave][r * MT + c][lane * 4] = acc[r][c];
     __syncthreads();
-    for (int o = threadIdx.x; o < here * (RT * 16); o += W * 64) {
-      const int j = o % (RT * 16), i = o / (RT * 16);
+    const float alpha = a.alpha[e];
+    constexpr int kRowBits = 4 + (W == 16 ? 4 : W == 8 ? 3 : 2);
+    const int row_bits = kRowBits - a.deal;          // the workgroup's weight rows
+    for (int o = threadIdx.x; o < here << row_bits; o += W * 64) {
+      const int j = o & ((1 << row_bits) - 1), i = o >> row_bits;
       if (row0 + j >= a.rows) continue;
       float sum = 0.0f;
       for (int p = a.group - 1; p >= 0; --p) {         // the smallest part first
-        const int col = i * a.group + p;
-        const int at = ((j & 15) >> 2) * 64 + (col & 15) * 4 + (j & 3);
-#pragma unroll
-        for (int w = 0; w < W; ++w) sum += part[w][(j >> 4) * MT + (col >> 4)][at];
+        const float* from = part + ((j >> 4) << a.deal) * kPart + (i * a.group + p) * 16 + (j & 15);
+        for (int w = 0; w < deal; ++w) sum += from[w * kPart];
       }
       sum *= alpha;
       const int64_t m = EXPERT ? (int)list[first + i] : first + i, to = m * a.rows + row0 + j;
@@ -255,11 +396,30 @@ __global__ __launch_bounds__(256) void split_kernel(const float* x, int64_t stri
   for (int p = 0; p < 3; ++p) *(u32x4*)(out + (row * 3 + p) * cols + at) = r[p];
 }
 
-template <int RT, int MT, int W, int DEPTH>
-void launch(const Matvec& a, int64_t tiles, hipStream_t stream) {
-  const dim3 grid((unsigned)((tiles + RT - 1) / RT), (unsigned)a.experts);
-  if (a.expert) matvec_kernel<RT, MT, W, DEPTH, true><<<grid, W * 64, 0, stream>>>(a);
-  else matvec_kernel<RT, MT, W, DEPTH, false><<<grid, W * 64, 0, stream>>>(a);
+// `room`: shared memory for x, so that one (150 KB), two or more workgroups share a compute unit.
+template <bool FEW, int MT, int W, int DEPTH, bool EXPERT, bool SHORT = false>
+void launch(Matvec a, int64_t columns, int room, int deal, hipStream_t stream) {
+  const int64_t tiles = (a.rows + 15) / 16, units = (a.cols + kUnit - 1) / kUnit;
+  const auto turn = [](int deal) { return (kUnit * DEPTH * 2 << deal) + 16; };     // bytes of a column
+  // enough workgroups for the compute units: where the rows are few, more wavefronts deal a tile's units, as
+  // far as there are units and every column fits
+  constexpr int kMany = 192;
+  a.deal = units > 1 ? deal : 0;
+  while ((2 << a.deal) <= W && (1 << a.deal) < units && !SHORT && columns * turn(a.deal + 1) <= room &&
+         a.experts * ((tiles << a.deal) / W) < kMany)
+    ++a.deal;
+  // all of x, or what there is
+  const int64_t want = columns * (units * (2 * kUnit) + 16);
+  const int least = 3 * turn(a.deal);
+  a.lds = (int)(want < room ? want : room);
+  if (a.lds < least) a.lds = least;
+  constexpr int kSums = W * MT * (FEW ? 256 : 1024);
+  const int bytes = a.lds > kSums ? a.lds : kSums;
+  const dim3 grid((unsigned)((tiles + (W >> a.deal) - 1) / (W >> a.deal)), (unsigned)a.experts);
+  const auto kernel = matvec_kernel<FEW, MT, W, DEPTH, EXPERT, SHORT>;
+  if (bytes > 60 * 1024)
+    (void)hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  kernel<<<grid, W * 64, bytes, stream>>>(a);
 }
 
 }  // namespace
@@ -304,7 +464,7 @@ NVFP4_EXPORT nvfp4_status nvfp4_packed_matvec(const void* x, int64_t x_stride, c
   if (overlap(out[0], out[1])) return NVFP4_ERR_ALIAS;
   (void)hipGetLastError();
   Matvec a = {(const uint16_t*)x, codes, scales, alpha, expert, y, x_stride, rows, cols, (int)out_rows,
-              (int)picks, (int)E, 1, itype == NVFP4_I64, ytype == NVFP4_T_F32};
+              (int)picks, (int)E, 1, itype == NVFP4_I64, ytype == NVFP4_T_F32, 0, 0};
   if (xtype == NVFP4_T_F32) {
     split_kernel<<<dim3((unsigned)((cols + 2047) / 2048), (unsigned)tokens), 256, 0, stream>>>(
         (const float*)x, x_stride, cols, (uint16_t*)workspace);
@@ -314,10 +474,24 @@ NVFP4_EXPORT nvfp4_status nvfp4_packed_matvec(const void* x, int64_t x_stride, c
     a.x_stride = cols;
     a.group = 3;
   }
-  const int64_t tiles = (rows + 15) / 16;
-  const int64_t columns = (out_rows + E - 1) / E * a.group;
-  if (columns <= 16) launch<1, 1, 8, 3>(a, tiles, stream);
-  else if (columns <= 32) launch<2, 2, 8, 2>(a, tiles, stream);
-  else launch<2, 4, 4, 1>(a, tiles, stream);
+  constexpr int kOne = 150 * 1024, kFive = 30 * 1024;
+  if (expert) {
+    // what an expert gets is not known here: twice its share
+    const int64_t columns = (2 * out_rows + E - 1) / E * a.group;
+    if (cols < kUnit) launch<false, 1, 4, 1, true, true>(a, 16, kOne, 0, stream);
+    else if (columns <= 16) launch<false, 1, 4, 2, true>(a, columns, kFive, 0, stream);
+    else if (columns <= 32) launch<false, 2, 8, 2, true>(a, columns, kOne / 2, 0, stream);
+    else launch<false, 4, 8, 1, true>(a, 64, kOne, 0, stream);
+  } else {
+    const int64_t columns = out_rows * a.group;
+    if (cols < kUnit && columns <= 4) launch<true, 1, 4, 1, false, true>(a, columns, kOne, 0, stream);
+    else if (cols < kUnit) launch<false, 1, 4, 1, false, true>(a, 16, kOne, 0, stream);
+    else if (columns <= 4 && rows > 6144) launch<true, 1, 4, 1, false>(a, columns, kOne, 1, stream);
+    else if (columns <= 4) launch<true, 1, 8, 1, false>(a, columns, kOne, 1, stream);
+    else if (columns <= 8 && rows < 16384) launch<true, 2, 8, 2, false>(a, columns, kOne, 0, stream);
+    else if (columns <= 16) launch<false, 1, 16, 1, false>(a, columns, kOne, 0, stream);
+    else if (columns <= 32) launch<false, 2, 16, 1, false>(a, columns, kOne, 0, stream);
+    else launch<false, 4, 8, 1, false>(a, columns < 64 ? columns : 64, kOne, 0, stream);
+  }
   return launched();
 }
