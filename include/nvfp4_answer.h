@@ -106,13 +106,13 @@ nvfp4_status nvfp4_token_logprobs_backward(const void* logits, int64_t stride, c
  * 0, a NaN gives NaN in both.  scale (may be NULL) is what nvfp4_adamw_step takes as grad_scale.
  * `tensors`: host array of `count` entries, read before the call returns; empty ones are skipped and
  * may have NULL pointers.  All have `type`.  numel <= 2^36.  max_norm >= 0, eps >= 0, finite.
- * workspace: nvfp4_grad_norm_workspace(...) bytes, 16-byte aligned, any content.  One launch per
+ * workspace: NVFP4_GRAD_NORM_WORKSPACE(count) bytes, 16-byte aligned, any content.  One launch per
  * 200 tensors, and one. */
+#define NVFP4_GRAD_NORM_WORKSPACE(count) (16384 * ((int64_t)(count) / 200 + 1))
 typedef struct {
   void* grad;          /* [numel] float or bf16 */
   int64_t numel;
 } nvfp4_grad_tensor;
-int64_t nvfp4_grad_norm_workspace(const nvfp4_grad_tensor* tensors, int64_t count);
 nvfp4_status nvfp4_grad_norm(const nvfp4_grad_tensor* tensors, int64_t count, nvfp4_type type,
                              double max_norm, double eps, float* norm, float* scale,
                              void* workspace, hipStream_t stream);

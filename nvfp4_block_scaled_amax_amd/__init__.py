@@ -31,7 +31,7 @@ __all__ = ["quantize", "fakequant", "amax", "quantize_from_amax", "fakequant_fro
            "layer_norm", "layer_norm_backward", "distill_loss", "adamw_plan", "adamw_step",
            "AdamWPlan", "ADAMW_BLOCK",
            "packed_matvec", "token_logprobs", "token_logprobs_backward", "grad_norm", "clip_grads",
-           "MATVEC_MAX_ROWS", "LOGPROBS_MAX",
+           "grad_norm_workspace",           "MATVEC_MAX_ROWS", "LOGPROBS_MAX",
            "NVFP4Error", "MODES", "RULES", "STATS", "FUSED_WS_WORDS", "LIB_PATH"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnvfp4_amax.so")
@@ -367,5 +367,5 @@ from . import train  # noqa: E402  (it uses the helpers above)
 from .train import (ADAMW_BLOCK, AdamWPlan, adamw_plan, adamw_step, distill_loss,  # noqa: E402
                     layer_norm, layer_norm_backward)
 from . import answer  # noqa: E402
-from .answer import (LOGPROBS_MAX, MATVEC_MAX_ROWS, clip_grads, grad_norm, packed_matvec,  # noqa: E402
-                     token_logprobs, token_logprobs_backward)
+from .answer import (LOGPROBS_MAX, MATVEC_MAX_ROWS, clip_grads, grad_norm,  # noqa: E402
+                     grad_norm_workspace, packed_matvec, token_logprobs, token_logprobs_backward)

@@ -24,9 +24,15 @@ from .train import (_BOTH, _F32, TYPES, AdamWPlan, _call, _like, _out, _ptr, _ro
                     _work)
 
 INDICES = {torch.int32: 0, torch.int64: 1}
+_U8 = (torch.uint8,)
 ANSWER_ABI_VERSION = 1          # NVFP4_ANSWER_ABI_VERSION
 MATVEC_MAX_ROWS = 1024          # NVFP4_MATVEC_MAX_ROWS
 LOGPROBS_MAX = 64               # NVFP4_LOGPROBS_MAX
+
+
+def grad_norm_workspace(count: int) -> int:
+    """NVFP4_GRAD_NORM_WORKSPACE(count): bytes of grad_norm's workspace for `count` tensors."""
+    return 16384 * (count // 200 + 1)
 
 
 def bind(L: ctypes.CDLL) -> None:
@@ -46,13 +52,19 @@ def bind(L: ctypes.CDLL) -> None:
     L.nvfp4_token_logprobs.argtypes = [P, i64, P, i64, i64, i64, i64, i32, i32, f32, P, P, P, P, P, P, P]
     L.nvfp4_token_logprobs_backward.argtypes = [P, i64, P, P, P, P, P, i64, i64, i64, i32, i32, f32, P,
                                                 i64, P]
-    L.nvfp4_grad_norm_workspace.argtypes = [P, i64]
-    L.nvfp4_grad_norm_workspace.restype = i64
     L.nvfp4_grad_norm.argtypes = [P, i64, i32, f64, f64, P, P, P, P]
     L.nvfp4_clip_grads.argtypes = [P, P, i64, i32, P, P]
     for name in ("nvfp4_packed_matvec", "nvfp4_token_logprobs", "nvfp4_token_logprobs_backward",
                  "nvfp4_grad_norm", "nvfp4_clip_grads"):
         getattr(L, name).restype = i32
+
+
+def _output(t, shape, dtype, x: torch.Tensor) -> torch.Tensor:
+    """The caller's output, checked, or a new one.  (Sizes one by one: torch takes 1.1 us for these and 1.6
+    for a tuple, and a call has up to five outputs.)"""
+    if t is None and shape:
+        return x.new_empty(*shape, dtype=dtype)
+    return _out(t, shape, dtype, x)
 
 
 def packed_matvec(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, alpha: torch.Tensor, *,
@@ -74,9 +86,9 @@ def packed_matvec(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, al
     if cols % 16:
         raise ValueError("x must have a last dimension that is a multiple of 16")
     E, rows = (1 if expert is None else codes.shape[0]), codes.shape[lead]
-    head = tuple(codes.shape[:lead + 1])
-    _vector(codes, head + (cols // 2,), (torch.uint8,), x, "codes")
-    _vector(scales, head + (cols // 16,), (torch.uint8,), x, "scales")
+    head = (E, rows) if lead else (rows,)
+    _vector(codes, (*head, cols // 2), _U8, x, "codes")
+    _vector(scales, (*head, cols // 16), _U8, x, "scales")
     _vector(alpha, (E,), _F32, x, "alpha")
     tokens, picks, itype = x.numel() // cols, 1, 0
     to = shape[:-1]
@@ -94,7 +106,7 @@ def packed_matvec(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, al
     dtype = x.dtype if dtype is None else dtype
     if dtype not in TYPES:
         raise TypeError("dtype must be bfloat16 or float32, got %s" % dtype)
-    y = _out(y, tuple(to) + (rows,), dtype, x)
+    y = _output(y, (*to, rows), dtype, x)
     if y.numel() == 0:
         return y
     need = lib().nvfp4_packed_matvec_workspace(tokens, cols, kind)
@@ -138,14 +150,14 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor = None, *, top: in
     given, itype = 0, 0
     if tokens is not None:
         given, itype = _given(tokens, lead, logits), INDICES[tokens.dtype]
-        logp = _out(logp, tokens.shape, torch.float32, logits)
+        logp = _output(logp, tokens.shape, torch.float32, logits)
     elif logp is not None:
         raise ValueError("logp is an output of the form with tokens only")
-    entropy = _out(entropy, lead, torch.float32, logits)
-    stats = _out(stats, tuple(lead) + (2,), torch.float32, logits)
+    entropy = _output(entropy, lead, torch.float32, logits)
+    stats = _output(stats, (*lead, 2), torch.float32, logits)
     if top:
-        top_logp = _out(top_logp, tuple(lead) + (top,), torch.float32, logits)
-        top_index = _out(top_index, tuple(lead) + (top,), torch.int64, logits)
+        top_logp = _output(top_logp, (*lead, top), torch.float32, logits)
+        top_index = _output(top_index, (*lead, top), torch.int64, logits)
     elif top_logp is not None or top_index is not None:
         raise ValueError("top_logp and top_index are outputs of the form with top only")
     rows = entropy.numel()
@@ -189,12 +201,16 @@ def token_logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor, stats: t
     return grad
 
 
-def _table(plan: AdamWPlan, grads) -> np.ndarray:
-    """The entries of nvfp4_grad_tensor for these tensors."""
-    table = np.empty((len(grads), 2), np.int64)
-    table[:, 0] = [g.data_ptr() for g in grads]
-    table[:, 1] = plan.numels
-    return table
+def _table(plan: AdamWPlan, name: str, grads) -> int:
+    """The address of the entries of nvfp4_grad_tensor for these tensors, which the plan keeps (read by
+    the library before the call returns)."""
+    table = plan.tables.get(name)
+    if table is None:
+        table = np.empty((len(grads), 2), np.int64)
+        table[:, 1] = plan.numels
+        plan.tables[name] = table = table, table.ctypes.data
+    table[0][:, 0] = [g.data_ptr() for g in grads]
+    return table[1]
 
 
 def _look(plan: AdamWPlan, grads):
@@ -212,14 +228,13 @@ def grad_norm(plan: AdamWPlan, grads, *, max_norm: float = None, eps: float = 1e
     multiplies by; None without max_norm.  Nothing waits for the GPU.  Gradients as in adamw_step."""
     grads, kind = _look(plan, grads)
     like = plan.params[0]
-    norm = _out(norm, (1,), torch.float32, like)
+    norm = _output(norm, (1,), torch.float32, like)
     if max_norm is not None:
-        scale = _out(scale, (1,), torch.float32, like)
+        scale = _output(scale, (1,), torch.float32, like)
     elif scale is not None:
         raise ValueError("scale is an output of the form with max_norm only")
-    table = _table(plan, grads)
-    ws = _work(workspace, lib().nvfp4_grad_norm_workspace(table.ctypes.data, len(grads)), like)
-    _call("nvfp4_grad_norm", like, table.ctypes.data, len(grads), kind,
+    ws = _work(workspace, grad_norm_workspace(len(grads)), like)
+    _call("nvfp4_grad_norm", like, _table(plan, "grads", grads), len(grads), kind,
           0.0 if max_norm is None else max_norm, eps, norm.data_ptr(), _ptr(scale), ws.data_ptr())
     return norm, scale
 
@@ -232,7 +247,7 @@ def clip_grads(plan: AdamWPlan, grads, scale: torch.Tensor, *, out=None):
     grads, kind = _look(plan, grads)
     like = plan.params[0]
     _vector(scale, (1,), _F32, like, "scale")
-    table, to = _table(plan, grads), None
+    table, to = _table(plan, "grads", grads), None
     if out is not None:
         out = list(out)
         if len(out) != len(grads):
@@ -241,7 +256,6 @@ def clip_grads(plan: AdamWPlan, grads, scale: torch.Tensor, *, out=None):
             for t, n in zip(out, plan.numels):
                 plan._look("out", t, n, grads[0].dtype)
             plan._seen_out.keep(out)
-        to = _table(plan, out)
-    _call("nvfp4_clip_grads", like, table.ctypes.data, None if to is None else to.ctypes.data,
-          len(grads), kind, scale.data_ptr())
+        to = _table(plan, "out", out)
+    _call("nvfp4_clip_grads", like, table, to, len(grads), kind, scale.data_ptr())
     return grads if out is None else out

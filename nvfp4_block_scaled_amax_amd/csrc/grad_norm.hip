@@ -41,6 +41,8 @@ struct Batch {
 };
 typedef Batch<Entry, kTable> NormBatch;
 typedef Batch<EntryTo, kTableTo> ToBatch;
+static_assert(NVFP4_GRAD_NORM_WORKSPACE(kTable - 1) == kGroups * 8 && NVFP4_GRAD_NORM_WORKSPACE(kTable) == 2 * kGroups * 8,
+              "a sum for each workgroup of each launch");
 static_assert(sizeof(NormBatch) <= 4096 && sizeof(ToBatch) <= 4096, "kernel arguments");
 
 // The tensor of a chunk, from one that is not after it (uniform).
@@ -178,12 +180,6 @@ bool size_ok(double v) { return v >= 0.0 && v < 3.0e38; }
 
 using namespace train;
 
-NVFP4_EXPORT int64_t nvfp4_grad_norm_workspace(const nvfp4_grad_tensor* tensors, int64_t count) {
-  (void)tensors;
-  if (count <= 0 || count > kMaxCount) return 16;
-  return ((count + kTable - 1) / kTable) * kGroups * 8;
-}
-
 NVFP4_EXPORT nvfp4_status nvfp4_grad_norm(const nvfp4_grad_tensor* tensors, int64_t count,
                                           nvfp4_type type, double max_norm, double eps, float* norm,
                                           float* scale, void* workspace, hipStream_t stream) {
@@ -196,7 +192,7 @@ NVFP4_EXPORT nvfp4_status nvfp4_grad_norm(const nvfp4_grad_tensor* tensors, int6
   nvfp4_status st = look(tensors, count, es);
   if (st != NVFP4_OK) return st;
   const Range out[] = {range(norm, 4), range(scale, 4),
-                       range(workspace, nvfp4_grad_norm_workspace(tensors, count))};
+                       range(workspace, NVFP4_GRAD_NORM_WORKSPACE(count))};
   for (int o = 0; o < 3; ++o) {
     for (int q = 0; q < o; ++q)
       if (overlap(out[o], out[q])) return NVFP4_ERR_ALIAS;

@@ -108,18 +108,27 @@ __device__ __forceinline__ void skip_row(const Args& a, int64_t row) {
   if (i == 0 && a.entropy) a.entropy[row] = 0.0f;
 }
 
-// What a row's statistics give, but for the top alternatives; returns ln Z (NaN: no distribution).
+// A given token and its logit, a lane each.
+struct Given {
+  int64_t id;
+  float x;
+};
 template <typename T>
-__device__ __forceinline__ float finish_row(const Args& a, int64_t row, Stat t) {
+__device__ __forceinline__ Given given_of(const Args& a, int64_t row) {
+  Given g = {-1, 0.0f};
+  if (threadIdx.x < a.given) {
+    g.id = token(a.tokens, a.wide, row * a.given + threadIdx.x);
+    if (g.id >= 0 && g.id < a.vocab) g.x = to_f32(((const T*)a.logits)[row * a.stride + g.id]);
+  }
+  return g;
+}
+
+// What a row's statistics give, but for the top alternatives; returns ln Z (NaN: no distribution).
+__device__ __forceinline__ float finish_row(const Args& a, int64_t row, Stat t, Given g) {
   const float z = t.good() ? logf(t.z) : NAN, m = t.good() ? t.m : NAN;
   const int i = threadIdx.x;
-  if (i < a.given) {
-    const int64_t id = token(a.tokens, a.wide, row * a.given + i);
-    float v = 0.0f;
-    if (id >= a.vocab) v = NAN;
-    else if (id >= 0) v = (to_f32(((const T*)a.logits)[row * a.stride + id]) - m) * a.inv_t - z;
-    a.logp[row * a.given + i] = v;
-  }
+  if (i < a.given)
+    a.logp[row * a.given + i] = g.id < 0 ? 0.0f : g.id >= a.vocab ? NAN : (g.x - m) * a.inv_t - z;
   if (i == 0) {
     a.stats[row * 2] = m;
     a.stats[row * 2 + 1] = z;
@@ -128,15 +137,30 @@ __device__ __forceinline__ float finish_row(const Args& a, int64_t row, Stat t) 
   return z;
 }
 
-constexpr int kColumns = 256;
-constexpr int kHeld = 1024;               // candidates in shared memory
+template <int THREADS>
+constexpr int kHeld = THREADS == 64 ? 512 : 1024;        // candidates in shared memory
 
+template <int THREADS>
 struct TopShared {
-  uint64_t column[kColumns];
-  uint64_t held[kHeld];
-  uint32_t owner[kMost];
-  uint64_t limit, best[16];
-  int count;
+  uint64_t cell[THREADS], best[THREADS / 64], limit;
+  uint64_t held[kHeld<THREADS>];
+  u32x4 vector[kHeld<THREADS> / 4];                      // those that may hold candidates
+  uint32_t place[kHeld<THREADS> / 4], owner[THREADS];
+  int owners, vectors, count;
+};
+
+// A row's part in cells: the threads of a group of G neighbours, in one of G blocks of steps (a step is a
+// vector of every thread).  There are as many cells as threads; a cell's vectors lie G together.
+template <int THREADS, int N>
+struct Cells {
+  uint32_t steps, block;             // of the part; of a block, a multiple of kStepsAhead
+  int bits;                          // log2 G
+  static constexpr uint32_t kStepsAhead = 4;
+  __device__ __forceinline__ Cells(uint32_t size) {
+    steps = (size + THREADS * N - 1) / (THREADS * N);
+    bits = steps < 2 * kStepsAhead ? 0 : steps < 4 * kStepsAhead ? 1 : steps < 8 * kStepsAhead ? 2 : 3;
+    block = (((steps + (1u << bits) - 1) >> bits) + kStepsAhead - 1) / kStepsAhead * kStepsAhead;
+  }
 };
 
 // The places of `count` numbers among themselves: put(place, number) for the first `top`.
@@ -145,89 +169,157 @@ __device__ __forceinline__ void rank(const uint64_t* held, int count, int top, P
   for (int i = threadIdx.x; i < count; i += THREADS) {
     const uint64_t mine = held[i];
     int before = 0;
+#pragma unroll 4
     for (int j = 0; j < count; ++j) before += held[j] > mine;
     if (before < top) put(before, mine);
   }
 }
 
-// The top entries of a row's part [lo, hi), from each thread's largest entry and its place.
+// A lower bound for the top-th largest of PER numbers of each lane of a wavefront, none of them equal but for 0:
+// `top` or somewhat more of them reach it (0 where fewer are not 0).  Bit by bit, first the entries' 32 and, where
+// too many are left by equal entries, the places'.
+template <int PER>
+__device__ __forceinline__ uint64_t threshold(const uint64_t (&key)[PER], int top) {
+  const int enough = top + 4 + top / 4;
+  uint32_t t = 0;
+  int have = 64 * PER;
+  for (uint32_t bit = 1u << 31; bit && have > enough; bit >>= 1) {
+    const uint32_t next = t | bit;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) n += __popcll(__ballot((uint32_t)(key[i] >> 32) >= next));
+    if (n >= top) t = next, have = n;
+  }
+  uint64_t low = (uint64_t)t << 32;
+  if (t == 0) return low;
+  for (uint32_t bit = 1u << 31; bit && have > enough; bit >>= 1) {
+    const uint64_t next = low | bit;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) n += __popcll(__ballot(key[i] >= next));
+    if (n >= top) low = next, have = n;
+  }
+  return low;
+}
+
+// The top entries of a row's part [lo, hi), from each cell's largest entry and its place (sh.cell).
 // put(place, key) for all of them, at most once each.
-template <typename T, int THREADS, typename Put>
-__device__ __forceinline__ void find_top(const T* row, uint32_t lo, uint32_t hi, int top, uint64_t mine,
-                                         TopShared& sh, Put put) {
-  constexpr int N = 16 / sizeof(T);
-  constexpr int kPer = THREADS > kColumns ? THREADS / kColumns : 1;      // threads of a column
-  constexpr int kHave = THREADS / kPer;
-  // columns of neighbouring threads
-#pragma unroll
-  for (int d = 1; d < kPer; d *= 2) {
-    const uint64_t other = __shfl_xor((unsigned long long)mine, d);
-    mine = other > mine ? other : mine;
-  }
-  if (threadIdx.x % kPer == 0) sh.column[threadIdx.x / kPer] = mine;
-  if (threadIdx.x == 0) sh.count = 0, sh.limit = 0;
-  if (threadIdx.x < kMost) sh.owner[threadIdx.x] = ~0u;
+template <typename T, int THREADS, int N, typename Put>
+__device__ __forceinline__ void find_top(const T* row, uint32_t lo, uint32_t hi, int top, Cells<THREADS, N> cells,
+                                         TopShared<THREADS>& sh, Put put) {
+  constexpr int WAVES = THREADS / 64;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   __syncthreads();
-  if (threadIdx.x < kHave) {
-    const uint64_t k = sh.column[threadIdx.x];
-    if (k) {
-      int before = 0;
-#pragma unroll 8
-      for (int j = 0; j < kHave; ++j) before += sh.column[j] > k;
-      if (before < top) sh.owner[before] = threadIdx.x;
-      if (before == top - 1) sh.limit = k;
+  if (wave == 0) {
+    uint64_t key[WAVES];
+#pragma unroll
+    for (int i = 0; i < WAVES; ++i) key[i] = sh.cell[i * 64 + lane];
+    const uint64_t limit = threshold(key, top);
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < WAVES; ++i) {
+      const bool in = key[i] && key[i] >= limit;
+      const uint64_t all = __ballot(in);
+      if (in) sh.owner[n + __popcll(all & ((uint64_t(1) << lane) - 1))] = i * 64 + lane;
+      n += __popcll(all);
     }
+    if (lane == 0) sh.owners = n, sh.limit = limit, sh.count = 0, sh.vectors = 0;
   }
   __syncthreads();
-  // fewer columns than `top`: everything is a candidate
+  // an entry above the limit's, or equal to it and no further than its vector, is a candidate (of fewer columns
+  // than `top`, and of less than that many entries at all, everything is)
   const uint64_t limit = sh.limit;
-  const uint32_t low = (uint32_t)(limit >> 32), until = limit ? ~(uint32_t)limit + N : ~0u;
-  const uint32_t vectors = (hi - lo + N - 1) / N;                     // of the part
-  const uint32_t deep = (vectors + THREADS - 1) / THREADS;            // of a thread
-  const uint32_t total = deep * kPer * top;
+  const int owners = sh.owners;
+  const uint32_t low = (uint32_t)(limit >> 32);
+  const uint32_t until = (uint32_t)limit ? ~(uint32_t)limit + N : ~0u;
+  const int block_bits = cells.block < 2 ? 0 : 32 - __builtin_clz(cells.block - 1);
+  const int deep_bits = block_bits + cells.bits;        // vectors of a cell, of which some may not be there
+  // f(vector, place) for the owners' vectors, -inf past the end
   const auto visit = [&](auto f) {
-    for (uint32_t i = threadIdx.x; i < total; i += THREADS) {
-      const uint32_t owner = sh.owner[i % top], t = i / top;
-      if (owner == ~0u) continue;
-      const uint32_t at = lo + ((t / kPer) * THREADS + owner * kPer + t % kPer) * N;
-      if (at >= hi) continue;
-      if (at + N <= hi) {
-        const Vec<T, N> v = load_vec<N>(row + at);
+    constexpr uint32_t kAhead = 4;                     // vectors in flight per thread
+    constexpr int kThreadBits = THREADS == 64 ? 6 : 8;
+    static_assert(THREADS == 1 << kThreadBits, "");
+    const uint32_t total = (uint32_t)owners << deep_bits;
+    for (uint32_t i = threadIdx.x; i < total; i += THREADS * kAhead) {
+      Vec<T, N> v[kAhead];
+      uint32_t at[kAhead];
 #pragma unroll
-        for (int j = 0; j < N; ++j) f(v[j], at + j);
-      } else {
-        for (uint32_t j = at; j < hi; ++j) f(to_f32(row[j]), j);
+      for (uint32_t k = 0; k < kAhead; ++k) {
+        const uint32_t j = i + k * THREADS, owner = j < total ? sh.owner[j >> deep_bits] : 0;
+        const uint32_t t = j & ((1u << deep_bits) - 1), in = t >> cells.bits;          // step of the block
+        const uint32_t group = owner & ((THREADS >> cells.bits) - 1), block = owner >> (kThreadBits - cells.bits);
+        const uint32_t step = block * cells.block + in;
+        at[k] = j < total && in < cells.block && step < cells.steps
+                    ? lo + (step * THREADS + (group << cells.bits) + (t & ((1u << cells.bits) - 1))) * N
+                    : hi;
+        at[k] = min(at[k], hi);
+        if (at[k] + N <= hi) v[k] = load_vec<N>(row + at[k]);
+      }
+#pragma unroll
+      for (uint32_t k = 0; k < kAhead; ++k) {
+        if (at[k] + N <= hi) {
+          f(v[k], at[k]);
+        } else if (at[k] < hi) {
+          float w[N];
+#pragma unroll
+          for (int j = 0; j < N; ++j) w[j] = at[k] + j < hi ? to_f32(row[at[k] + j]) : -INFINITY;
+          f(make_vec<T>(w), at[k]);
+        }
       }
     }
   };
-  visit([&](float x, uint32_t at) {
-    const uint32_t o = order(x);
-    if (o > low || (o == low && at < until)) {
-      const int n = atomicAdd(&sh.count, 1);
-      if (n < kHeld) sh.held[n] = (uint64_t)o << 32 | (uint32_t)~at;
+  // vectors with an entry that reaches the limit, and of these the candidates
+  const float least = low ? entry(low) : -INFINITY;
+  constexpr int kVectors = kHeld<THREADS> / 4;
+  visit([&](const Vec<T, N>& v, uint32_t at) {
+    float most = v[0];
+#pragma unroll
+    for (int j = 1; j < N; ++j) most = fmaxf(most, v[j]);
+    if (most >= least) {
+      const int n = atomicAdd(&sh.vectors, 1);
+      if (n < kVectors) {
+        sh.vector[n] = u32x4{v.w[0], v.w[1], v.w[2], v.w[3]};
+        sh.place[n] = at;
+      }
     }
   });
   __syncthreads();
-  const int count = sh.count;
-  if (count <= kHeld) {
-    rank<THREADS>(sh.held, count, top, put);
-    return;
+  const int vectors = sh.vectors;
+  if (vectors <= kVectors) {
+    for (int i = threadIdx.x; i < vectors * N; i += THREADS) {
+      const uint32_t at = sh.place[i / N];
+      const T* held = (const T*)&sh.vector[i / N];
+      const uint32_t o = order(to_f32(held[i % N]));
+      if (at + i % N < hi && (o > low || (o == low && at + i % N < until))) {
+        const int n = atomicAdd(&sh.count, 1);
+        if (n < kHeld<THREADS>) sh.held[n] = (uint64_t)o << 32 | (uint32_t)~(at + i % N);
+      }
+    }
+    __syncthreads();
+    if (sh.count <= kHeld<THREADS>) {
+      rank<THREADS>(sh.held, sh.count, top, put);
+      return;
+    }
   }
+  // more than fit: one by one
   uint64_t last = ~uint64_t(0);
   for (int k = 0; k < top; ++k) {
     uint64_t best = 0;
-    visit([&](float x, uint32_t at) {
-      const uint64_t n = key_of(x, at);
-      if (n < last && n > best) best = n;
+    visit([&](const Vec<T, N>& v, uint32_t at) {
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const uint64_t n = at + j < hi ? key_of(v[j], at + j) : 0;
+        if (n < last && n > best) best = n;
+      }
     });
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
       const uint64_t other = __shfl_xor((unsigned long long)best, d);
       best = other > best ? other : best;
     }
-    if ((threadIdx.x & 63) == 0) sh.best[threadIdx.x >> 6] = best;
+    if (lane == 0) sh.best[wave] = best;
     __syncthreads();
-    for (int w = 0; w < THREADS / 64; ++w) best = sh.best[w] > best ? sh.best[w] : best;
+    for (int w = 0; w < WAVES; ++w) best = sh.best[w] > best ? sh.best[w] : best;
     if (threadIdx.x == 0) put(k, best);
     last = best;
     __syncthreads();
@@ -250,26 +342,40 @@ template <typename T, int THREADS, bool TOP, bool SPLIT>
 __global__ __launch_bounds__(THREADS) void forward_kernel(const Args a) {
   constexpr int N = 16 / sizeof(T);
   __shared__ Stat slots[THREADS / 64];
-  __shared__ TopShared sh;
+  __shared__ TopShared<THREADS> sh;
   const int64_t row = SPLIT ? (int64_t)blockIdx.y : (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
   if (row >= a.rows) return;
-  if (!is_read(a.tokens, a.wide, a.given, row)) {
-    if (!SPLIT) skip_row(a, row);
-    return;
-  }
+  if (!SPLIT && !is_read(a.tokens, a.wide, a.given, row)) return skip_row(a, row);
   const T* x = (const T*)a.logits + row * a.stride;
   const uint32_t lo = SPLIT ? min(blockIdx.x * a.split_size, a.vocab) : 0;
   const uint32_t hi = SPLIT ? min(lo + a.split_size, a.vocab) : a.vocab;
   Stat t{kLowest, 0.0f, 0.0f};
-  // the thread's largest entry, and the first vector that holds it
+  // the thread's largest entry of a block, and the first vector that holds it
+  const Cells<THREADS, N> cells(hi - lo);
+  constexpr uint32_t step = THREADS * N;
+  const uint32_t start = lo + threadIdx.x * N;
   float most = -INFINITY;
-  uint32_t place = lo + threadIdx.x * N;
-  const bool any = place < hi;
+  uint32_t place = start;
+  const auto flush = [&](uint32_t block) {            // of the block that ends; then the next begins
+    uint64_t key = place < hi ? key_of(most, place) : 0;
+    for (int d = 1; d < 1 << cells.bits; d *= 2) {
+      const uint64_t other = __shfl_xor((unsigned long long)key, d);
+      key = other > key ? other : key;
+    }
+    if ((threadIdx.x & ((1 << cells.bits) - 1)) == 0)
+      sh.cell[(block * THREADS + threadIdx.x) >> cells.bits] = key;
+    most = -INFINITY;
+    place = start + (block + 1) * cells.block * step;
+  };
+  if (TOP) {
+    sh.cell[threadIdx.x] = 0;
+    __syncthreads();
+  }
   const auto unit = [&](const Vec<T, N>& v, uint32_t at) {
     float top = v[0];
 #pragma unroll
     for (int i = 1; i < N; ++i) top = fmaxf(top, v[i]);
-    if (top > most) {
+    if (top > (TOP ? most : t.m)) {
       most = top;
       place = at;
       if (top > t.m) t.raise(top, a.c);
@@ -277,28 +383,66 @@ __global__ __launch_bounds__(THREADS) void forward_kernel(const Args a) {
 #pragma unroll
     for (int i = 0; i < N; ++i) t.add(v[i], a.c);
   };
-  constexpr int kAhead = 4;                         // vectors in flight per thread
-  uint32_t at = lo + threadIdx.x * N;
-  const uint32_t step = THREADS * N;
-  for (; at + (kAhead - 1) * step + N <= hi; at += kAhead * step) {
+  // vectors are loaded kAhead at a time, the next ones before these are looked at
+  constexpr int kAhead = Cells<THREADS, N>::kStepsAhead;
+  struct Batch {
     Vec<T, N> v[kAhead];
+  };
+  const auto load = [&](uint32_t at) {
+    Batch b;
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) v[k] = load_vec<N>(x + at + k * step);
+    for (int k = 0; k < kAhead; ++k) b.v[k] = load_vec<N>(x + at + k * step);
+    return b;
+  };
+  const auto load_rest = [&](uint32_t at) {
+    Batch b = {};
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) unit(v[k], at + k * step);
+    for (int k = 0; k < kAhead; ++k)
+      if (at + k * step + N <= hi) b.v[k] = load_vec<N>(x + at + k * step);
+    return b;
+  };
+  const uint32_t batches = (hi - lo) / (step * kAhead);          // that all threads have
+  uint32_t at = start, block = 0;
+  Batch now = batches ? load(at) : load_rest(at);
+  // (a part of a row is on its way before it is known whether the row is read)
+  if (SPLIT && !is_read(a.tokens, a.wide, a.given, row)) return;
+  Given given = {-1, 0.0f};
+  if (!SPLIT) given = given_of<T>(a, row);
+  uint32_t in = 0;
+  const auto take = [&] {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) unit(now.v[k], at + k * step);
+    at += kAhead * step;
+    in += kAhead;
+    if (TOP && in == cells.block) {
+      flush(block++);
+      in = 0;
+    }
+  };
+  if (batches) {
+    for (uint32_t i = 1; i < batches; ++i) {
+      const Batch next = load(at + kAhead * step);
+      take();
+      now = next;
+    }
+    const Batch next = load_rest(at + kAhead * step);
+    take();
+    now = next;
   }
-  for (; at < hi; at += step) {
-    if (at + N <= hi) {
-      unit(load_vec<N>(x + at), at);
-    } else {
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) {
+    const uint32_t to = at + k * step;
+    if (to + N <= hi) {
+      unit(now.v[k], to);
+    } else if (to < hi) {
       float w[N];
 #pragma unroll
-      for (int i = 0; i < N; ++i) w[i] = at + i < hi ? to_f32(x[at + i]) : -INFINITY;
-      unit(make_vec<T>(w), at);
+      for (int i = 0; i < N; ++i) w[i] = to + i < hi ? to_f32(x[to + i]) : -INFINITY;
+      unit(make_vec<T>(w), to);
     }
   }
+  if (TOP && block * cells.block < cells.steps) flush(block);
   const Stat whole = join_group<THREADS / 64>(t, a.c, slots);
-  const uint64_t mine = any ? key_of(most, place) : 0;
   if (SPLIT) {
     if (threadIdx.x == 0) {
       float* out = a.part + (row * a.splits + blockIdx.x) * 4;
@@ -307,13 +451,13 @@ __global__ __launch_bounds__(THREADS) void forward_kernel(const Args a) {
     if (TOP) {
       uint64_t* keys = a.keys + (row * a.splits + blockIdx.x) * a.top;
       if (threadIdx.x < a.top && threadIdx.x >= hi - lo) keys[threadIdx.x] = 0;      // a short last part
-      find_top<T, THREADS>(x, lo, hi, a.top, mine, sh, [&](int p, uint64_t k) { keys[p] = k; });
+      find_top<T, THREADS, N>(x, lo, hi, a.top, cells, sh, [&](int p, uint64_t k) { keys[p] = k; });
     }
   } else {
-    const float z = finish_row<T>(a, row, whole);
+    const float z = finish_row(a, row, whole, given);
     if (!TOP) return;
     if (!whole.good()) return no_top(a, row);
-    find_top<T, THREADS>(x, lo, hi, a.top, mine, sh,
+    find_top<T, THREADS, N>(x, lo, hi, a.top, cells, sh,
                          [&](int p, uint64_t k) { put_top(a, row, whole, z, p, k); });
   }
 }
@@ -328,6 +472,7 @@ __global__ __launch_bounds__(256) void join_kernel(const Args a) {
   __shared__ int count;
   const int64_t row = blockIdx.x;
   if (!is_read(a.tokens, a.wide, a.given, row)) return skip_row(a, row);
+  const Given given = given_of<T>(a, row);
   // a lane of every wavefront takes a part
   const int lane = threadIdx.x & 63;
   Stat t{kLowest, 0.0f, 0.0f};
@@ -335,23 +480,26 @@ __global__ __launch_bounds__(256) void join_kernel(const Args a) {
     const float* in = a.part + (row * a.splits + lane) * 4;
     t = Stat{in[0], in[1], in[2]};
   }
+  // the k-th largest of the first few of each list is a lower bound for all
+  const uint64_t* keys = a.keys + row * a.splits * a.top;
+  const int first = min(a.top, 256 / a.splits), some = first * a.splits;
+  uint64_t key[4] = {0, 0, 0, 0};
+  if (threadIdx.x < 64) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int j = i * 64 + lane;
+      if (j < some) key[i] = keys[j / first * a.top + j % first];
+    }
+  }
   t.raise(reduce64(t.m, Max()), a.c);
   t.z = reduce64(t.z, Sum());
   t.s = reduce64(t.s, Sum());
-  const float z = finish_row<T>(a, row, t);
+  const float z = finish_row(a, row, t, given);
   if (!a.top) return;
   if (!t.good()) return no_top(a, row);
-  // the k-th largest of the first few of each list is a lower bound for all
-  const uint64_t* keys = a.keys + row * a.splits * a.top;
-  const int first = min(a.top, max(4, (a.top + a.splits - 1) / a.splits)), some = first * a.splits;
-  if (threadIdx.x == 0) limit = 1, count = 0;
-  for (int i = threadIdx.x; i < some; i += 256) held[i] = keys[i / first * a.top + i % first];
-  __syncthreads();
-  for (int i = threadIdx.x; i < some; i += 256) {
-    const uint64_t mine = held[i];
-    int before = 0;
-    for (int j = 0; j < some; ++j) before += held[j] > mine;
-    if (before == a.top - 1 && mine) limit = mine;
+  if (threadIdx.x < 64) {
+    const uint64_t t = threshold(key, a.top);
+    if (lane == 0) limit = t ? t : 1, count = 0;
   }
   __syncthreads();
   const uint64_t least = limit;
@@ -391,18 +539,32 @@ __global__ __launch_bounds__(256) void backward_kernel(const BackArgs a) {
   const uint32_t lo = blockIdx.x * a.split_size, hi = min(lo + a.split_size, a.vocab);
   const T* x = (const T*)a.logits + row * a.stride;
   T* grad = (T*)a.grad + row * a.grad_stride;
+  constexpr int kAhead = 4;
+  uint32_t at = lo + threadIdx.x * N;
+  constexpr uint32_t step = THREADS * N;
+  const auto whole_batch = [&](uint32_t at) { return at + (kAhead - 1) * step + N <= hi; };
+  struct Batch {
+    Vec<T, N> v[kAhead];
+  };
+  const auto load = [&](uint32_t at) {
+    Batch b;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) b.v[k] = load_vec<N>(x + at + k * step);
+    return b;
+  };
   const int i = threadIdx.x & 63;
   int64_t mine = -1;
-  float g = 0.0f;
-  if (i < a.given) {
-    mine = token(a.tokens, a.wide, row * a.given + i);
-    g = mine < 0 ? 0.0f : a.dlogp[row * a.given + i];
-  }
+  if (i < a.given) mine = token(a.tokens, a.wide, row * a.given + i);
   if (__ballot(mine >= 0) == 0) {
     const Vec<T, N> zero = zero_vec<T, N>();
-    for (uint32_t at = lo + threadIdx.x * N; at < hi; at += THREADS * N) store_vec<kAny>(grad, at, hi, zero);
+    for (; at < hi; at += step) store_vec<kAny>(grad, at, hi, zero);
     return;
   }
+  // the first vectors are on their way while the row's numbers come
+  bool more = whole_batch(at);
+  Batch now = {};
+  if (more) now = load(at);
+  float g = mine < 0 ? 0.0f : a.dlogp[row * a.given + i];
   if (mine >= (int64_t)a.vocab) g = NAN;
   const float m = a.stats[row * 2], z = a.stats[row * 2 + 1];
   const float h = a.dentropy ? a.dentropy[row] : 0.0f, all = reduce64(g, Sum());
@@ -410,8 +572,8 @@ __global__ __launch_bounds__(256) void backward_kernel(const BackArgs a) {
   float B = a.dentropy ? -fmaf(h, a.entropy[row], all) * a.inv_t : -all * a.inv_t;
   if (!(z == z)) B = NAN;                          // no distribution
   const float z2 = z * kLog2e;
-  const auto value = [&](float v) {
-    const float y = fmaxf(fmaf(v - m, a.c, -z2), kNone);
+  const auto value = [&](float e) {
+    const float y = fmaxf(fmaf(e - m, a.c, -z2), kNone);
     return exp2_(y) * fmaf(A, y, B);
   };
   // the first of equal tokens in this part takes their sum
@@ -432,21 +594,20 @@ __global__ __launch_bounds__(256) void backward_kernel(const BackArgs a) {
     if (fixes) fix = fmaf(fix, a.inv_t, value(to_f32(x[mine])));
   }
   __syncthreads();
-  constexpr int kAhead = 4;
-  uint32_t at = lo + threadIdx.x * N;
-  constexpr uint32_t step = THREADS * N;
   const auto unit = [&](const Vec<T, N>& v, uint32_t to) {
     float r[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) r[k] = value(v[k]);
     store_vec<kAny>(grad, to, hi, make_vec<T>(r));
   };
-  for (; at + (kAhead - 1) * step + N <= hi; at += kAhead * step) {
-    Vec<T, N> v[kAhead];
+  while (more) {
+    const uint32_t then = at + kAhead * step;
+    more = whole_batch(then);
+    const Batch next = load(more ? then : at);
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) v[k] = load_vec<N>(x + at + k * step);
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) unit(v[k], at + k * step);
+    for (int k = 0; k < kAhead; ++k) unit(now.v[k], at + k * step);
+    at = then;
+    now = next;
   }
   for (; at < hi; at += step) unit(load_vec<N, kAny>(x, at, hi), at);
   __syncthreads();
@@ -479,7 +640,9 @@ void launch_forward(const Args& a, hipStream_t s) {
   }
   constexpr int64_t kLine = 1 << 20;                // workgroups in x: threads stay below 2^32
   const dim3 grid((unsigned)(a.rows < kLine ? a.rows : kLine), (unsigned)((a.rows + kLine - 1) / kLine));
-  launch_forward<T, 256, false>(a, grid, s);
+  // a wavefront to a row of up to 16 vectors a lane
+  if (a.vocab <= 64 * 16 * (16 / sizeof(T)) && a.top <= 24) launch_forward<T, 64, false>(a, grid, s);
+  else launch_forward<T, 256, false>(a, grid, s);
 }
 
 bool temperature_ok(float temperature, float& inv_t, float& c) {

@@ -37,8 +37,7 @@ def test_library_exports_what_the_header_declares(L):
     names = set(re.findall(r"^(?:nvfp4_status|int|int64_t|const char\*)\s+(nvfp4_\w+)\s*\(", text, re.M))
     assert names == {"nvfp4_answer_abi_version", "nvfp4_packed_matvec_workspace", "nvfp4_packed_matvec",
                      "nvfp4_token_logprobs_workspace", "nvfp4_token_logprobs",
-                     "nvfp4_token_logprobs_backward", "nvfp4_grad_norm_workspace", "nvfp4_grad_norm",
-                     "nvfp4_clip_grads"}
+                     "nvfp4_token_logprobs_backward", "nvfp4_grad_norm", "nvfp4_clip_grads"}
     for n in names:
         assert hasattr(L, n), n
     assert L.nvfp4_answer_abi_version() == 1
@@ -169,7 +168,9 @@ def test_workspace_sizes_need_no_gpu(L):
     assert L.nvfp4_token_logprobs_workspace(1, 0, 5) == 0
     assert L.nvfp4_token_logprobs_workspace(4096, 100000, 5) == 0
     assert L.nvfp4_token_logprobs_workspace(1, 128000, 64) > 0
-    assert L.nvfp4_grad_norm_workspace(None, 0) > 0
+    macro = re.search(r"#define NVFP4_GRAD_NORM_WORKSPACE\(count\) (.*)", open(HEADER).read()).group(1)
+    for count in (0, 1, 199, 200, 201, 100000):
+        assert nv.grad_norm_workspace(count) == eval(macro.replace("(int64_t)(count) /", "count //"))
 
 
 def test_python_refusals():
