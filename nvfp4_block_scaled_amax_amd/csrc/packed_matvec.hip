@@ -82,37 +82,48 @@ __global__ __launch_bounds__(W * 64) void matvec_kernel(const Matvec a) {
   constexpr int kCols = FEW ? 4 : 16;                // of a tile
   constexpr int S = FEW ? 4 : 1;
   extern __shared__ __align__(16) char held[];       // x, then the wavefronts' sums
-  __shared__ uint16_t list[EXPERT ? kMaxRows : 1];
-  __shared__ int counts[2], x_row[EXPERT ? 64 : 1];
+  // the rows of y that go to this expert, in order, and behind the end those that go nowhere; their tokens
+  __shared__ uint16_t list[EXPERT ? kMaxRows : 1], tokens[EXPERT ? kMaxRows : 1];
+  __shared__ int counts[2];
   __shared__ u32x4 zeros[FEW ? 16 : 1];
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int deal = 1 << a.deal, wr = wave >> a.deal, wk = wave & (deal - 1);
   const int e = EXPERT ? blockIdx.y : 0;
   const int64_t row0 = (int64_t)blockIdx.x * (W * 16 >> a.deal);      // the workgroup's first weight row
+  const float alpha = a.alpha[e];
   int count = a.out_rows;
   if (EXPERT) {
-    // the rows that go to this expert, in order; behind the end those that go nowhere (expert 0's
-    // workgroups write their zeros)
     if (wave == 0) {
       int n = 0, none = 0;
-      for (int base = 0; base < a.out_rows; base += 64) {
-        const int m = base + lane;
-        int64_t id = -1;
-        if (m < a.out_rows) id = a.wide ? ((const int64_t*)a.expert)[m] : ((const int32_t*)a.expert)[m];
-        const bool mine = m < a.out_rows && id == e;
-        const bool lost = m < a.out_rows && e == 0 && (id < 0 || id >= a.experts);
-        const uint64_t got = __ballot(mine), gone = __ballot(lost), below = (uint64_t(1) << lane) - 1;
-        if (mine) list[n + __popcll(got & below)] = (uint16_t)m;
-        if (lost) list[kMaxRows - 1 - none - __popcll(gone & below)] = (uint16_t)m;
-        n += __popcll(got);
-        none += __popcll(gone);
+      constexpr int kAhead = 4;
+      for (int base = 0; base < a.out_rows; base += 64 * kAhead) {
+        int64_t id[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const int m = min(base + k * 64 + lane, a.out_rows - 1);
+          id[k] = a.wide ? ((const int64_t*)a.expert)[m] : ((const int32_t*)a.expert)[m];
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const int m = base + k * 64 + lane;
+          const bool mine = m < a.out_rows && id[k] == e;
+          const bool lost = m < a.out_rows && e == 0 && (id[k] < 0 || id[k] >= a.experts);
+          const uint64_t got = __ballot(mine), gone = __ballot(lost), below = (uint64_t(1) << lane) - 1;
+          if (mine) {
+            list[n + __popcll(got & below)] = (uint16_t)m;
+            tokens[n + __popcll(got & below)] = (uint16_t)(m / a.picks);
+          }
+          if (lost) list[kMaxRows - 1 - none - __popcll(gone & below)] = (uint16_t)m;
+          n += __popcll(got);
+          none += __popcll(gone);
+        }
       }
       if (lane == 0) counts[0] = n, counts[1] = none;
     }
     __syncthreads();
     count = counts[0];
-    for (int i = 0; i < counts[1]; ++i) {
+    for (int i = 0; i < counts[1]; ++i) {              // expert 0's workgroups write zeros
       const int64_t m = list[kMaxRows - 1 - i];
       for (int64_t j = row0 + threadIdx.x; j < row0 + (W * 16 >> a.deal) && j < a.rows; j += W * 64) {
         if (a.f32) ((float*)a.y)[m * a.rows + j] = 0.0f;
@@ -187,11 +198,6 @@ __global__ __launch_bounds__(W * 64) void matvec_kernel(const Matvec a) {
     // x: all of it, or as many elements of each column as fit, a multiple of a turn
     const int fit = (a.lds / wide - 16) / 2, chunk = (fit >= all * kUnit ? all * kUnit : fit / turn * turn) / kUnit;
     const int pitch = chunk * (kUnit * 2) + 16;
-    if (EXPERT) {
-      for (int col = threadIdx.x; col < wide; col += W * 64)
-        x_row[col] = list[first + col / a.group] / a.picks * a.group + col % a.group;
-      __syncthreads();
-    }
     // A wavefront stages units of columns: with `beside` wavefronts to a column it takes every beside-th
     // unit of every (W / beside)-th column, kAhead at a time.  The first ones are asked for before the
     // weights: loads come back in order.
@@ -216,7 +222,9 @@ __global__ __launch_bounds__(W * 64) void matvec_kernel(const Matvec a) {
       for (int k = 0; k < kAhead; ++k) {
         const int col = min(p.col, wide - 1), unit = min(from + min(p.unit, chunk - 1), all - 1);
         const int at = start(unit) + lane * 8;
-        const int64_t row = EXPERT ? __builtin_amdgcn_readfirstlane(x_row[col]) : first * a.group + col;
+        const int i = a.group == 1 ? col : col / 3;
+        const int64_t row = EXPERT ? __builtin_amdgcn_readfirstlane(tokens[first + i]) * a.group + (col - i * a.group)
+                                   : first * a.group + col;
         const uint16_t* x = a.x + row * a.x_stride;
         v[k] = *(const u32x4_a2*)(x + (uint32_t)(SHORT ? min(at, cols - 8) : at));
         const bool fresh = SHORT ? at < cols : at >= unit * kUnit;
@@ -347,7 +355,6 @@ __global__ __launch_bounds__(W * 64) void matvec_kernel(const Matvec a) {
       }
     }
     __syncthreads();
-    const float alpha = a.alpha[e];
     constexpr int kRowBits = 4 + (W == 16 ? 4 : W == 8 ? 3 : 2);
     const int row_bits = kRowBits - a.deal;          // the workgroup's weight rows
     for (int o = threadIdx.x; o < here << row_bits; o += W * 64) {
@@ -401,12 +408,13 @@ template <bool FEW, int MT, int W, int DEPTH, bool EXPERT, bool SHORT = false>
 void launch(Matvec a, int64_t columns, int room, int deal, hipStream_t stream) {
   const int64_t tiles = (a.rows + 15) / 16, units = (a.cols + kUnit - 1) / kUnit;
   const auto turn = [](int deal) { return (kUnit * DEPTH * 2 << deal) + 16; };     // bytes of a column
+  const int64_t hit = a.experts < a.out_rows ? a.experts : a.out_rows;       // weights that are read
   // enough workgroups for the compute units: where the rows are few, more wavefronts deal a tile's units, as
   // far as there are units and every column fits
   constexpr int kMany = 192;
   a.deal = units > 1 ? deal : 0;
   while ((2 << a.deal) <= W && (1 << a.deal) < units && !SHORT && columns * turn(a.deal + 1) <= room &&
-         a.experts * ((tiles << a.deal) / W) < kMany)
+         hit * ((tiles << a.deal) / W) < kMany)
     ++a.deal;
   // all of x, or what there is
   const int64_t want = columns * (units * (2 * kUnit) + 16);
@@ -474,13 +482,14 @@ NVFP4_EXPORT nvfp4_status nvfp4_packed_matvec(const void* x, int64_t x_stride, c
     a.x_stride = cols;
     a.group = 3;
   }
-  constexpr int kOne = 150 * 1024, kFive = 30 * 1024;
+  constexpr int kOne = 150 * 1024, kFour = 40 * 1024;
   if (expert) {
     // what an expert gets is not known here: twice its share
     const int64_t columns = (2 * out_rows + E - 1) / E * a.group;
     if (cols < kUnit) launch<false, 1, 4, 1, true, true>(a, 16, kOne, 0, stream);
-    else if (columns <= 16) launch<false, 1, 4, 2, true>(a, columns, kFive, 0, stream);
-    else if (columns <= 32) launch<false, 2, 8, 2, true>(a, columns, kOne / 2, 0, stream);
+    else if (columns <= 4 && rows * (E < out_rows ? E : out_rows) <= 16384) launch<true, 1, 4, 1, true>(a, 4, kFour, 1, stream);
+    else if (columns <= 16) launch<false, 1, 4, 1, true>(a, 16, kFour, 0, stream);
+    else if (columns <= 32) launch<false, 2, 8, 2, true>(a, 32, kOne / 2, 0, stream);
     else launch<false, 4, 8, 1, true>(a, 64, kOne, 0, stream);
   } else {
     const int64_t columns = out_rows * a.group;
@@ -490,7 +499,7 @@ NVFP4_EXPORT nvfp4_status nvfp4_packed_matvec(const void* x, int64_t x_stride, c
     else if (columns <= 4) launch<true, 1, 8, 1, false>(a, columns, kOne, 1, stream);
     else if (columns <= 8 && rows < 16384) launch<true, 2, 8, 2, false>(a, columns, kOne, 0, stream);
     else if (columns <= 16) launch<false, 1, 16, 1, false>(a, columns, kOne, 0, stream);
-    else if (columns <= 32) launch<false, 2, 16, 1, false>(a, columns, kOne, 0, stream);
+    else if (columns <= 32) launch<false, 2, 16, 2, false>(a, columns, kOne, 0, stream);
     else launch<false, 4, 8, 1, false>(a, columns < 64 ? columns : 64, kOne, 0, stream);
   }
   return launched();

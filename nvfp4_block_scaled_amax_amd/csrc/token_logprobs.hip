@@ -730,7 +730,9 @@ NVFP4_EXPORT nvfp4_status nvfp4_token_logprobs_backward(const void* logits, int6
                       range(dentropy, rows * 4)};
   for (int i = 0; i < 6; ++i)
     if (!(i == 0 && grad == logits && grad_stride == stride) && overlap(out, in[i])) return NVFP4_ERR_ALIAS;
-  const uint32_t size = 16384;
+  // workgroups of up to 16384 elements, all alike (as much as eight divide)
+  const int64_t parts = (vocab + 16383) / 16384;
+  const uint32_t size = (uint32_t)(((vocab + parts - 1) / parts + 7) / 8 * 8);
   const int64_t line = rows < 32768 ? rows : 32768;
   const BackArgs a = {logits, tokens, stats, entropy, dlogp, dentropy, grad, stride, grad_stride, rows,
                       (uint32_t)vocab, size, (int)given, itype == NVFP4_I64, c, inv_t};
