@@ -45,7 +45,8 @@ int nvfp4_answer_abi_version(void);
  * x [tokens][cols] of `xtype` with row stride x_stride (elements, >= cols); codes [E][rows][cols/2]
  * (8-byte aligned), scales [E][rows][cols/16] and alpha [E] as nvfp4_quantize_batched writes them;
  * expert [tokens][picks] of `itype`; y [tokens][picks][rows] of `ytype`, contiguous.  y overlaps
- * nothing.  tokens >= 0, tokens * picks <= NVFP4_MATVEC_MAX_ROWS, cols % 16 == 0, 1 <= E <= 65535.
+ * nothing.  tokens >= 0, tokens * picks <= NVFP4_MATVEC_MAX_ROWS, 1 <= rows <= 2^26, cols % 16 == 0,
+ * cols <= 2^27, 1 <= E <= 65535.
  * workspace: nvfp4_packed_matvec_workspace(...) bytes, 16-byte aligned, any content (may be NULL
  * where that is 0: bf16 x).  One launch, two for binary32 x. */
 #define NVFP4_MATVEC_MAX_ROWS 1024
@@ -71,8 +72,8 @@ nvfp4_status nvfp4_packed_matvec(const void* x, int64_t x_stride, const uint8_t*
  * logits [rows][vocab] of `type` with row stride `stride` (elements, >= vocab); tokens [rows][given]
  * of `itype` (NULL where given is 0); logp float [rows][given]; entropy float [rows] or NULL;
  * top_logp float and top_index int64 [rows][top] (NULL where top is 0); stats float [rows][2].
- * 0 <= given, top <= NVFP4_LOGPROBS_MAX, top <= vocab, 1 <= vocab <= 2^28, rows >= 0; T > 0 and 1 / T
- * finite.  workspace: nvfp4_token_logprobs_workspace(...) bytes, 16-byte aligned, any content (may
+ * 0 <= given, top <= NVFP4_LOGPROBS_MAX, top <= vocab, 1 <= vocab <= 2^28, 0 <= rows <= 2^30; T > 0 and
+ * 1 / T finite.  workspace: nvfp4_token_logprobs_workspace(...) bytes, 16-byte aligned, any content (may
  * be NULL where that is 0).  One launch; two for few long rows, which several workgroups share. */
 #define NVFP4_LOGPROBS_MAX 64
 int64_t nvfp4_token_logprobs_workspace(int64_t rows, int64_t vocab, int64_t top);
@@ -118,9 +119,9 @@ nvfp4_status nvfp4_grad_norm(const nvfp4_grad_tensor* tensors, int64_t count, nv
                              void* workspace, hipStream_t stream);
 
 /* out_i = round(grad_i * scale[0]) over many tensors.  `out`: host array of entries like `tensors`
- * with the same sizes, or NULL: in place, where a scale of 1 leaves the tensors alone.  Tensors of
- * `out` may be those of `tensors` but must not overlap them otherwise (checked within an entry).
- * One launch per 140 tensors (200 in place). */
+ * with the same sizes, or NULL: in place, where a scale of 1 leaves the tensors alone.  An entry of
+ * `out` may be that of `tensors`; any other overlap of a written tensor with a written or read one (the
+ * same tensor twice) is rejected.  One launch per 140 tensors (200 in place). */
 nvfp4_status nvfp4_clip_grads(const nvfp4_grad_tensor* tensors, const nvfp4_grad_tensor* out,
                               int64_t count, nvfp4_type type, const float* scale,
                               hipStream_t stream);

@@ -201,16 +201,12 @@ def token_logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor, stats: t
     return grad
 
 
-def _table(plan: AdamWPlan, name: str, grads) -> int:
-    """The address of the entries of nvfp4_grad_tensor for these tensors, which the plan keeps (read by
-    the library before the call returns)."""
-    table = plan.tables.get(name)
-    if table is None:
-        table = np.empty((len(grads), 2), np.int64)
-        table[:, 1] = plan.numels
-        plan.tables[name] = table = table, table.ctypes.data
-    table[0][:, 0] = [g.data_ptr() for g in grads]
-    return table[1]
+def _table(plan: AdamWPlan, grads) -> np.ndarray:
+    """The entries of nvfp4_grad_tensor for these tensors."""
+    table = np.empty((len(grads), 2), np.int64)
+    table[:, 0] = [g.data_ptr() for g in grads]
+    table[:, 1] = plan.numels
+    return table
 
 
 def _look(plan: AdamWPlan, grads):
@@ -234,7 +230,8 @@ def grad_norm(plan: AdamWPlan, grads, *, max_norm: float = None, eps: float = 1e
     elif scale is not None:
         raise ValueError("scale is an output of the form with max_norm only")
     ws = _work(workspace, grad_norm_workspace(len(grads)), like)
-    _call("nvfp4_grad_norm", like, _table(plan, "grads", grads), len(grads), kind,
+    table = _table(plan, grads)
+    _call("nvfp4_grad_norm", like, table.ctypes.data, len(grads), kind,
           0.0 if max_norm is None else max_norm, eps, norm.data_ptr(), _ptr(scale), ws.data_ptr())
     return norm, scale
 
@@ -247,7 +244,7 @@ def clip_grads(plan: AdamWPlan, grads, scale: torch.Tensor, *, out=None):
     grads, kind = _look(plan, grads)
     like = plan.params[0]
     _vector(scale, (1,), _F32, like, "scale")
-    table, to = _table(plan, "grads", grads), None
+    table, to = _table(plan, grads), None
     if out is not None:
         out = list(out)
         if len(out) != len(grads):
@@ -256,6 +253,7 @@ def clip_grads(plan: AdamWPlan, grads, scale: torch.Tensor, *, out=None):
             for t, n in zip(out, plan.numels):
                 plan._look("out", t, n, grads[0].dtype)
             plan._seen_out.keep(out)
-        to = _table(plan, "out", out)
-    _call("nvfp4_clip_grads", like, table, to, len(grads), kind, scale.data_ptr())
+        to = _table(plan, out)
+    _call("nvfp4_clip_grads", like, table.ctypes.data, None if to is None else to.ctypes.data,
+          len(grads), kind, scale.data_ptr())
     return grads if out is None else out

@@ -5,6 +5,10 @@
 // overflows, vanishes or needs a second pass.  Workgroups take chunks of the tensors in turn and leave
 // one sum each, which a last workgroup adds in a fixed order.  The tensors' table travels as a kernel
 // argument.
+#include <stdlib.h>
+
+#include <algorithm>
+
 #include "nvfp4_answer.h"
 #include "train_common.h"
 
@@ -173,6 +177,33 @@ nvfp4_status look(const nvfp4_grad_tensor* t, int64_t count, int64_t es) {
   return NVFP4_OK;
 }
 
+// Whether what is written (out, or the tensors themselves) overlaps nothing else that is written or read.
+nvfp4_status apart(const nvfp4_grad_tensor* in, const nvfp4_grad_tensor* out, int64_t count, int64_t es) {
+  struct Part {
+    uintptr_t lo, hi;
+    bool written;
+  };
+  Part* part = (Part*)malloc((size_t)(count ? count : 1) * 2 * sizeof(Part));
+  if (!part) return NVFP4_ERR_HIP;
+  int64_t n = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    if (in[i].numel == 0) continue;
+    const Range from = range(in[i].grad, in[i].numel * es), to = out ? range(out[i].grad, in[i].numel * es) : from;
+    part[n++] = {to.lo, to.hi, true};
+    if (to.lo != from.lo) part[n++] = {from.lo, from.hi, false};
+  }
+  std::sort(part, part + n, [](const Part& a, const Part& b) { return a.lo < b.lo; });
+  uintptr_t written = 0, read = 0;                     // the furthest ends so far
+  bool ok = true;
+  for (int64_t i = 0; i < n && ok; ++i) {
+    ok = part[i].lo >= written && (!part[i].written || part[i].lo >= read);
+    uintptr_t& end = part[i].written ? written : read;
+    if (part[i].hi > end) end = part[i].hi;
+  }
+  free(part);
+  return ok ? NVFP4_OK : NVFP4_ERR_ALIAS;
+}
+
 bool size_ok(double v) { return v >= 0.0 && v < 3.0e38; }
 
 }  // namespace
@@ -227,12 +258,11 @@ NVFP4_EXPORT nvfp4_status nvfp4_clip_grads(const nvfp4_grad_tensor* tensors, con
   const Range by = range(scale, 4);
   for (int64_t i = 0; i < count; ++i) {
     if (out && out[i].numel != tensors[i].numel) return NVFP4_ERR_SHAPE;
-    if (tensors[i].numel == 0) continue;
-    const Range from = range(tensors[i].grad, tensors[i].numel * es);
-    if (overlap(by, out ? range(out[i].grad, out[i].numel * es) : from)) return NVFP4_ERR_ALIAS;
-    if (out && out[i].grad != tensors[i].grad && overlap(from, range(out[i].grad, out[i].numel * es)))
+    if (tensors[i].numel && overlap(by, range(out ? out[i].grad : tensors[i].grad, tensors[i].numel * es)))
       return NVFP4_ERR_ALIAS;
   }
+  st = apart(tensors, out, count, es);
+  if (st != NVFP4_OK) return st;
   (void)hipGetLastError();
   if (!out)
     return batches<NormBatch, kTable>(tensors, count, type, [](Entry&, int64_t) {}, [&](NormBatch& b, unsigned groups) {

@@ -25,6 +25,8 @@ typedef u32x4 u32x4_a8 __attribute__((aligned(8)));
 typedef u32x2 u32x2_a8 __attribute__((aligned(8)));
 
 constexpr int kMaxRows = NVFP4_MATVEC_MAX_ROWS;
+// Threads of a launch stay below 2^32, offsets within a tile of 16 rows below 2^31.
+constexpr int64_t kMaxWeightRows = int64_t(1) << 26, kMaxCols = int64_t(1) << 27;
 constexpr int kUnit = 512;                  // elements of 16 weight rows that a wavefront takes at a time
 
 struct Matvec {
@@ -438,7 +440,7 @@ using namespace train;
 NVFP4_EXPORT int nvfp4_answer_abi_version(void) { return NVFP4_ANSWER_ABI_VERSION; }
 
 NVFP4_EXPORT int64_t nvfp4_packed_matvec_workspace(int64_t tokens, int64_t cols, nvfp4_type xtype) {
-  if (xtype != NVFP4_T_F32 || tokens <= 0 || tokens > kMaxRows || cols <= 0 || cols > (int64_t(1) << 30)) return 0;
+  if (xtype != NVFP4_T_F32 || tokens <= 0 || tokens > kMaxRows || cols <= 0 || cols > kMaxCols) return 0;
   return tokens * cols * 6;
 }
 
@@ -451,8 +453,8 @@ NVFP4_EXPORT nvfp4_status nvfp4_packed_matvec(const void* x, int64_t x_stride, c
                                               hipStream_t stream) {
   if (!known(xtype) || !known(ytype) || (itype != NVFP4_I32 && itype != NVFP4_I64)) return NVFP4_ERR_ENUM;
   if (tokens < 0 || tokens > kMaxRows || picks < 1 || picks > kMaxRows || tokens * picks > kMaxRows ||
-      E < 1 || E > 65535 || (!expert && (E != 1 || picks != 1)) || rows < 1 || rows > (int64_t(1) << 30) ||
-      cols < 16 || cols % 16 || cols > (int64_t(1) << 30) || !shape_ok(tokens, cols, x_stride) ||
+      E < 1 || E > 65535 || (!expert && (E != 1 || picks != 1)) || rows < 1 || rows > kMaxWeightRows ||
+      cols < 16 || cols % 16 || cols > kMaxCols || !shape_ok(tokens, cols, x_stride) ||
       E > (int64_t(1) << 58) / (rows * cols))
     return NVFP4_ERR_SHAPE;
   if (tokens == 0) return NVFP4_OK;

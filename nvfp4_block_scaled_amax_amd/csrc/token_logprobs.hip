@@ -614,7 +614,7 @@ __global__ __launch_bounds__(256) void backward_kernel(const BackArgs a) {
   if (fixes) grad[mine] = from_f32<T>(fix);
 }
 
-constexpr int64_t kMaxVocab = int64_t(1) << 28;
+constexpr int64_t kMaxVocab = int64_t(1) << 28, kMaxTokenRows = int64_t(1) << 30;
 
 // Workgroups per row: few long rows are shared.
 int splits_of(int64_t rows, int64_t vocab) {
@@ -668,7 +668,7 @@ NVFP4_EXPORT nvfp4_status nvfp4_token_logprobs(const void* logits, int64_t strid
                                                int64_t* top_index, float* stats, void* workspace,
                                                hipStream_t stream) {
   if (!known(type) || (itype != NVFP4_I32 && itype != NVFP4_I64)) return NVFP4_ERR_ENUM;
-  if (vocab > kMaxVocab || !shape_ok(rows, vocab, stride) || rows >= (int64_t(1) << 40) || given < 0 ||
+  if (vocab > kMaxVocab || !shape_ok(rows, vocab, stride) || rows > kMaxTokenRows || given < 0 ||
       given > kMost || top < 0 || top > kMost || top > vocab)
     return NVFP4_ERR_SHAPE;
   float inv_t, c;
@@ -714,7 +714,7 @@ NVFP4_EXPORT nvfp4_status nvfp4_token_logprobs_backward(const void* logits, int6
                                                         hipStream_t stream) {
   if (!known(type) || (itype != NVFP4_I32 && itype != NVFP4_I64)) return NVFP4_ERR_ENUM;
   if (vocab > kMaxVocab || !shape_ok(rows, vocab, stride) || !shape_ok(rows, vocab, grad_stride) ||
-      rows >= (int64_t(1) << 31) || given < 1 || given > kMost)
+      rows > kMaxTokenRows || given < 1 || given > kMost)
     return NVFP4_ERR_SHAPE;
   float inv_t, c;
   if (!temperature_ok(temperature, inv_t, c)) return NVFP4_ERR_VALUE;

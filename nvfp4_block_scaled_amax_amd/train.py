@@ -316,7 +316,6 @@ class AdamWPlan:
         self._table = np.zeros((len(params), 8), np.int64)
         self._table[:, 7] = self.numels
         self._at = {}                   # the addresses in it
-        self.tables = {}                # of the calls over its gradients (answer.py)
         self._seen, self._seen_grads, self._seen_out = _Seen(), _Seen(), _Seen()
         self._columns = [(k, kind, sizes, dtype) for k, kind, sizes, dtype in (
             (0, "params", self.numels, self.dtype), (2, "exp_avg", self.numels, state),

@@ -58,8 +58,8 @@ def matvec(L, x=A, xs=64, codes=B, scales=C, alpha=D, expert=None, tokens=4, pic
     (dict(cols=40), ESHAPE), (dict(xs=63), ESHAPE), (dict(picks=2), ESHAPE), (dict(experts=2), ESHAPE),
     (dict(expert=E, picks=0), ESHAPE), (dict(expert=E, picks=257), ESHAPE),
     (dict(expert=E, experts=65536), ESHAPE), (dict(expert=E, experts=0), ESHAPE),
-    (dict(expert=E, experts=65535, rows=1 << 30, cols=1 << 30, xs=1 << 30), ESHAPE),
-    (dict(rows=(1 << 30) + 1), ESHAPE), (dict(xs=1 << 41), ESHAPE),
+    (dict(expert=E, experts=65535, rows=1 << 26, cols=1 << 27, xs=1 << 27), ESHAPE),
+    (dict(rows=(1 << 26) + 1), ESHAPE), (dict(xs=1 << 41), ESHAPE), (dict(cols=(1 << 27) + 16, xs=1 << 28), ESHAPE),
     (dict(xt=2), EENUM), (dict(yt=-1), EENUM), (dict(it=2), EENUM),
     (dict(x=A + 1), EALIGN), (dict(xt=F32, x=A + 2), EALIGN), (dict(codes=B + 4), EALIGN),
     (dict(alpha=D + 2), EALIGN), (dict(yt=F32, y=F + 2), EALIGN), (dict(xt=F32, ws=G + 8), EALIGN),
@@ -83,7 +83,7 @@ LONG = dict(vocab=100000, xs=100000)
     (dict(ti=None), ENULL), (dict(st=None), ENULL), (dict(ws=None, **LONG), ENULL),
     (dict(vocab=0), ESHAPE), (dict(vocab=(1 << 28) + 1, xs=1 << 29), ESHAPE), (dict(rows=-1), ESHAPE),
     (dict(xs=99), ESHAPE), (dict(given=-1), ESHAPE), (dict(given=65), ESHAPE), (dict(top=-1), ESHAPE),
-    (dict(top=65), ESHAPE), (dict(vocab=1, top=2), ESHAPE),
+    (dict(top=65), ESHAPE), (dict(vocab=1, top=2), ESHAPE), (dict(rows=(1 << 30) + 1), ESHAPE),
     (dict(ty=2), EENUM), (dict(it=-1), EENUM), (dict(temp=0.0), EVALUE), (dict(temp=-2.0), EVALUE),
     (dict(temp=float("nan")), EVALUE), (dict(temp=float("inf")), EVALUE), (dict(temp=1e-39), EVALUE),
     (dict(x=A + 1), EALIGN), (dict(ty=F32, x=A + 2), EALIGN), (dict(t=B + 4), EALIGN), (dict(it=I32, t=B + 2), EALIGN),
@@ -104,7 +104,7 @@ def back(L, x=A, xs=100, t=B, st=C, ent=D, dl=E, dh=F, rows=2, vocab=100, given=
     (dict(x=None), ENULL), (dict(t=None), ENULL), (dict(st=None), ENULL), (dict(dl=None), ENULL),
     (dict(g=None), ENULL), (dict(ent=None), ENULL),
     (dict(vocab=0), ESHAPE), (dict(rows=-1), ESHAPE), (dict(xs=99), ESHAPE), (dict(gs=99), ESHAPE),
-    (dict(given=0), ESHAPE), (dict(given=65), ESHAPE), (dict(rows=1 << 31), ESHAPE),
+    (dict(given=0), ESHAPE), (dict(given=65), ESHAPE), (dict(rows=(1 << 30) + 1), ESHAPE),
     (dict(ty=3), EENUM), (dict(it=2), EENUM), (dict(temp=0.0), EVALUE), (dict(temp=float("inf")), EVALUE),
     (dict(x=A + 1), EALIGN), (dict(g=G + 1), EALIGN), (dict(t=B + 4), EALIGN), (dict(dl=E + 2), EALIGN),
     (dict(st=C + 2), EALIGN), (dict(ent=D + 2), EALIGN), (dict(dh=F + 2), EALIGN),
@@ -147,7 +147,10 @@ def clip(L, entries=((A, 100), (B, 50)), out=None, ty=F32, scale=E):
     (dict(entries=((A, -1),)), ESHAPE), (dict(out=((C, 100), (D, 51))), ESHAPE), (dict(ty=-1), EENUM),
     (dict(entries=((A + 1, 4),)), EALIGN), (dict(out=((C, 100), (D + 2, 50))), EALIGN), (dict(scale=E + 2), EALIGN),
     (dict(scale=A + 8), EALIAS), (dict(out=((A + 4, 100), (D, 50))), EALIAS),
-    (dict(out=((C, 100), (D, 50)), scale=D + 4), EALIAS)])
+    (dict(out=((C, 100), (D, 50)), scale=D + 4), EALIAS),
+    (dict(entries=((A, 100), (A, 100))), EALIAS), (dict(entries=((B, 4), (A, 100), (A + 396, 2))), EALIAS),
+    (dict(out=((C, 100), (C + 200, 50))), EALIAS), (dict(out=((B, 100), (A, 50))), EALIAS),
+    (dict(out=((C, 100), (A, 50))), EALIAS), (dict(entries=((A, 100), (A, 100)), out=((A, 100), (C, 100))), EALIAS)])
 def test_clip_grads_refuses(L, kw, status):
     assert clip(L, **kw) == status
 

@@ -182,10 +182,22 @@ def test_graphs(nv):
         torch.cuda.synchronize()
 
 
+def test_the_same_gradient_twice(nv):
+    """Counts twice in the norm; scaled into two outputs."""
+    plan = plan_of(nv, [500, 500])
+    g = grads_of([500], F32, 3)[0]
+    norm, scale = nv.grad_norm(plan, [g, g], max_norm=1.0)
+    want = math.sqrt(2 * float(g.double().square().sum()))
+    assert close(norm, want)
+    out = [torch.zeros_like(g), torch.zeros_like(g)]
+    nv.clip_grads(plan, [g, g], scale, out=out)
+    assert torch.equal(out[0], g * scale) and torch.equal(out[1], out[0])
+
+
 def test_refusals(nv):
     plan = plan_of(nv, [8, 9])
     g = [torch.zeros(8, device="cuda"), torch.zeros(9, device="cuda")]
-    s = torch.ones(1, device="cuda")
+    s, nine, t9 = torch.ones(1, device="cuda"), plan_of(nv, [9, 9]), torch.zeros(9, device="cuda")
     bad = [
         (ValueError, "1 gradients for 2", lambda: nv.grad_norm(plan, g[:1])),
         (ValueError, "gradient 1 is None", lambda: nv.grad_norm(plan, [g[0], None])),
@@ -206,6 +218,8 @@ def test_refusals(nv):
         (TypeError, "out must be", lambda: nv.clip_grads(plan, g, s, out=[t.bfloat16() for t in g])),
         (ValueError, "out must be", lambda: nv.clip_grads(plan, g, s, out=[g[1], g[0]])),
         (nv.NVFP4Error, "overlap", lambda: nv.clip_grads(plan, g, g[0][:1])),
+        (nv.NVFP4Error, "overlap", lambda: nv.clip_grads(nine, [g[1], g[1]], s)),
+        (nv.NVFP4Error, "overlap", lambda: nv.clip_grads(nine, [g[1], g[1].clone()], s, out=[t9, t9])),
         (nv.NVFP4Error, "overlap", lambda: nv.clip_grads(
             plan, [torch.zeros(16, device="cuda")[i:i + n] for i, n in ((0, 8), (0, 9))], g[1][:1], out=g)),
     ]
