@@ -47,15 +47,13 @@ int nvfp4_answer_abi_version(void);
  * expert [tokens][picks] of `itype`; y [tokens][picks][rows] of `ytype`, contiguous.  y overlaps
  * nothing.  tokens >= 0, tokens * picks <= NVFP4_MATVEC_MAX_ROWS, 1 <= rows <= 2^26, cols % 16 == 0,
  * cols <= 2^27, 1 <= E <= 65535.
- * workspace: nvfp4_packed_matvec_workspace(...) bytes, 16-byte aligned, any content (may be NULL
- * where that is 0: bf16 x).  One launch, two for binary32 x. */
+ * One launch. */
 #define NVFP4_MATVEC_MAX_ROWS 1024
-int64_t nvfp4_packed_matvec_workspace(int64_t tokens, int64_t cols, nvfp4_type xtype);
 nvfp4_status nvfp4_packed_matvec(const void* x, int64_t x_stride, const uint8_t* codes,
                                  const uint8_t* scales, const float* alpha, const void* expert,
                                  int64_t tokens, int64_t picks, int64_t E, int64_t rows,
                                  int64_t cols, nvfp4_type xtype, nvfp4_type ytype,
-                                 nvfp4_index itype, void* y, void* workspace, hipStream_t stream);
+                                 nvfp4_index itype, void* y, hipStream_t stream);
 
 /* Log probabilities of given tokens under p = softmax(logits / T), per row:
  *   m = max_j x_j,  z = ln sum_j exp((x_j - m) / T)          (stats[row] = {m, z})

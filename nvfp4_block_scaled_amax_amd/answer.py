@@ -43,10 +43,7 @@ def bind(L: ctypes.CDLL) -> None:
     if L.nvfp4_answer_abi_version() != ANSWER_ABI_VERSION:
         raise RuntimeError("libnvfp4_amax.so has answer ABI version %d, this binding needs %d: "
                            "rebuild it" % (L.nvfp4_answer_abi_version(), ANSWER_ABI_VERSION))
-    L.nvfp4_packed_matvec_workspace.argtypes = [i64, i64, i32]
-    L.nvfp4_packed_matvec_workspace.restype = i64
-    L.nvfp4_packed_matvec.argtypes = [P, i64, P, P, P, P, i64, i64, i64, i64, i64, i32, i32, i32, P, P,
-                                      P]
+    L.nvfp4_packed_matvec.argtypes = [P, i64, P, P, P, P, i64, i64, i64, i64, i64, i32, i32, i32, P, P]
     L.nvfp4_token_logprobs_workspace.argtypes = [i64, i64, i64]
     L.nvfp4_token_logprobs_workspace.restype = i64
     L.nvfp4_token_logprobs.argtypes = [P, i64, P, i64, i64, i64, i64, i32, i32, f32, P, P, P, P, P, P, P]
@@ -68,7 +65,7 @@ def _output(t, shape, dtype, x: torch.Tensor) -> torch.Tensor:
 
 
 def packed_matvec(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, alpha: torch.Tensor, *,
-                  expert: torch.Tensor = None, dtype: torch.dtype = None, y=None, workspace=None):
+                  expert: torch.Tensor = None, dtype: torch.dtype = None, y=None):
     """x W^T for a few rows of x with a packed NVFP4 weight -> y [..., rows].
 
     x is [..., cols], bfloat16 or float32 (2-D with a row stride, or contiguous); codes, scales and alpha
@@ -109,11 +106,9 @@ def packed_matvec(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, al
     y = _output(y, (*to, rows), dtype, x)
     if y.numel() == 0:
         return y
-    need = lib().nvfp4_packed_matvec_workspace(tokens, cols, kind)
-    ws = _work(workspace, need, x) if need else None
     _call("nvfp4_packed_matvec", x, x.data_ptr(), xs, codes.data_ptr(), scales.data_ptr(),
           alpha.data_ptr(), _ptr(expert), tokens, picks, E, rows, cols, kind, TYPES[dtype], itype,
-          y.data_ptr(), _ptr(ws))
+          y.data_ptr())
     return y
 
 

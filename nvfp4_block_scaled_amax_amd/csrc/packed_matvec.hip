@@ -30,14 +30,14 @@ constexpr int64_t kMaxWeightRows = int64_t(1) << 26, kMaxCols = int64_t(1) << 27
 constexpr int kUnit = 512;                  // elements of 16 weight rows that a wavefront takes at a time
 
 struct Matvec {
-  const uint16_t* x;        // bf16; binary32 rows are three each
+  const void* x;
   const uint8_t* codes;
   const uint8_t* scales;
   const float* alpha;
   const void* expert;
   void* y;
   int64_t x_stride, rows, cols;
-  int out_rows, picks, experts, group;      // tokens * picks; 1 or 3 rows of x per token
+  int out_rows, picks, experts;             // tokens * picks
   int wide, f32;                            // 64-bit indices; binary32 y
   int lds;                                  // bytes of shared memory for x
   int deal;                                 // log2 of the wavefronts that deal a tile's units among them
@@ -78,10 +78,34 @@ struct Unit {
   u32x2 scale[S];
 };
 
+// Eight binary32 values as three times eight bf16 whose sums they are: the upper 8 significant bits, the next, the
+// last.
+__device__ __forceinline__ void thirds(const Vec<float, 8>& v, u32x4 (&r)[3]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t w[2][3];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float f = v[2 * i + h];
+      // of an infinity and a NaN (whose lower bits may be all it has) the first part is all
+      const bool odd = !(fabsf(f) < INFINITY);
+      const float first = odd ? (f != f ? NAN : f) : __uint_as_float(__float_as_uint(f) & 0xFFFF0000u);
+      const float rest = odd ? 0.0f : f - first;
+      const float second = __uint_as_float(__float_as_uint(rest) & 0xFFFF0000u);
+      w[h][0] = __float_as_uint(first);
+      w[h][1] = __float_as_uint(second);
+      w[h][2] = __float_as_uint(rest - second);
+    }
+#pragma unroll
+    for (int p = 0; p < 3; ++p) r[p][i] = (w[0][p] >> 16) | (w[1][p] & 0xFFFF0000u);
+  }
+}
+
 // SHORT: rows of less than a unit.
-template <bool FEW, int MT, int W, int DEPTH, bool EXPERT, bool SHORT>
+template <typename X, bool FEW, int MT, int W, int DEPTH, bool EXPERT, bool SHORT>
 __global__ __launch_bounds__(W * 64) void matvec_kernel(const Matvec a) {
   constexpr int kCols = FEW ? 4 : 16;                // of a tile
+  constexpr int kGroup = sizeof(X) == 4 ? 3 : 1;     // columns of a row of x
   constexpr int S = FEW ? 4 : 1;
   extern __shared__ __align__(16) char held[];       // x, then the wavefronts' sums
   // the rows of y that go to this expert, in order, and behind the end those that go nowhere; their tokens
@@ -192,54 +216,60 @@ __global__ __launch_bounds__(W * 64) void matvec_kernel(const Matvec a) {
       }
     }
   };
-  // columns of which a turn of all wavefronts fits: at least a.group of them
+  // rows of x of which a turn of all wavefronts fits: at least one
   const int turn = kUnit * deal * DEPTH;
-  const int per_pass = min(MT * kCols, a.lds / (turn * 2 + 16)) / a.group;
+  const int per_pass = min(MT * kCols, a.lds / (turn * 2 + 16)) / kGroup;
   for (int first = 0; first < count; first += per_pass) {
-    const int here = min(per_pass, count - first), wide = here * a.group;
+    const int here = min(per_pass, count - first), wide = here * kGroup;
     // x: all of it, or as many elements of each column as fit, a multiple of a turn
     const int fit = (a.lds / wide - 16) / 2, chunk = (fit >= all * kUnit ? all * kUnit : fit / turn * turn) / kUnit;
     const int pitch = chunk * (kUnit * 2) + 16;
-    // A wavefront stages units of columns: with `beside` wavefronts to a column it takes every beside-th
-    // unit of every (W / beside)-th column, kAhead at a time.  The first ones are asked for before the
-    // weights: loads come back in order.
-    constexpr int kAhead = FEW ? 4 : 8;
-    const int beside = 31 - __builtin_clz(min(chunk, W)), col_step = W >> beside;
+    // A wavefront stages units of rows of x: with 2^beside wavefronts to a row it takes every so-manieth unit of
+    // every W / 2^beside-th row, kAhead at a time.  The first ones are asked for before the weights: loads come
+    // back in order.
+    constexpr int kAhead = FEW || kGroup == 3 ? 4 : 8;
+    const int beside = 31 - __builtin_clz(min(chunk, W)), row_step = W >> beside;
     struct Place {
-      int col, unit;
+      int row, unit;
     };
     const Place begin = {wave >> beside, wave & ((1 << beside) - 1)};
     const auto after = [&](Place p) {
-      p.col += col_step;
-      if (p.col >= wide) {
-        p.col = begin.col;
+      p.row += row_step;
+      if (p.row >= here) {
+        p.row = begin.row;
         p.unit += 1 << beside;
       }
       return p;
     };
-    u32x4 v[kAhead];
+    Vec<X, 8> v[kAhead];
     // (a place past the last one is the last one again, and no branch stands between the loads)
     const auto fetch = [&](int from, Place p) {
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        const int col = min(p.col, wide - 1), unit = min(from + min(p.unit, chunk - 1), all - 1);
+        const int i = first + min(p.row, here - 1), unit = min(from + min(p.unit, chunk - 1), all - 1);
         const int at = start(unit) + lane * 8;
-        const int i = a.group == 1 ? col : col / 3;
-        const int64_t row = EXPERT ? __builtin_amdgcn_readfirstlane(tokens[first + i]) * a.group + (col - i * a.group)
-                                   : first * a.group + col;
-        const uint16_t* x = a.x + row * a.x_stride;
-        v[k] = *(const u32x4_a2*)(x + (uint32_t)(SHORT ? min(at, cols - 8) : at));
+        const int64_t row = EXPERT ? __builtin_amdgcn_readfirstlane(tokens[i]) : i;
+        const X* x = (const X*)a.x + row * a.x_stride;
+        v[k] = load_vec<8>(x + (uint32_t)(SHORT ? min(at, cols - 8) : at));
         const bool fresh = SHORT ? at < cols : at >= unit * kUnit;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[k][i] = fresh ? v[k][i] : 0u;
+        for (int w = 0; w < Vec<X, 8>::kWords; ++w) v[k].w[w] = fresh ? v[k].w[w] : 0u;
         p = after(p);
       }
     };
     const auto put = [&](Place p) {
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        const int col = min(p.col, wide - 1), unit = min(p.unit, chunk - 1);
-        *(u32x4*)(held + col * pitch + unit * (kUnit * 2) + lane * 16) = v[k];
+        const int col = min(p.row, here - 1) * kGroup, unit = min(p.unit, chunk - 1);
+        char* to = held + col * pitch + unit * (kUnit * 2) + lane * 16;
+        if constexpr (kGroup == 1) {
+          *(u32x4*)to = u32x4{v[k].w[0], v[k].w[1], v[k].w[2], v[k].w[3]};
+        } else {
+          u32x4 r[3];
+          thirds(v[k], r);
+#pragma unroll
+          for (int q = 0; q < 3; ++q) *(u32x4*)(to + q * pitch) = r[q];
+        }
         p = after(p);
       }
       return p;
@@ -363,8 +393,9 @@ __global__ __launch_bounds__(W * 64) void matvec_kernel(const Matvec a) {
       const int j = o & ((1 << row_bits) - 1), i = o >> row_bits;
       if (row0 + j >= a.rows) continue;
       float sum = 0.0f;
-      for (int p = a.group - 1; p >= 0; --p) {         // the smallest part first
-        const float* from = part + ((j >> 4) << a.deal) * kPart + (i * a.group + p) * 16 + (j & 15);
+#pragma unroll
+      for (int p = kGroup - 1; p >= 0; --p) {          // the smallest part first
+        const float* from = part + ((j >> 4) << a.deal) * kPart + (i * kGroup + p) * 16 + (j & 15);
         for (int w = 0; w < deal; ++w) sum += from[w * kPart];
       }
       sum *= alpha;
@@ -375,38 +406,8 @@ __global__ __launch_bounds__(W * 64) void matvec_kernel(const Matvec a) {
   }
 }
 
-// binary32 rows as three bf16 rows each: the upper 8 significant bits, the next, the last.
-__global__ __launch_bounds__(256) void split_kernel(const float* x, int64_t stride, int64_t cols,
-                                                    uint16_t* out) {
-  const int64_t row = blockIdx.y;
-  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
-  if (at >= cols) return;
-  const Vec<float, 8> v = load_vec<8>(x + row * stride + at);
-  u32x4 r[3];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t w[2][3];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float f = v[2 * i + h];
-      // of an infinity and a NaN (whose lower bits may be all it has) the first part is all
-      const bool odd = !(fabsf(f) < INFINITY);
-      const float first = odd ? (f != f ? NAN : f) : __uint_as_float(__float_as_uint(f) & 0xFFFF0000u);
-      const float rest = odd ? 0.0f : f - first;
-      const float second = __uint_as_float(__float_as_uint(rest) & 0xFFFF0000u);
-      w[h][0] = __float_as_uint(first);
-      w[h][1] = __float_as_uint(second);
-      w[h][2] = __float_as_uint(rest - second);
-    }
-#pragma unroll
-    for (int p = 0; p < 3; ++p) r[p][i] = (w[0][p] >> 16) | (w[1][p] & 0xFFFF0000u);
-  }
-#pragma unroll
-  for (int p = 0; p < 3; ++p) *(u32x4*)(out + (row * 3 + p) * cols + at) = r[p];
-}
-
 // `room`: shared memory for x, so that one (150 KB), two or more workgroups share a compute unit.
-template <bool FEW, int MT, int W, int DEPTH, bool EXPERT, bool SHORT = false>
+template <typename X, bool FEW, int MT, int W, int DEPTH, bool EXPERT, bool SHORT = false>
 void launch(Matvec a, int64_t columns, int room, int deal, hipStream_t stream) {
   const int64_t tiles = (a.rows + 15) / 16, units = (a.cols + kUnit - 1) / kUnit;
   const auto turn = [](int deal) { return (kUnit * DEPTH * 2 << deal) + 16; };     // bytes of a column
@@ -426,10 +427,35 @@ void launch(Matvec a, int64_t columns, int room, int deal, hipStream_t stream) {
   constexpr int kSums = W * MT * (FEW ? 256 : 1024);
   const int bytes = a.lds > kSums ? a.lds : kSums;
   const dim3 grid((unsigned)((tiles + (W >> a.deal) - 1) / (W >> a.deal)), (unsigned)a.experts);
-  const auto kernel = matvec_kernel<FEW, MT, W, DEPTH, EXPERT, SHORT>;
+  const auto kernel = matvec_kernel<X, FEW, MT, W, DEPTH, EXPERT, SHORT>;
   if (bytes > 60 * 1024)
     (void)hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
   kernel<<<grid, W * 64, bytes, stream>>>(a);
+}
+
+template <typename X>
+void launch(const Matvec& a, hipStream_t stream) {
+  constexpr int kOne = 150 * 1024, kFour = 40 * 1024, kGroup = sizeof(X) == 4 ? 3 : 1;
+  if (a.expert) {
+    // what an expert gets is not known here: twice its share
+    const int64_t E = a.experts, hit = E < a.out_rows ? E : a.out_rows;
+    const int64_t columns = (2 * a.out_rows + E - 1) / E * kGroup;
+    if (a.cols < kUnit) launch<X, false, 1, 4, 1, true, true>(a, 16, kOne, 0, stream);
+    else if (columns <= 4 && a.rows * hit <= 16384) launch<X, true, 1, 4, 1, true>(a, 4, kFour, 1, stream);
+    else if (columns <= 16) launch<X, false, 1, 4, 1, true>(a, 16, kFour, 0, stream);
+    else if (columns <= 32) launch<X, false, 2, 8, 2, true>(a, 32, kOne / 2, 0, stream);
+    else launch<X, false, 4, 8, 1, true>(a, 64, kOne, 0, stream);
+  } else {
+    const int64_t columns = a.out_rows * kGroup;
+    if (a.cols < kUnit && columns <= 4) launch<X, true, 1, 4, 1, false, true>(a, columns, kOne, 0, stream);
+    else if (a.cols < kUnit) launch<X, false, 1, 4, 1, false, true>(a, 16, kOne, 0, stream);
+    else if (columns <= 4 && a.rows > 6144) launch<X, true, 1, 4, 1, false>(a, columns, kOne, 1, stream);
+    else if (columns <= 4) launch<X, true, 1, 8, 1, false>(a, columns, kOne, 1, stream);
+    else if (columns <= 8 && a.rows < 16384) launch<X, true, 2, 8, 2, false>(a, columns, kOne, 0, stream);
+    else if (columns <= 16) launch<X, false, 1, 16, 1, false>(a, columns, kOne, 0, stream);
+    else if (columns <= 32) launch<X, false, 2, 16, 2, false>(a, columns, kOne, 0, stream);
+    else launch<X, false, 4, 8, 1, false>(a, columns < 64 ? columns : 64, kOne, 0, stream);
+  }
 }
 
 }  // namespace
@@ -439,18 +465,12 @@ using namespace train;
 
 NVFP4_EXPORT int nvfp4_answer_abi_version(void) { return NVFP4_ANSWER_ABI_VERSION; }
 
-NVFP4_EXPORT int64_t nvfp4_packed_matvec_workspace(int64_t tokens, int64_t cols, nvfp4_type xtype) {
-  if (xtype != NVFP4_T_F32 || tokens <= 0 || tokens > kMaxRows || cols <= 0 || cols > kMaxCols) return 0;
-  return tokens * cols * 6;
-}
-
 NVFP4_EXPORT nvfp4_status nvfp4_packed_matvec(const void* x, int64_t x_stride, const uint8_t* codes,
                                               const uint8_t* scales, const float* alpha,
                                               const void* expert, int64_t tokens, int64_t picks,
                                               int64_t E, int64_t rows, int64_t cols,
                                               nvfp4_type xtype, nvfp4_type ytype,
-                                              nvfp4_index itype, void* y, void* workspace,
-                                              hipStream_t stream) {
+                                              nvfp4_index itype, void* y, hipStream_t stream) {
   if (!known(xtype) || !known(ytype) || (itype != NVFP4_I32 && itype != NVFP4_I64)) return NVFP4_ERR_ENUM;
   if (tokens < 0 || tokens > kMaxRows || picks < 1 || picks > kMaxRows || tokens * picks > kMaxRows ||
       E < 1 || E > 65535 || (!expert && (E != 1 || picks != 1)) || rows < 1 || rows > kMaxWeightRows ||
@@ -458,51 +478,20 @@ NVFP4_EXPORT nvfp4_status nvfp4_packed_matvec(const void* x, int64_t x_stride, c
       E > (int64_t(1) << 58) / (rows * cols))
     return NVFP4_ERR_SHAPE;
   if (tokens == 0) return NVFP4_OK;
-  const int64_t need = nvfp4_packed_matvec_workspace(tokens, cols, xtype), out_rows = tokens * picks;
-  if (!x || !codes || !scales || !alpha || !y || (need && !workspace)) return NVFP4_ERR_NULL;
+  if (!x || !codes || !scales || !alpha || !y) return NVFP4_ERR_NULL;
   const int64_t xs = size_of(xtype), ys = size_of(ytype), is = itype == NVFP4_I32 ? 4 : 8;
-  if (!aligned(x, xs) || !aligned(codes, 8) || !aligned(alpha, 4) || !aligned(expert, is) ||
-      !aligned(y, ys) || !aligned(workspace, 16))
+  if (!aligned(x, xs) || !aligned(codes, 8) || !aligned(alpha, 4) || !aligned(expert, is) || !aligned(y, ys))
     return NVFP4_ERR_ALIGN;
+  const int64_t out_rows = tokens * picks;
   const Range in[] = {range(x, extent(tokens, cols, x_stride, xs)), range(codes, E * rows * (cols / 2)),
                       range(scales, E * rows * (cols / 16)), range(alpha, E * 4),
                       range(expert, out_rows * is)};
-  const Range out[] = {range(y, out_rows * rows * ys), range(need ? workspace : nullptr, need)};
-  for (int o = 0; o < 2; ++o)
-    for (const Range& r : in)
-      if (overlap(out[o], r)) return NVFP4_ERR_ALIAS;
-  if (overlap(out[0], out[1])) return NVFP4_ERR_ALIAS;
+  for (const Range& r : in)
+    if (overlap(range(y, out_rows * rows * ys), r)) return NVFP4_ERR_ALIAS;
   (void)hipGetLastError();
-  Matvec a = {(const uint16_t*)x, codes, scales, alpha, expert, y, x_stride, rows, cols, (int)out_rows,
-              (int)picks, (int)E, 1, itype == NVFP4_I64, ytype == NVFP4_T_F32, 0, 0};
-  if (xtype == NVFP4_T_F32) {
-    split_kernel<<<dim3((unsigned)((cols + 2047) / 2048), (unsigned)tokens), 256, 0, stream>>>(
-        (const float*)x, x_stride, cols, (uint16_t*)workspace);
-    const nvfp4_status st = launched();
-    if (st != NVFP4_OK) return st;
-    a.x = (const uint16_t*)workspace;
-    a.x_stride = cols;
-    a.group = 3;
-  }
-  constexpr int kOne = 150 * 1024, kFour = 40 * 1024;
-  if (expert) {
-    // what an expert gets is not known here: twice its share
-    const int64_t columns = (2 * out_rows + E - 1) / E * a.group;
-    if (cols < kUnit) launch<false, 1, 4, 1, true, true>(a, 16, kOne, 0, stream);
-    else if (columns <= 4 && rows * (E < out_rows ? E : out_rows) <= 16384) launch<true, 1, 4, 1, true>(a, 4, kFour, 1, stream);
-    else if (columns <= 16) launch<false, 1, 4, 1, true>(a, 16, kFour, 0, stream);
-    else if (columns <= 32) launch<false, 2, 8, 2, true>(a, 32, kOne / 2, 0, stream);
-    else launch<false, 4, 8, 1, true>(a, 64, kOne, 0, stream);
-  } else {
-    const int64_t columns = out_rows * a.group;
-    if (cols < kUnit && columns <= 4) launch<true, 1, 4, 1, false, true>(a, columns, kOne, 0, stream);
-    else if (cols < kUnit) launch<false, 1, 4, 1, false, true>(a, 16, kOne, 0, stream);
-    else if (columns <= 4 && rows > 6144) launch<true, 1, 4, 1, false>(a, columns, kOne, 1, stream);
-    else if (columns <= 4) launch<true, 1, 8, 1, false>(a, columns, kOne, 1, stream);
-    else if (columns <= 8 && rows < 16384) launch<true, 2, 8, 2, false>(a, columns, kOne, 0, stream);
-    else if (columns <= 16) launch<false, 1, 16, 1, false>(a, columns, kOne, 0, stream);
-    else if (columns <= 32) launch<false, 2, 16, 2, false>(a, columns, kOne, 0, stream);
-    else launch<false, 4, 8, 1, false>(a, columns < 64 ? columns : 64, kOne, 0, stream);
-  }
+  const Matvec a = {x, codes, scales, alpha, expert, y, x_stride, rows, cols, (int)out_rows, (int)picks, (int)E,
+                    itype == NVFP4_I64, ytype == NVFP4_T_F32, 0, 0};
+  if (xtype == NVFP4_T_F32) launch<float>(a, stream);
+  else launch<bf16>(a, stream);
   return launched();
 }

@@ -127,12 +127,9 @@ def test_nothing_beside_the_outputs_is_written(nv, tokens):
     for xtype in (BF16, F32):
         x = whole((tokens, cols), 2)
         held = torch.full((tokens * rows + 64,), 7.0, device="cuda")
-        work = torch.full((tokens * cols * 6 + 64,), 9, dtype=torch.uint8, device="cuda")
         y = held[32:32 + tokens * rows].view(tokens, rows)
-        nv.packed_matvec(x.to(xtype).cuda(), codes[0].cuda(), scales[0].cuda(), alpha.cuda(), dtype=F32, y=y,
-                         workspace=work[32:32 + tokens * cols * 6] if tokens else None)
+        nv.packed_matvec(x.to(xtype).cuda(), codes[0].cuda(), scales[0].cuda(), alpha.cuda(), dtype=F32, y=y)
         assert (held[:32] == 7).all() and (held[32 + tokens * rows:] == 7).all()
-        assert (work[:32] == 9).all() and (work[32 + tokens * cols * 6:] == 9).all()
         if tokens:
             assert same(y, rounded(x.double() @ value[0].t(), alpha, F32))
 
@@ -275,7 +272,6 @@ def test_refusals(nv):
         (ValueError, "tokens, cols", lambda: nv.packed_matvec(x[None], c, s, a, expert=e)),
         (ValueError, "at most 1024", lambda: nv.packed_matvec(x[:1].expand(1025, 64).contiguous(), *one)),
         (ValueError, "output must be", lambda: nv.packed_matvec(x, *one, y=torch.empty(3, 32, device="cuda"))),
-        (ValueError, "workspace", lambda: nv.packed_matvec(x.float(), *one, workspace=torch.empty(8, device="cuda"))),
         (nv.NVFP4Error, "overlap", lambda: nv.packed_matvec(
             x, *one, y=x.view(-1)[:96].view(3, 32))),
     ]
