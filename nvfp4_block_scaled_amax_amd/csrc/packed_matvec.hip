@@ -227,7 +227,7 @@ __global__ __launch_bounds__(W * 64) void matvec_kernel(const Matvec a) {
     // A wavefront stages units of rows of x: with 2^beside wavefronts to a row it takes every so-manieth unit of
     // every W / 2^beside-th row, kAhead at a time.  The first ones are asked for before the weights: loads come
     // back in order.
-    constexpr int kAhead = FEW || kGroup == 3 ? 4 : 8;
+    constexpr int kAhead = FEW || kGroup == 3 || (W == 16 && MT > 1) ? 4 : 8;
     const int beside = 31 - __builtin_clz(min(chunk, W)), row_step = W >> beside;
     struct Place {
       int row, unit;
@@ -453,7 +453,7 @@ void launch(const Matvec& a, hipStream_t stream) {
     else if (columns <= 4) launch<X, true, 1, 8, 1, false>(a, columns, kOne, 1, stream);
     else if (columns <= 8 && a.rows < 16384) launch<X, true, 2, 8, 2, false>(a, columns, kOne, 0, stream);
     else if (columns <= 16) launch<X, false, 1, 16, 1, false>(a, columns, kOne, 0, stream);
-    else if (columns <= 32) launch<X, false, 2, 16, 2, false>(a, columns, kOne, 0, stream);
+    else if (columns <= 32) launch<X, false, 2, 16, 1, false>(a, columns, kOne, 0, stream);
     else launch<X, false, 4, 8, 1, false>(a, columns < 64 ? columns : 64, kOne, 0, stream);
   }
 }
