@@ -15,8 +15,8 @@ the library's kernels, and no call records an autograd graph.
 from __future__ import annotations
 
 import ctypes
+import struct
 
-import numpy as np
 import torch
 
 from . import lib
@@ -196,12 +196,13 @@ def token_logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor, stats: t
     return grad
 
 
-def _table(plan: AdamWPlan, grads) -> np.ndarray:
-    """The entries of nvfp4_grad_tensor for these tensors."""
-    table = np.empty((len(grads), 2), np.int64)
-    table[:, 0] = [g.data_ptr() for g in grads]
-    table[:, 1] = plan.numels
-    return table
+def _table(plan: AdamWPlan, grads) -> bytes:
+    """The entries of nvfp4_grad_tensor for these tensors.  (Packed at once: half the time of an array of
+    numpy's, and of each call its own.)"""
+    entries = [0] * (2 * len(grads))
+    entries[0::2] = [g.data_ptr() for g in grads]
+    entries[1::2] = plan.numels
+    return struct.pack("%dq" % len(entries), *entries)
 
 
 def _look(plan: AdamWPlan, grads):
@@ -225,8 +226,7 @@ def grad_norm(plan: AdamWPlan, grads, *, max_norm: float = None, eps: float = 1e
     elif scale is not None:
         raise ValueError("scale is an output of the form with max_norm only")
     ws = _work(workspace, grad_norm_workspace(len(grads)), like)
-    table = _table(plan, grads)
-    _call("nvfp4_grad_norm", like, table.ctypes.data, len(grads), kind,
+    _call("nvfp4_grad_norm", like, _table(plan, grads), len(grads), kind,
           0.0 if max_norm is None else max_norm, eps, norm.data_ptr(), _ptr(scale), ws.data_ptr())
     return norm, scale
 
@@ -239,7 +239,7 @@ def clip_grads(plan: AdamWPlan, grads, scale: torch.Tensor, *, out=None):
     grads, kind = _look(plan, grads)
     like = plan.params[0]
     _vector(scale, (1,), _F32, like, "scale")
-    table, to = _table(plan, grads), None
+    to = None
     if out is not None:
         out = list(out)
         if len(out) != len(grads):
@@ -249,6 +249,5 @@ def clip_grads(plan: AdamWPlan, grads, scale: torch.Tensor, *, out=None):
                 plan._look("out", t, n, grads[0].dtype)
             plan._seen_out.keep(out)
         to = _table(plan, out)
-    _call("nvfp4_clip_grads", like, table.ctypes.data, None if to is None else to.ctypes.data,
-          len(grads), kind, scale.data_ptr())
+    _call("nvfp4_clip_grads", like, _table(plan, grads), to, len(grads), kind, scale.data_ptr())
     return grads if out is None else out

@@ -275,7 +275,7 @@ __device__ __forceinline__ void find_top(const T* row, uint32_t lo, uint32_t hi,
     float most = v[0];
 #pragma unroll
     for (int j = 1; j < N; ++j) most = fmaxf(most, v[j]);
-    if (most >= least) {
+    if (most > least || (most == least && at < until)) {
       const int n = atomicAdd(&sh.vectors, 1);
       if (n < kVectors) {
         sh.vector[n] = u32x4{v.w[0], v.w[1], v.w[2], v.w[3]};

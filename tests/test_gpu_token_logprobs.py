@@ -51,6 +51,12 @@ def logits_of(shape, seed, kind="model"):
         x[..., shape[-1] // 2] = 1.0
     elif kind == "lowest":
         x[torch.rand(shape, generator=gen(seed + 1)) < 0.5] = torch.finfo(BF16).min
+    elif kind == "allowed":                   # a grammar's few tokens
+        x[torch.rand(shape, generator=gen(seed + 1)) < 1 - 7 / shape[-1]] = -INF
+        x[..., 3] = 0.5
+    elif kind == "stairs":                    # the largest in one thread's vectors, many of them alike
+        at = torch.arange(shape[-1])
+        x = torch.where((at // 8) % 256 == 17, 8.0, x.round())
     elif kind == "zeros":
         x = torch.where(x > 0, 0.0, -0.0)
     return x
@@ -126,7 +132,7 @@ def test_forward(nv, rows, vocab, given, top, T, dtype):
     check_forward(nv, x, tokens_of(rows, given, vocab, 3, 0.2), T, top, torch.int32 if rows % 2 else torch.int64)
 
 
-KINDS = ["ties", "equal", "rising", "clumped", "large", "masked", "lowest", "zeros"]
+KINDS = ["ties", "equal", "rising", "clumped", "large", "masked", "lowest", "zeros", "allowed", "stairs"]
 
 
 @pytest.mark.parametrize("kind", KINDS)
