@@ -100,6 +100,7 @@ nvfp4_status nvfp4_token_logprobs_backward(const void* logits, int64_t stride, c
 
 /* The 2-norm over all elements of many tensors, and the coefficient that clips it:
  *   norm[0] = sqrt(sum_i sum_j grad_i[j]^2),   scale[0] = min(1, max_norm / (norm + eps))
+ * (1 where all three are 0).
  * Squares and sums are binary64 (no binary32 input overflows or vanishes), in an order that the
  * sizes fix; both results are rounded once.  An infinite sum of gradients gives norm inf and scale
  * 0, a NaN gives NaN in both.  scale (may be NULL) is what nvfp4_adamw_step takes as grad_scale.

@@ -244,7 +244,8 @@ def clip_grads(plan: AdamWPlan, grads, scale: torch.Tensor, *, out=None):
         out = list(out)
         if len(out) != len(grads):
             raise ValueError("%d outputs for %d gradients" % (len(out), len(grads)))
-        if not plan._seen_out.again(out):
+        # (those that were checked were all of one type, which need not be that of these gradients)
+        if not (out and out[0].dtype == grads[0].dtype and plan._seen_out.again(out)):
             for t, n in zip(out, plan.numels):
                 plan._look("out", t, n, grads[0].dtype)
             plan._seen_out.keep(out)

@@ -4,7 +4,11 @@
 // Squares and sums are binary64, which multiplies and adds at binary32's rate here: nothing
 // overflows, vanishes or needs a second pass.  Workgroups take chunks of the tensors in turn and leave
 // one sum each, which a last workgroup adds in a fixed order.  The tensors' table travels as a kernel
-// argument.
+// argument: nothing is copied ahead and a captured graph holds it.
+//
+// Bound by the tensors' bytes, read once by the norm, read and written once by the clipping, which goes through
+// them from the end.  Measured on one MI355X: norm of 224 million bf16 elements in tensors of all sizes 77 + 4.7 us
+// (5.8 TB/s), of 64 x 2048 x 5120 bf16 221 us (6.1 TB/s), clipping these into other tensors 480 us (5.6 TB/s).
 #include <stdlib.h>
 
 #include <algorithm>
@@ -105,9 +109,10 @@ __global__ __launch_bounds__(1024) void norm_end_kernel(const double* part, int6
   if (threadIdx.x == 0) {
     sum = 0.0;
     for (int w = 0; w < 16; ++w) sum += slots[w];
-    const double all = sqrt(sum), q = max_norm / (all + eps);
+    const double all = sqrt(sum);
     *norm = (float)all;
-    if (scale) *scale = q > 1.0 ? 1.0f : (float)q;
+    // (a NaN goes on; 0 / 0 does not arise)
+    if (scale) *scale = max_norm >= all + eps ? 1.0f : (float)(max_norm / (all + eps));
   }
 }
 

@@ -182,6 +182,31 @@ def test_graphs(nv):
         torch.cuda.synchronize()
 
 
+def test_outputs_of_another_type_than_before(nv):
+    """What was recognized for gradients of one type is not taken for those of another."""
+    plan, grads = plan_of(nv, [5, 4096, 77]), grads_of([5, 4096, 77], BF16, 3)
+    scale = torch.full((1,), 0.5, device="cuda")
+    out = [torch.empty_like(g) for g in grads]
+    nv.clip_grads(plan, grads, scale, out=out)
+    nv.clip_grads(plan, grads, scale, out=out)
+    wide = [g.float() for g in grads]
+    with pytest.raises(TypeError, match="out must be"):
+        nv.clip_grads(plan, wide, scale, out=out)
+    to = [torch.empty_like(g) for g in wide]
+    for _ in range(2):
+        for a, b in zip(nv.clip_grads(plan, wide, scale, out=to), wide):
+            assert torch.equal(a, b * 0.5)
+    with pytest.raises(TypeError, match="out must be"):
+        nv.clip_grads(plan, grads, scale, out=to)
+
+
+def test_a_bound_of_nothing_for_gradients_of_nothing(nv):
+    plan, grads = plan_of(nv, [5, 300]), grads_of([5, 300], F32, 3)
+    zeros = [torch.zeros_like(g) for g in grads]
+    norm, scale = nv.grad_norm(plan, zeros, max_norm=0.0, eps=0.0)
+    assert norm.item() == 0.0 and scale.item() == 1.0
+
+
 def test_the_same_gradient_twice(nv):
     """Counts twice in the norm; scaled into two outputs."""
     plan = plan_of(nv, [500, 500])
