@@ -6,12 +6,20 @@
 // and moves both when m grows: Z 2^-D and (S - D Z) 2^-D for m + D / c.  With exact differences the
 // size of the logits costs no precision, and entropy = ln Z - ln 2 S / Z has no term below 0.
 //
-// Top alternatives without a sort: a column is the vectors that a few threads read; its largest
-// entry and the first vector that holds it are known after the pass.  The k columns that come first by
-// (entry, place) hold all of the top k: an entry of another column comes after k others.  What those
-// columns hold down to the k-th column's entry is read again (20 columns of 256: a thirteenth of the
-// row, from the caches), collected in shared memory, and each entry's place is the number of those
-// before it.  More than fit (many equal or rising entries in few columns) are found one by one.
+// Top alternatives without a sort: a cell is the vectors that a few threads read in a part of the row's
+// length, as many cells as threads; its largest entry and the first vector that holds it are known
+// after the pass.  The k cells that come first by (entry, place) hold all of the top k: an entry of
+// another cell comes after k others.  A bound that a few more than k cells reach is found bit by bit, the vectors
+// of these cells are read again from the caches (24 or so cells of 256: a tenth of the row), what
+// reaches the bound is collected in shared memory, and each entry's place is the number of those before
+// it.  More than fit (many equal or rising entries in few cells) are found one by one.  The order in which the
+// collecting atomics run changes nothing: the numbers are distinct and their places follow from them.
+//
+// Bound by the row's bytes; the exponential of every entry hides behind them at 16 workgroups' wavefronts a
+// compute unit.  Measured on one MI355X: 4096 x 128000 bf16 185 us without alternatives, 203 us with 20 (5.2
+// TB/s); 129 x 151000 binary32 15.5 us (5.0 TB/s); gradient, 4096 x 128000 bf16 402 us (5.2 TB/s).  512 x 128000 with
+// 20 alternatives of rows of which half the entries are equal, or of which few threads hold all large ones, 120-140
+// us, of other rows 37.
 #include "nvfp4_answer.h"
 #include "train_common.h"
 
@@ -226,7 +234,7 @@ __device__ __forceinline__ void find_top(const T* row, uint32_t lo, uint32_t hi,
     if (lane == 0) sh.owners = n, sh.limit = limit, sh.count = 0, sh.vectors = 0;
   }
   __syncthreads();
-  // an entry above the limit's, or equal to it and no further than its vector, is a candidate (of fewer columns
+  // an entry above the limit's, or equal to it and no further than its vector, is a candidate (of fewer cells
   // than `top`, and of less than that many entries at all, everything is)
   const uint64_t limit = sh.limit;
   const int owners = sh.owners;
@@ -616,9 +624,11 @@ __global__ __launch_bounds__(256) void backward_kernel(const BackArgs a) {
 
 constexpr int64_t kMaxVocab = int64_t(1) << 28, kMaxTokenRows = int64_t(1) << 30;
 
-// Workgroups per row: few long rows are shared.
+// Workgroups per row: few long rows are shared by several, where that saves more than a second launch costs.  bf16 with
+// 20 alternatives, one workgroup a row against several: 4 x 128000 23.5 us, 12.1; 192 x 128000 26.1, 25.6; 64 x 65536
+// 16.3, 14.5; 128 x 65536 16.6, 16.1; 4 x 40960 11.5 both; 4 x 32768 10.6, 11.7; 100 x 32768 11.4, 13.7.
 int splits_of(int64_t rows, int64_t vocab) {
-  if (rows <= 0 || rows > 100 || vocab <= 16384) return 1;
+  if (rows <= 0 || vocab < 40960 || rows * 640 > vocab) return 1;
   int64_t want = 512 / rows;
   const int64_t most = (vocab + 4095) / 4096;
   want = want < most ? want : most;
@@ -640,8 +650,11 @@ void launch_forward(const Args& a, hipStream_t s) {
   }
   constexpr int64_t kLine = 1 << 20;                // workgroups in x: threads stay below 2^32
   const dim3 grid((unsigned)(a.rows < kLine ? a.rows : kLine), (unsigned)((a.rows + kLine - 1) / kLine));
-  // a wavefront to a row of up to 16 vectors a lane
-  if (a.vocab <= 64 * 16 * (16 / sizeof(T)) && a.top <= 24) launch_forward<T, 64, false>(a, grid, s);
+  // A wavefront to a row of up to 16 vectors a lane, where there are more rows than the compute units hold workgroups.
+  // bf16, 20 alternatives, 256 threads against 64: 4096 x 512 16.4 us, 9.8; 4096 x 2048 17.7, 13.4; 4096 x 8192 26.7,
+  // 26.4; 8192 x 16384 61, 77; 1024 x 2048 8.1, 8.6; 16 x 8192 7.4, 12.1; 40 alternatives of 64 cells are too
+  // many (4096 x 2048: found one by one).
+  if (a.rows > 2048 && a.vocab <= 64 * 16 * (16 / sizeof(T)) && a.top <= 24) launch_forward<T, 64, false>(a, grid, s);
   else launch_forward<T, 256, false>(a, grid, s);
 }
 

@@ -2,9 +2,9 @@
 
 Tolerances, with u = 2^-24.  d = (x - m) / T carries three roundings of a binary32 operation or constant,
 so a term 2^d of Z is off by 3 |d| u and its own power (2 u); a thread adds vocab / 256 terms or fewer one
-after the other and the rest in a tree, each addition u of the sum.  ln Z is off by as much absolutely
-as Z is relatively; logp adds the roundings of its own d and of the result.  In S = sum d 2^d a term's
-error counts d-fold.  A gradient is p (A y + B) with y = d - z."""
+after the other (vocab / 64 where a wavefront takes a row) and the rest in a tree, each addition u of the
+sum.  ln Z is off by as much absolutely as Z is relatively; logp adds the roundings of its own d and of the
+result.  In S = sum d 2^d a term's error counts d-fold.  A gradient is p (A y + B) with y = d - z."""
 from __future__ import annotations
 
 import math
@@ -68,7 +68,7 @@ def tokens_of(rows, given, vocab, seed, none=0.0):
     return t
 
 
-def reference(x, tokens, T, top):
+def reference(x, tokens, T, top, threads=256):
     """In 64 bits, with the bounds of logp, of entropy and of ln Z."""
     x = x.double().cpu()
     vocab = x.shape[1]
@@ -78,7 +78,7 @@ def reference(x, tokens, T, top):
     total = e.sum(1, keepdim=True)
     p, z = e / total, total.log()
     far = torch.where(e > 0, d, torch.zeros_like(d))
-    n = vocab / 256 + 40
+    n = vocab / threads + 40
     dz = U * (n + 3 * (p * far.abs()).sum(1) + 4)
     h = z[:, 0] - (p * far).sum(1)
     dh = 2 * dz + U * (3 * (p * far * far).sum(1) + (n + 8) * (1 + h))
@@ -99,11 +99,11 @@ def near(got, want, bound):
     assert (off <= bound).all(), (off / bound).max()
 
 
-def check_forward(nv, x, tokens, T, top, itype=torch.int64):
+def check_forward(nv, x, tokens, T, top, itype=torch.int64, threads=256):
     logp, entropy, top_logp, top_index, stats = nv.token_logprobs(x, tokens.to(itype).cuda(), top=top,
                                                                   temperature=T)
     live = (tokens >= 0).any(1)
-    r = reference(x, tokens, T, top)
+    r = reference(x, tokens, T, top, threads)
     bound = lambda v: r["dz"][:, None] + U * (8 * v.abs().nan_to_num(posinf=0.0) + 4 * r["z"][:, None])
     near(logp.cpu()[live], r["logp"][live], bound(r["logp"])[live])
     near(entropy.cpu()[live], r["h"][live], r["dh"][live])
@@ -141,6 +141,32 @@ KINDS = ["ties", "equal", "rising", "clumped", "large", "masked", "lowest", "zer
 def test_forward_of_difficult_rows(nv, rows, vocab, top, dtype, kind):
     x = logits_of((rows, vocab), 5, kind).to(dtype).cuda()
     check_forward(nv, x, tokens_of(rows, 4, vocab, 3), 1.0, top)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rows,vocab,given,top", [
+    (2049, 1, 1, 1), (2100, 7, 2, 7), (2050, 64, 1, 20), (2500, 333, 3, 24), (3001, 2048, 1, 0), (2049, 4095, 1, 24),
+    (2049, 8192, 20, 1), (2100, 8193, 1, 20), (2600, 2000, 64, 64)])
+def test_many_short_rows(nv, rows, vocab, given, top, dtype):
+    x = logits_of((rows, vocab), vocab + rows).to(dtype).cuda()
+    check_forward(nv, x, tokens_of(rows, given, vocab, 3, 0.2), 1.0, top, threads=64)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_many_short_difficult_rows(nv, dtype, kind):
+    x = logits_of((2100, 3333), 5, kind).to(dtype).cuda()
+    check_forward(nv, x, tokens_of(2100, 4, 3333, 3), 1.0, 20, threads=64)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_many_short_rows_without_a_distribution(nv, dtype):
+    x = logits_of((2304, 1001), 1).to(dtype)
+    x[0, 1000], x[1, 0], x[2], x[3, 500], x[4, 3:5], x[5] = NAN, INF, -INF, -NAN, INF, NAN
+    got = [v.cpu() for v in nv.token_logprobs(x.cuda(), tokens_of(2304, 2, 1001, 1).cuda(), top=9)]
+    for v in (got[0], got[1], got[2], got[4]):
+        assert torch.isnan(v[:6]).all() and not torch.isnan(v[6:]).any()
+    assert (got[3][:6] == -1).all() and (got[3][6:] >= 0).all()
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
