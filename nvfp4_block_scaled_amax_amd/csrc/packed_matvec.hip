@@ -1,17 +1,35 @@
 // Products of a few rows with packed NVFP4 weights for gfx950 (include/nvfp4_answer.h defines the
-// operation).
+// operation):  y[m, j] = alpha sum_k x[m, k] code[j, k] scale[j, k / 16].
+//
+// The weights are 0.5625 bytes an element and are read once: with few rows of x that is the floor.
+// At one to sixteen rows a 16x16x32 matrix instruction serves 512 weights in 18 cycles of a wavefront, while
+// turning their codes into bf16 takes the vector unit longer than that, so the work is bound by the
+// reads first and by the vector instructions soon after, never by the matrix cores.
 //
 // A code (2 significant bits) times its E4M3 scale (4) has 6 significant bits and lies between
-// 2^-10 and 2688: exact in bf16.  So the matrix cores take the weights as
-// bf16(code * scale), the rows of x as they are, and alpha comes last.  A row of binary32 x goes in
-// as three rows of bf16 whose sum it is (24 bits in three times 8), which a small kernel writes first.
+// 2^-10 and 2688: exact in bf16.  So the matrix cores take the weights as bf16(code * scale), the rows
+// of x as they are, and alpha comes last.  A row of binary32 x goes in as three columns of bf16 whose sum it is
+// (24 bits in three times 8), split while x is staged.  Of four columns or fewer (FEW) the other twelve of a
+// tile would idle: there the tile's 16 columns are 4 columns of x by 4 groups of 16 elements, zero outside
+// the group's own ("block diagonal"), the codes go in alone, one conversion for two elements, and the
+// four products of a block are scaled in binary32 afterwards.  4096 x 14336 by one row: 10.0 us (3.3 TB/s),
+// with scaled weights 13; 50251 x 4080 by one row 28, scaled 33.
 //
-// A wavefront holds RT tiles of 16 rows of the weights and MT tiles of 16 columns (rows of x).  A
-// lane loads 16 bytes of codes of one weight row at a time (32 elements, two scales); four lanes
-// read 64 bytes in a row.  Their 32 elements are what four matrix instructions take: which k
-// a lane's elements stand for does not matter as long as both operands agree, so the lane
-// reads the same 32 elements of its column of x.  The wavefronts of a workgroup take steps of 128 elements
-// in turn and add up their tiles in shared memory, in order.
+// A wavefront takes units of 16 weight rows by 512 elements: a lane holds 64 bytes of one row's codes
+// (128 elements, eight scales), four lanes a row's 256.  Which k a lane's elements stand for does not
+// matter as long as both operands agree, so the lane reads the same 32 elements at a time of its column of x,
+// from shared memory, where each workgroup puts x (as much as fits) before it starts.  Loading by
+// lines and transposing the codes through shared memory was not faster (50251 x 4080) or slower (64 rows).
+// The last unit of a row ends with the row and overlaps the one before, with x zero there; units past
+// the end are loaded from the first one, so that no branch stands between loads and the waits count them.
+//
+// 2^deal wavefronts share out a tile's units and add up in shared memory, in order; the other
+// wavefronts of the workgroup take further tiles, which share its x.
+//
+// Measured on one MI355X, kernel alone, bf16 x unless it says so: 4096 x 14336 by 1 row 10.0 us; 14336 x 4096 by 16
+// rows 13.2 us, by 24 rows 16, by 64 rows 26; 50251 x 4080 by 7 binary32 rows 40 us (2.9 TB/s); 24 rows to 4 of
+// 64 experts of 2048 x 5120, 44 of them hit, 65 us (4.0 TB/s; the weights' loads alone, without any use
+// of them, take 47); 131072 x 4096 by 16 rows 70 us (4.3 TB/s).
 #include "nvfp4_answer.h"
 #include "train_common.h"
 
@@ -437,10 +455,15 @@ template <typename X>
 void launch(const Matvec& a, hipStream_t stream) {
   constexpr int kOne = 150 * 1024, kFour = 40 * 1024, kGroup = sizeof(X) == 4 ? 3 : 1;
   if (a.expert) {
-    // what an expert gets is not known here: twice its share
+    // What an expert gets is not known here: twice its share is taken for it.  Several small workgroups to a compute
+    // unit, whose starts (the list of rows, x) hide behind each other's loads: 24 rows to 4 of 64 experts of
+    // 2048 x 5120 by 4 wavefronts and 40 KB 62-64 us, by 8 wavefronts 67-72, with two units in flight and 50 KB 70.
     const int64_t E = a.experts, hit = E < a.out_rows ? E : a.out_rows;
     const int64_t columns = (2 * a.out_rows + E - 1) / E * kGroup;
     if (a.cols < kUnit) launch<X, false, 1, 4, 1, true, true>(a, 16, kOne, 0, stream);
+    // The scaled products are faster where a workgroup or two a compute unit are all there is (one row to 4
+    // experts of that size 13 us against 21), and slower where many hide each other's latency (the 24 rows 68-77
+    // against 62-64).
     else if (columns <= 4 && a.rows * hit <= 16384) launch<X, true, 1, 4, 1, true>(a, 4, kFour, 1, stream);
     else if (columns <= 16) launch<X, false, 1, 4, 1, true>(a, 16, kFour, 0, stream);
     else if (columns <= 32) launch<X, false, 2, 8, 2, true>(a, 32, kOne / 2, 0, stream);
@@ -449,11 +472,19 @@ void launch(const Matvec& a, hipStream_t stream) {
     const int64_t columns = a.out_rows * kGroup;
     if (a.cols < kUnit && columns <= 4) launch<X, true, 1, 4, 1, false, true>(a, columns, kOne, 0, stream);
     else if (a.cols < kUnit) launch<X, false, 1, 4, 1, false, true>(a, 16, kOne, 0, stream);
+    // Up to 4 columns, many rows: two tiles a workgroup share an x (50251 x 4080 28.3 us, one wavefront a tile
+    // 32.2, scaled weights 33; 14336 x 4096 10.3, 8 wavefronts 10.7).  Few rows: as many wavefronts as there are
+    // deal a tile's units (4096 x 14336 10.4 us, two units in flight 11.0, scaled weights 13).
     else if (columns <= 4 && a.rows > 6144) launch<X, true, 1, 4, 1, false>(a, columns, kOne, 1, stream);
     else if (columns <= 4) launch<X, true, 1, 8, 1, false>(a, columns, kOne, 1, stream);
+    // Up to 8 columns, two of FEW's tiles: 4096 x 14336 15.5 us against 19; 14336 x 4096 the same (12.4, 11.8), and
+    // with more rows the scaled weights are ahead.
     else if (columns <= 8 && a.rows < 16384) launch<X, true, 2, 8, 2, false>(a, columns, kOne, 0, stream);
+    // 16 wavefronts and one unit in flight each: 14336 x 4096 by 16 rows 12.8 us, 8 wavefronts and two units 13.7; by
+    // 24 rows 16 against 22; 50251 x 4080 by 21 columns 42.7 against 44.
     else if (columns <= 16) launch<X, false, 1, 16, 1, false>(a, columns, kOne, 0, stream);
     else if (columns <= 32) launch<X, false, 2, 16, 1, false>(a, columns, kOne, 0, stream);
+    // More, four tiles of sums a wavefront: registers for 8 wavefronts.  14336 x 4096 by 64 rows 26 us.
     else launch<X, false, 4, 8, 1, false>(a, columns < 64 ? columns : 64, kOne, 0, stream);
   }
 }

@@ -262,6 +262,8 @@ def test_refusals(nv):
         (ValueError, "codes must be", lambda: nv.packed_matvec(x, *one, expert=e)),
         (ValueError, "codes must have shape", lambda: nv.packed_matvec(x[:, :48], *one)),
         (ValueError, "multiple of 16", lambda: nv.packed_matvec(x[:, :40], *one)),
+        (ValueError, "at least 1", lambda: nv.packed_matvec(x[:, :0].contiguous(), c[0, :, :0].contiguous(),
+                                                            s[0, :, :0].contiguous(), a[:1])),
         (ValueError, "alpha must have shape", lambda: nv.packed_matvec(x, c[0], s[0], a)),
         (ValueError, "scales must have shape", lambda: nv.packed_matvec(x, c[0], s[0, :31], a[:1])),
         (ValueError, "contiguous", lambda: nv.packed_matvec(x, c[0].t().contiguous().t(), s[0], a[:1])),
