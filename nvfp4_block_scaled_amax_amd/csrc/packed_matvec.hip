@@ -27,7 +27,7 @@
 // wavefronts of the workgroup take further tiles, which share its x.
 //
 // Measured on one MI355X, kernel alone, bf16 x unless it says so: 4096 x 14336 by 1 row 10.0 us; 14336 x 4096 by 16
-// rows 13.2 us, by 24 rows 16, by 64 rows 26; 50251 x 4080 by 7 binary32 rows 40 us (2.9 TB/s); 24 rows to 4 of
+// rows 13.0 us, by 24 rows 15.6, by 64 rows 24.4; 50251 x 4080 by 7 binary32 rows 40 us (2.9 TB/s); 24 rows to 4 of
 // 64 experts of 2048 x 5120, 44 of them hit, 65 us (4.0 TB/s; the weights' loads alone, without any use
 // of them, take 47); 131072 x 4096 by 16 rows 70 us (4.3 TB/s).
 #include "nvfp4_answer.h"
@@ -120,7 +120,7 @@ __device__ __forceinline__ void thirds(const Vec<float, 8>& v, u32x4 (&r)[3]) {
 }
 
 // SHORT: rows of less than a unit.
-template <typename X, bool FEW, int MT, int W, int DEPTH, bool EXPERT, bool SHORT>
+template <typename X, bool FEW, int MT, int W, bool EXPERT, bool SHORT>
 __global__ __launch_bounds__(W * 64) void matvec_kernel(const Matvec a) {
   constexpr int kCols = FEW ? 4 : 16;                // of a tile
   constexpr int kGroup = sizeof(X) == 4 ? 3 : 1;     // columns of a row of x
@@ -234,8 +234,8 @@ __global__ __launch_bounds__(W * 64) void matvec_kernel(const Matvec a) {
       }
     }
   };
-  // rows of x of which a turn of all wavefronts fits: at least one
-  const int turn = kUnit * deal * DEPTH;
+  // rows of x of which a turn of the wavefronts (a unit each) fits: at least one
+  const int turn = kUnit * deal;
   const int per_pass = min(MT * kCols, a.lds / (turn * 2 + 16)) / kGroup;
   for (int first = 0; first < count; first += per_pass) {
     const int here = min(per_pass, count - first), wide = here * kGroup;
@@ -293,9 +293,8 @@ __global__ __launch_bounds__(W * 64) void matvec_kernel(const Matvec a) {
       return p;
     };
     fetch(0, begin);
-    Unit<S> s[DEPTH];
-#pragma unroll
-    for (int d = 0; d < DEPTH; ++d) load(s[d], wk + d * deal);
+    Unit<S> s;
+    load(s, wk);
     f32x4 acc[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m) acc[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -376,14 +375,9 @@ __global__ __launch_bounds__(W * 64) void matvec_kernel(const Matvec a) {
       }
       lds_barrier();
       const int until = min(from + chunk, all);
-      while (t < until) {
-#pragma unroll
-        for (int d = 0; d < DEPTH; ++d) {
-          add(s[d], t - from);
-          load(s[d], t + DEPTH * deal);
-          t += deal;
-          if (t >= until) break;
-        }
+      for (; t < until; t += deal) {
+        add(s, t - from);
+        load(s, t + deal);
       }
     }
     __syncthreads();                                 // x is read
@@ -425,10 +419,10 @@ __global__ __launch_bounds__(W * 64) void matvec_kernel(const Matvec a) {
 }
 
 // `room`: shared memory for x, so that one (150 KB), two or more workgroups share a compute unit.
-template <typename X, bool FEW, int MT, int W, int DEPTH, bool EXPERT, bool SHORT = false>
+template <typename X, bool FEW, int MT, int W, bool EXPERT, bool SHORT = false>
 void launch(Matvec a, int64_t columns, int room, int deal, hipStream_t stream) {
   const int64_t tiles = (a.rows + 15) / 16, units = (a.cols + kUnit - 1) / kUnit;
-  const auto turn = [](int deal) { return (kUnit * DEPTH * 2 << deal) + 16; };     // bytes of a column
+  const auto turn = [](int deal) { return (kUnit * 2 << deal) + 16; };     // bytes of a column
   const int64_t hit = a.experts < a.out_rows ? a.experts : a.out_rows;       // weights that are read
   // enough workgroups for the compute units: where the rows are few, more wavefronts deal a tile's units, as
   // far as there are units and every column fits
@@ -445,47 +439,55 @@ void launch(Matvec a, int64_t columns, int room, int deal, hipStream_t stream) {
   constexpr int kSums = W * MT * (FEW ? 256 : 1024);
   const int bytes = a.lds > kSums ? a.lds : kSums;
   const dim3 grid((unsigned)((tiles + (W >> a.deal) - 1) / (W >> a.deal)), (unsigned)a.experts);
-  const auto kernel = matvec_kernel<X, FEW, MT, W, DEPTH, EXPERT, SHORT>;
+  const auto kernel = matvec_kernel<X, FEW, MT, W, EXPERT, SHORT>;
   if (bytes > 60 * 1024)
     (void)hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
   kernel<<<grid, W * 64, bytes, stream>>>(a);
 }
 
+// Which form, after a sweep of all of them over 420 single matrices (256 to 131072 rows, 848 to 16384 columns, 1 to 64
+// rows of x of both types) and 404 of 8 to 64 experts (256 to 8192 rows, 512 to 10848 columns, one token to
+// 128, 1 to 8 picks, some experts picked more often), weights from memory: the single ones are within 1.5 % of
+// the fastest form on average, the experts' within 5 %.  The figures are us, of experts the geometric means of
+// the cases that a rule takes.
 template <typename X>
 void launch(const Matvec& a, hipStream_t stream) {
-  constexpr int kOne = 150 * 1024, kFour = 40 * 1024, kGroup = sizeof(X) == 4 ? 3 : 1;
+  constexpr int kOne = 150 * 1024, kTwo = 75 * 1024, kFour = 40 * 1024, kGroup = sizeof(X) == 4 ? 3 : 1;
+  const int64_t units = (a.cols + kUnit - 1) / kUnit;
   if (a.expert) {
-    // What an expert gets is not known here: twice its share is taken for it.  Several small workgroups to a compute
-    // unit, whose starts (the list of rows, x) hide behind each other's loads: 24 rows to 4 of 64 experts of
-    // 2048 x 5120 by 4 wavefronts and 40 KB 62-64 us, by 8 wavefronts 67-72, with two units in flight and 50 KB 70.
-    const int64_t E = a.experts, hit = E < a.out_rows ? E : a.out_rows;
-    const int64_t columns = (2 * a.out_rows + E - 1) / E * kGroup;
-    if (a.cols < kUnit) launch<X, false, 1, 4, 1, true, true>(a, 16, kOne, 0, stream);
-    // The scaled products are faster where a workgroup or two a compute unit are all there is (one row to 4
-    // experts of that size 13 us against 21), and slower where many hide each other's latency (the 24 rows 68-77
-    // against 62-64).
-    else if (columns <= 4 && a.rows * hit <= 16384) launch<X, true, 1, 4, 1, true>(a, 4, kFour, 1, stream);
-    else if (columns <= 16) launch<X, false, 1, 4, 1, true>(a, 16, kFour, 0, stream);
-    else if (columns <= 32) launch<X, false, 2, 8, 2, true>(a, 32, kOne / 2, 0, stream);
-    else launch<X, false, 4, 8, 1, true>(a, 64, kOne, 0, stream);
+    // What an expert gets is not known here: `all` / E columns on average.
+    const int64_t E = a.experts, all = a.out_rows * kGroup, hit = E < a.out_rows ? E : a.out_rows;
+    if (a.cols < kUnit) launch<X, false, 1, 4, true, true>(a, 16, kOne, 0, stream);
+    // Many columns, 64 a pass: 49.6, 32 columns 57.7, 16 66.
+    else if (all >= 12 * E) launch<X, false, 4, 8, true>(a, 64, kOne, 0, stream);
+    // Few, of up to 64000 weight rows: the scaled products, 10.8, with 8 wavefronts 11.3, scaled weights 12.6.
+    else if (all * kGroup <= E && hit * a.rows < 64000) launch<X, true, 1, 4, true>(a, 4, kFour, 1, stream);
+    // 32 columns a pass: 46.6, 16 columns 55, 64 62.
+    else if (all > 6 * E && units > 4) launch<X, false, 2, 16, true>(a, 32, kOne, 0, stream);
+    // Long rows and few of them: 16 wavefronts share a tile's units, 20.1, 8 20.9, 4 24.4.
+    else if (units > 4 && hit * a.rows < 40000) launch<X, false, 1, 16, true>(a, 16, kOne, 0, stream);
+    // The others: small workgroups, whose starts (the list of rows, x) hide behind each other's loads, 18.2, with 8
+    // wavefronts 19.2, with 16 22.8.
+    else launch<X, false, 1, 4, true>(a, 16, kFour, 0, stream);
   } else {
-    const int64_t columns = a.out_rows * kGroup;
-    if (a.cols < kUnit && columns <= 4) launch<X, true, 1, 4, 1, false, true>(a, columns, kOne, 0, stream);
-    else if (a.cols < kUnit) launch<X, false, 1, 4, 1, false, true>(a, 16, kOne, 0, stream);
-    // Up to 4 columns, many rows: two tiles a workgroup share an x (50251 x 4080 28.3 us, one wavefront a tile
-    // 32.2, scaled weights 33; 14336 x 4096 10.3, 8 wavefronts 10.7).  Few rows: as many wavefronts as there are
-    // deal a tile's units (4096 x 14336 10.4 us, two units in flight 11.0, scaled weights 13).
-    else if (columns <= 4 && a.rows > 6144) launch<X, true, 1, 4, 1, false>(a, columns, kOne, 1, stream);
-    else if (columns <= 4) launch<X, true, 1, 8, 1, false>(a, columns, kOne, 1, stream);
-    // Up to 8 columns, two of FEW's tiles: 4096 x 14336 15.5 us against 19; 14336 x 4096 the same (12.4, 11.8), and
-    // with more rows the scaled weights are ahead.
-    else if (columns <= 8 && a.rows < 16384) launch<X, true, 2, 8, 2, false>(a, columns, kOne, 0, stream);
-    // 16 wavefronts and one unit in flight each: 14336 x 4096 by 16 rows 12.8 us, 8 wavefronts and two units 13.7; by
-    // 24 rows 16 against 22; 50251 x 4080 by 21 columns 42.7 against 44.
-    else if (columns <= 16) launch<X, false, 1, 16, 1, false>(a, columns, kOne, 0, stream);
-    else if (columns <= 32) launch<X, false, 2, 16, 1, false>(a, columns, kOne, 0, stream);
-    // More, four tiles of sums a wavefront: registers for 8 wavefronts.  14336 x 4096 by 64 rows 26 us.
-    else launch<X, false, 4, 8, 1, false>(a, columns < 64 ? columns : 64, kOne, 0, stream);
+    const int64_t columns = a.out_rows * kGroup, x_bytes = columns * (units * kUnit * 2 + 16);
+    if (a.cols < kUnit && columns <= 4) launch<X, true, 1, 4, false, true>(a, columns, kOne, 0, stream);
+    else if (a.cols < kUnit) launch<X, false, 1, 4, false, true>(a, 16, kOne, 0, stream);
+    // The scaled products; 4 wavefronts for short rows and for so many that each workgroup's x is read often
+    // (50251 x 4080 28.3, 8 wavefronts 30.3; 4096 x 1024 4.2 and 5.0), 8 for the others (8192 x 8192 12.0 and 15.5).
+    else if (columns <= 4 && (units <= 2 || a.rows > 32768))
+      launch<X, true, 1, 4, false>(a, columns, kOne, 1, stream);
+    else if (columns <= 4) launch<X, true, 1, 8, false>(a, columns, kOne, 1, stream);
+    // Up to 16 columns, the smallest workgroup that holds all of x: 4096 x 1024 by 16 rows of 4 wavefronts 5.0, of 8
+    // 6.1, of 16 8.6; 4096 x 4096 by 8 rows 7.3, 6.6, 8.9; 14336 x 4096 by 16 rows, more than 8 have room for,
+    // 14.1 by 8, 13.0 by 16.
+    else if (columns <= 16 && x_bytes <= kFour) launch<X, false, 1, 4, false>(a, columns, kFour, 0, stream);
+    else if (columns <= 16 && x_bytes <= kTwo) launch<X, false, 1, 8, false>(a, columns, kTwo, 0, stream);
+    else if (columns <= 16) launch<X, false, 1, 16, false>(a, columns, kOne, 0, stream);
+    // Up to 32, two tiles of sums and 16 wavefronts where there are many rows (50251 x 4080 by 24 columns 40.8, 8
+    // wavefronts of four tiles 57.9); else four tiles (4096 x 4096 by 24 columns 12.6, 15.6 by two tiles).
+    else if (columns <= 32 && a.rows > 8192) launch<X, false, 2, 16, false>(a, columns, kOne, 0, stream);
+    else launch<X, false, 4, 8, false>(a, columns < 64 ? columns : 64, kOne, 0, stream);
   }
 }
 

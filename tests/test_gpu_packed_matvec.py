@@ -71,6 +71,13 @@ def test_exact_sums(nv, tokens, rows, cols, xtype, ytype):
     assert same(got, want)
 
 
+@pytest.mark.parametrize("xtype", [BF16, F32])
+@pytest.mark.parametrize("tokens,rows,cols", [(1, 32801, 1040), (4, 130, 2000), (8, 90, 4112), (4, 70, 2576),
+                                              (20, 8211, 1040), (7, 8211, 1040), (9, 61, 12304)])
+def test_exact_sums_of_more_sizes(nv, tokens, rows, cols, xtype):
+    test_exact_sums(nv, tokens, rows, cols, xtype, F32)
+
+
 @pytest.mark.parametrize("bits", [9, 16, 17, 24])
 def test_every_bit_of_32_bit_rows_counts(nv, bits):
     """x of up to 24 significant bits against one weight of 1 per row: y is x."""
@@ -110,6 +117,26 @@ def test_experts(nv, picks, itype, tokens, E, rows, cols, xtype, ytype):
                            expert=expert.cuda(), dtype=ytype, y=y)
     assert got is y
     assert same(got.view(tokens * k, rows), want)
+
+
+@pytest.mark.parametrize("picks,tokens,E,rows,cols", [
+    (4, 60, 3, 40, 1552), (2, 12, 16, 70, 1008), (2, 20, 5, 100, 2064), (1, 14, 5, 50, 5136), (2, 3, 8, 100, 4112),
+    (1, 9, 9, 33, 10848), (1, 12, 8, 50, 1552), (1, 12, 64, 20, 1552), (2, 10, 5, 60, 4112), (1, 8, 10, 47, 8176),
+    (1, 7, 8, 8003, 1040), (1, 7, 64, 20, 1552)])
+@pytest.mark.parametrize("one", [False, True])
+@pytest.mark.parametrize("xtype,ytype", [(BF16, F32), (F32, BF16)])
+def test_experts_of_long_rows(nv, picks, tokens, E, rows, cols, one, xtype, ytype):
+    """Rows of several units; every token at the same expert, which is more than its share."""
+    codes, scales, alpha, value = weights((E, rows, cols), tokens)
+    x = whole((tokens, cols), 5)
+    expert = torch.full((tokens, picks), E // 2) if one else torch.randint(0, E, (tokens, picks), generator=gen(3))
+    want = torch.empty(tokens, picks, rows, dtype=ytype)
+    for e in expert.unique().tolist():
+        at = (expert == e).nonzero()
+        want[at[:, 0], at[:, 1]] = rounded(x[at[:, 0]].double() @ value[e].t(), alpha[e], ytype)
+    got = nv.packed_matvec(x.to(xtype).cuda(), codes.cuda(), scales.cuda(), alpha.cuda(), expert=expert.cuda(),
+                           dtype=ytype)
+    assert same(got, want)
 
 
 def test_no_row_has_an_expert(nv):
