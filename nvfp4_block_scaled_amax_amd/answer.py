@@ -200,7 +200,7 @@ def _table(plan: AdamWPlan, grads) -> bytes:
     """The entries of nvfp4_grad_tensor for these tensors.  (Packed at once: half the time of an array of
     numpy's, and of each call its own.)"""
     entries = [0] * (2 * len(grads))
-    entries[0::2] = [g.data_ptr() for g in grads]
+    entries[0::2] = map(torch.Tensor.data_ptr, grads)
     entries[1::2] = plan.numels
     return struct.pack("%dq" % len(entries), *entries)
 

@@ -30,6 +30,8 @@
 // rows 13.0 us, by 24 rows 15.6, by 64 rows 24.4; 50251 x 4080 by 7 binary32 rows 40 us (2.9 TB/s); 24 rows to 4 of
 // 64 experts of 2048 x 5120, 44 of them hit, 65 us (4.0 TB/s; the weights' loads alone, without any use
 // of them, take 47); 131072 x 4096 by 16 rows 70 us (4.3 TB/s).
+#include <algorithm>
+
 #include "nvfp4_answer.h"
 #include "train_common.h"
 
@@ -167,7 +169,7 @@ __global__ __launch_bounds__(W * 64) void matvec_kernel(const Matvec a) {
     }
     __syncthreads();
     count = counts[0];
-    for (int i = 0; i < counts[1]; ++i) {              // expert 0's workgroups write zeros
+    for (int i = 0; i < counts[1] && blockIdx.z == 0; ++i) {      // expert 0's workgroups write zeros
       const int64_t m = list[kMaxRows - 1 - i];
       for (int64_t j = row0 + threadIdx.x; j < row0 + (W * 16 >> a.deal) && j < a.rows; j += W * 64) {
         if (a.f32) ((float*)a.y)[m * a.rows + j] = 0.0f;
@@ -237,7 +239,7 @@ __global__ __launch_bounds__(W * 64) void matvec_kernel(const Matvec a) {
   // rows of x of which a turn of the wavefronts (a unit each) fits: at least one
   const int turn = kUnit * deal;
   const int per_pass = min(MT * kCols, a.lds / (turn * 2 + 16)) / kGroup;
-  for (int first = 0; first < count; first += per_pass) {
+  for (int first = blockIdx.z * per_pass; first < count; first += per_pass * gridDim.z) {
     const int here = min(per_pass, count - first), wide = here * kGroup;
     // x: all of it, or as many elements of each column as fit, a multiple of a turn
     const int fit = (a.lds / wide - 16) / 2, chunk = (fit >= all * kUnit ? all * kUnit : fit / turn * turn) / kUnit;
@@ -438,56 +440,76 @@ void launch(Matvec a, int64_t columns, int room, int deal, hipStream_t stream) {
   if (a.lds < least) a.lds = least;
   constexpr int kSums = W * MT * (FEW ? 256 : 1024);
   const int bytes = a.lds > kSums ? a.lds : kSums;
-  const dim3 grid((unsigned)((tiles + (W >> a.deal) - 1) / (W >> a.deal)), (unsigned)a.experts);
+  // The passes over the rows of x (of an expert: over twice its share) go one after the other or, where that leaves
+  // compute units without a workgroup, side by side: 2048 x 8192 by 64 rows 15.1 us, 40.9 one after the other with 64
+  // rows a pass.
+  constexpr int kFull = EXPERT ? 4096 : 8192;                                // wavefronts
+  const int64_t per_pass = std::min(MT * (FEW ? 4 : 16), a.lds / turn(a.deal)) / (sizeof(X) == 4 ? 3 : 1);
+  const int64_t groups = (tiles + (W >> a.deal) - 1) / (W >> a.deal), full = kFull / (groups * hit * W) + 1;
+  const int64_t likely = (a.out_rows * (EXPERT ? 2 : 1) + a.experts - 1) / a.experts;
+  const dim3 grid((unsigned)groups, (unsigned)a.experts,
+                  (unsigned)std::min<int64_t>((likely + per_pass - 1) / per_pass, full));
   const auto kernel = matvec_kernel<X, FEW, MT, W, EXPERT, SHORT>;
   if (bytes > 60 * 1024)
     (void)hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
   kernel<<<grid, W * 64, bytes, stream>>>(a);
 }
 
-// Which form, after a sweep of all of them over 420 single matrices (256 to 131072 rows, 848 to 16384 columns, 1 to 64
-// rows of x of both types) and 404 of 8 to 64 experts (256 to 8192 rows, 512 to 10848 columns, one token to
-// 128, 1 to 8 picks, some experts picked more often), weights from memory: the single ones are within 1.5 % of
-// the fastest form on average, the experts' within 5 %.  The figures are us, of experts the geometric means of
-// the cases that a rule takes.
+// Which form, after sweeps of all of them over 608 single matrices (128 to 131072 rows, 848 to 16384 columns, 2 to 256
+// rows of x of both types) and 450 of 4 to 64 experts (256 to 8192 rows, 512 to 10848 columns, one token to
+// 128, 1 to 8 picks, some experts picked more often), weights from memory: the single ones are within 3 % of the
+// fastest form on average, the experts' within 6 %.  The figures are us, geometric means of the cases that a
+// rule takes where no size stands with them.
 template <typename X>
 void launch(const Matvec& a, hipStream_t stream) {
   constexpr int kOne = 150 * 1024, kTwo = 75 * 1024, kFour = 40 * 1024, kGroup = sizeof(X) == 4 ? 3 : 1;
   const int64_t units = (a.cols + kUnit - 1) / kUnit;
   if (a.expert) {
     // What an expert gets is not known here: `all` / E columns on average.
-    const int64_t E = a.experts, all = a.out_rows * kGroup, hit = E < a.out_rows ? E : a.out_rows;
+    const int64_t E = a.experts, all = a.out_rows * kGroup, rows = a.rows * std::min<int64_t>(E, a.out_rows);
+    const int64_t work = rows * ((all + 16 * E - 1) / (16 * E));
     if (a.cols < kUnit) launch<X, false, 1, 4, true, true>(a, 16, kOne, 0, stream);
-    // Many columns, 64 a pass: 49.6, 32 columns 57.7, 16 66.
-    else if (all >= 12 * E) launch<X, false, 4, 8, true>(a, 64, kOne, 0, stream);
-    // Few, of up to 64000 weight rows: the scaled products, 10.8, with 8 wavefronts 11.3, scaled weights 12.6.
-    else if (all * kGroup <= E && hit * a.rows < 64000) launch<X, true, 1, 4, true>(a, 4, kFour, 1, stream);
-    // 32 columns a pass: 46.6, 16 columns 55, 64 62.
-    else if (all > 6 * E && units > 4) launch<X, false, 2, 16, true>(a, 32, kOne, 0, stream);
-    // Long rows and few of them: 16 wavefronts share a tile's units, 20.1, 8 20.9, 4 24.4.
-    else if (units > 4 && hit * a.rows < 40000) launch<X, false, 1, 16, true>(a, 16, kOne, 0, stream);
-    // The others: small workgroups, whose starts (the list of rows, x) hide behind each other's loads, 18.2, with 8
-    // wavefronts 19.2, with 16 22.8.
+    // Many columns, 64 a pass: 65, 32 columns 67-77, 16 84.
+    else if (all >= 20 * E && work > 25000) launch<X, false, 4, 8, true>(a, 64, kOne, 0, stream);
+    // Few: the scaled products, 10.7, with 8 wavefronts 11.2, scaled weights 12.4.
+    else if (all * kGroup <= E && rows < 64000) launch<X, true, 1, 4, true>(a, 4, kFour, 1, stream);
+    // 32 columns a pass: 49.3, 16 columns 49.3-56, 64 54.7.
+    else if (units > 4 && all > 5 * E && work > 14700) launch<X, false, 2, 16, true>(a, 32, kOne, 0, stream);
+    // Long rows and few of them: 16 wavefronts share a tile's units, 20.1, 8 21.3, 4 25.7.
+    else if (units > 4 && rows < 25000) launch<X, false, 1, 16, true>(a, 16, kOne, 0, stream);
+    // The others: small workgroups, whose starts (the list of rows, x) hide behind each other's loads, 18.3, with 8
+    // wavefronts 19.5, with 16 23.9.
     else launch<X, false, 1, 4, true>(a, 16, kFour, 0, stream);
-  } else {
-    const int64_t columns = a.out_rows * kGroup, x_bytes = columns * (units * kUnit * 2 + 16);
-    if (a.cols < kUnit && columns <= 4) launch<X, true, 1, 4, false, true>(a, columns, kOne, 0, stream);
-    else if (a.cols < kUnit) launch<X, false, 1, 4, false, true>(a, 16, kOne, 0, stream);
+    return;
+  }
+  const int64_t columns = a.out_rows * kGroup, work = a.rows * ((columns + 15) / 16);
+  const int64_t some = std::min<int64_t>(columns, 16), x = some * units;
+  if (a.cols < kUnit && columns <= 4) {
+    launch<X, true, 1, 4, false, true>(a, columns, kOne, 0, stream);
+  } else if (a.cols < kUnit) {
+    launch<X, false, 1, 4, false, true>(a, 16, kOne, 0, stream);
+  } else if (columns <= 4) {
     // The scaled products; 4 wavefronts for short rows and for so many that each workgroup's x is read often
     // (50251 x 4080 28.3, 8 wavefronts 30.3; 4096 x 1024 4.2 and 5.0), 8 for the others (8192 x 8192 12.0 and 15.5).
-    else if (columns <= 4 && (units <= 2 || a.rows > 32768))
-      launch<X, true, 1, 4, false>(a, columns, kOne, 1, stream);
-    else if (columns <= 4) launch<X, true, 1, 8, false>(a, columns, kOne, 1, stream);
-    // Up to 16 columns, the smallest workgroup that holds all of x: 4096 x 1024 by 16 rows of 4 wavefronts 5.0, of 8
-    // 6.1, of 16 8.6; 4096 x 4096 by 8 rows 7.3, 6.6, 8.9; 14336 x 4096 by 16 rows, more than 8 have room for,
-    // 14.1 by 8, 13.0 by 16.
-    else if (columns <= 16 && x_bytes <= kFour) launch<X, false, 1, 4, false>(a, columns, kFour, 0, stream);
-    else if (columns <= 16 && x_bytes <= kTwo) launch<X, false, 1, 8, false>(a, columns, kTwo, 0, stream);
-    else if (columns <= 16) launch<X, false, 1, 16, false>(a, columns, kOne, 0, stream);
-    // Up to 32, two tiles of sums and 16 wavefronts where there are many rows (50251 x 4080 by 24 columns 40.8, 8
-    // wavefronts of four tiles 57.9); else four tiles (4096 x 4096 by 24 columns 12.6, 15.6 by two tiles).
-    else if (columns <= 32 && a.rows > 8192) launch<X, false, 2, 16, false>(a, columns, kOne, 0, stream);
-    else launch<X, false, 4, 8, false>(a, columns < 64 ? columns : 64, kOne, 0, stream);
+    if (units <= 2 || a.rows > 32768) launch<X, true, 1, 4, false>(a, columns, kOne, 1, stream);
+    else launch<X, true, 1, 8, false>(a, columns, kOne, 1, stream);
+  } else if (columns <= 16 || work <= 14700) {
+    // 16 columns a pass, by the smallest workgroup that holds them whole: of 4 wavefronts 5.8, where 8 take 6.8 and 16
+    // 9.4; of 8 10.2, where 4 take 11.5 and 16 12.7; of 16 21.7, where 8 take 22.6 and 4 27.8.
+    if (x <= 36) launch<X, false, 1, 4, false>(a, some, kFour, 0, stream);
+    else if (x <= 72) launch<X, false, 1, 8, false>(a, some, kTwo, 0, stream);
+    // Long rows and few of them: the scaled products, 8 columns a pass, 10.6, the other forms 14.3 or more.
+    else if (a.rows * ((columns + 7) / 8) <= 4100)
+      launch<X, true, 2, 8, false>(a, std::min<int64_t>(columns, 8), kOne, 0, stream);
+    // (more than one pass over rows of up to 10 units, by 8 wavefronts: 12.1, by 16 14.3)
+    else if (columns > 16 && units <= 10) launch<X, false, 1, 8, false>(a, some, kTwo, 0, stream);
+    else launch<X, false, 1, 16, false>(a, some, kOne, 0, stream);
+  } else if (columns <= 32 || work <= 35000) {
+    // 32 columns a pass: 22.4, 16 columns 26.4, 64 29.2.
+    launch<X, false, 2, 16, false>(a, std::min<int64_t>(columns, 32), kOne, 0, stream);
+  } else {
+    // 64 columns a pass: 54.3, 32 columns 62.4, 16 68.3.
+    launch<X, false, 4, 8, false>(a, std::min<int64_t>(columns, 64), kOne, 0, stream);
   }
 }
 

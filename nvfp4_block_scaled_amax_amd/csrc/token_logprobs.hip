@@ -17,7 +17,7 @@
 //
 // Bound by the row's bytes; the exponential of every entry hides behind them at 16 workgroups' wavefronts a
 // compute unit.  Measured on one MI355X: 4096 x 128000 bf16 185 us without alternatives, 203 us with 20 (5.2
-// TB/s); 129 x 151000 binary32 15.5 us (5.0 TB/s); gradient, 4096 x 128000 bf16 402 us (5.2 TB/s).  512 x 128000 with
+// TB/s); 129 x 151000 binary32 15.5 us (5.0 TB/s); gradient, 4096 x 128000 bf16 385 us (5.4 TB/s).  512 x 128000 with
 // 20 alternatives of rows of which half the entries are equal, or of which few threads hold all large ones, 120-140
 // us, of other rows 37.
 #include "nvfp4_answer.h"
@@ -537,7 +537,10 @@ struct BackArgs {
 // A workgroup takes a part of a row.  With y = log2 p: grad = p (A y + B), A = -h ln 2 / T,
 // B = -(sum g + h entropy) / T; the given tokens' entries are read before anything is written (grad may be
 // logits) and written again at the end with what their g adds.
-template <typename T>
+// STREAM: past the caches, of a gradient that is more than they hold.  4096 x 128000 bf16 385 us, through them 403; 128
+// x 151000 binary32, which the last-level cache holds, 37.6 and 42.4, but with a reader after it (grad_norm)
+// 50.2 and 44.2.
+template <typename T, bool STREAM>
 __global__ __launch_bounds__(256) void backward_kernel(const BackArgs a) {
   constexpr int N = 16 / sizeof(T), THREADS = 256;
   __shared__ int64_t id[kMost];
@@ -606,7 +609,7 @@ __global__ __launch_bounds__(256) void backward_kernel(const BackArgs a) {
     float r[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) r[k] = value(v[k]);
-    store_vec<kAny>(grad, to, hi, make_vec<T>(r));
+    store_vec<kAny, STREAM>(grad, to, hi, make_vec<T>(r));
   };
   while (more) {
     const uint32_t then = at + kAhead * step;
@@ -622,6 +625,7 @@ __global__ __launch_bounds__(256) void backward_kernel(const BackArgs a) {
   if (fixes) grad[mine] = from_f32<T>(fix);
 }
 
+constexpr int64_t kCached = int64_t(128) << 20;       // bytes that are likely to stay in the last-level cache
 constexpr int64_t kMaxVocab = int64_t(1) << 28, kMaxTokenRows = int64_t(1) << 30;
 
 // Workgroups per row: few long rows are shared by several, where that saves more than a second launch costs.  bf16 with
@@ -656,6 +660,12 @@ void launch_forward(const Args& a, hipStream_t s) {
   // many (4096 x 2048: found one by one).
   if (a.rows > 2048 && a.vocab <= 64 * 16 * (16 / sizeof(T)) && a.top <= 24) launch_forward<T, 64, false>(a, grid, s);
   else launch_forward<T, 256, false>(a, grid, s);
+}
+
+template <typename T>
+void launch_backward(const BackArgs& a, dim3 grid, hipStream_t s) {
+  if (a.rows * a.vocab * (int64_t)sizeof(T) > kCached) backward_kernel<T, true><<<grid, 256, 0, s>>>(a);
+  else backward_kernel<T, false><<<grid, 256, 0, s>>>(a);
 }
 
 bool temperature_ok(float temperature, float& inv_t, float& c) {
@@ -751,7 +761,7 @@ NVFP4_EXPORT nvfp4_status nvfp4_token_logprobs_backward(const void* logits, int6
                       (uint32_t)vocab, size, (int)given, itype == NVFP4_I64, c, inv_t};
   const dim3 grid((unsigned)((vocab + size - 1) / size), (unsigned)line, (unsigned)((rows + line - 1) / line));
   (void)hipGetLastError();
-  if (type == NVFP4_T_BF16) backward_kernel<bf16><<<grid, 256, 0, stream>>>(a);
-  else backward_kernel<float><<<grid, 256, 0, stream>>>(a);
+  if (type == NVFP4_T_BF16) launch_backward<bf16>(a, grid, stream);
+  else launch_backward<float>(a, grid, stream);
   return launched();
 }

@@ -73,7 +73,10 @@ def test_exact_sums(nv, tokens, rows, cols, xtype, ytype):
 
 @pytest.mark.parametrize("xtype", [BF16, F32])
 @pytest.mark.parametrize("tokens,rows,cols", [(1, 32801, 1040), (4, 130, 2000), (8, 90, 4112), (4, 70, 2576),
-                                              (20, 8211, 1040), (7, 8211, 1040), (9, 61, 12304)])
+                                              (20, 8211, 1040), (7, 8211, 1040), (9, 61, 12304),
+                                              (40, 8211, 1040), (300, 130, 496), (1024, 70, 1040), (1000, 33, 4112),
+                                              (64, 515, 8208), (100, 2000, 4112), (90, 4100, 1552), (40, 515, 8208),
+                                              (12, 1000, 4112), (70, 12290, 528)])
 def test_exact_sums_of_more_sizes(nv, tokens, rows, cols, xtype):
     test_exact_sums(nv, tokens, rows, cols, xtype, F32)
 
@@ -122,7 +125,9 @@ def test_experts(nv, picks, itype, tokens, E, rows, cols, xtype, ytype):
 @pytest.mark.parametrize("picks,tokens,E,rows,cols", [
     (4, 60, 3, 40, 1552), (2, 12, 16, 70, 1008), (2, 20, 5, 100, 2064), (1, 14, 5, 50, 5136), (2, 3, 8, 100, 4112),
     (1, 9, 9, 33, 10848), (1, 12, 8, 50, 1552), (1, 12, 64, 20, 1552), (2, 10, 5, 60, 4112), (1, 8, 10, 47, 8176),
-    (1, 7, 8, 8003, 1040), (1, 7, 64, 20, 1552)])
+    (1, 7, 8, 8003, 1040), (1, 7, 64, 20, 1552), (2, 100, 4, 130, 1552),
+    (8, 128, 16, 64, 2576), (1, 1000, 3, 40, 4112), (4, 200, 8, 33, 400), (3, 90, 6, 3001, 1040),
+    (2, 24, 6, 1700, 2576)])
 @pytest.mark.parametrize("one", [False, True])
 @pytest.mark.parametrize("xtype,ytype", [(BF16, F32), (F32, BF16)])
 def test_experts_of_long_rows(nv, picks, tokens, E, rows, cols, one, xtype, ytype):

@@ -356,6 +356,21 @@ def test_far_rows(nv):
     assert abs(x[-2, 0].item() - 1) < 0.01 and abs(x[-2, 1].item() + 1 / vocab) < 1e-6
 
 
+@pytest.mark.parametrize("dtype,rows", [(BF16, 1400), (F32, 700)])
+def test_a_gradient_that_no_cache_holds(nv, dtype, rows):
+    """More than 128 MB at once: the bits of 100 rows at a time."""
+    vocab = 50001
+    wide = torch.randn(rows, vocab + 6, generator=torch.Generator("cuda").manual_seed(1), device="cuda").to(dtype)
+    x, t = wide[:, 3:3 + vocab], tokens_of(rows, 3, vocab, 2, 0.5).cuda()
+    entropy, stats = nv.token_logprobs(x, t)[1::3]
+    d, h = torch.randn(rows, 3, device="cuda"), torch.randn(rows, device="cuda")
+    whole = nv.token_logprobs_backward(x, t, stats, d, entropy=entropy, dentropy=h)
+    for i in range(0, rows, 100):
+        part = slice(i, i + 100)
+        got = nv.token_logprobs_backward(x[part], t[part], stats[part], d[part], entropy=entropy[part], dentropy=h[part])
+        assert torch.equal(got, whole[part])
+
+
 @pytest.mark.parametrize("rows,vocab", [(3, 1500), (2, 90000)])
 def test_graphs_and_streams(nv, rows, vocab):
     """Both ways captured on a stream of its own, replayed with other logits, eager calls between: the same
