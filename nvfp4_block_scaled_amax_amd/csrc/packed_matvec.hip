@@ -442,7 +442,7 @@ void launch(Matvec a, int64_t columns, int room, int deal, hipStream_t stream) {
   const int bytes = a.lds > kSums ? a.lds : kSums;
   // The passes over the rows of x (of an expert: over twice its share) go one after the other or, where that leaves
   // compute units without a workgroup, side by side: 2048 x 8192 by 64 rows 15.1 us, 40.9 one after the other with 64
-  // rows a pass.
+  // rows a pass; 512 x 496 by 1024 rows 7.1, 246.
   constexpr int kFull = EXPERT ? 4096 : 8192;                                // wavefronts
   const int64_t per_pass = std::min(MT * (FEW ? 4 : 16), a.lds / turn(a.deal)) / (sizeof(X) == 4 ? 3 : 1);
   const int64_t groups = (tiles + (W >> a.deal) - 1) / (W >> a.deal), full = kFull / (groups * hit * W) + 1;

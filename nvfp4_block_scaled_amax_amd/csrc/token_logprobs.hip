@@ -17,7 +17,7 @@
 //
 // Bound by the row's bytes; the exponential of every entry hides behind them at 16 workgroups' wavefronts a
 // compute unit.  Measured on one MI355X: 4096 x 128000 bf16 185 us without alternatives, 203 us with 20 (5.2
-// TB/s); 129 x 151000 binary32 15.5 us (5.0 TB/s); gradient, 4096 x 128000 bf16 385 us (5.4 TB/s).  512 x 128000 with
+// TB/s); 515 x 50251 binary32 of which a quarter is not read 15.5 us (5.0 TB/s); gradient, 4096 x 128000 bf16 385 us (5.4 TB/s).  512 x 128000 with
 // 20 alternatives of rows of which half the entries are equal, or of which few threads hold all large ones, 120-140
 // us, of other rows 37.
 #include "nvfp4_answer.h"
@@ -537,9 +537,9 @@ struct BackArgs {
 // A workgroup takes a part of a row.  With y = log2 p: grad = p (A y + B), A = -h ln 2 / T,
 // B = -(sum g + h entropy) / T; the given tokens' entries are read before anything is written (grad may be
 // logits) and written again at the end with what their g adds.
-// STREAM: past the caches, of a gradient that is more than they hold.  4096 x 128000 bf16 385 us, through them 403; 128
-// x 151000 binary32, which the last-level cache holds, 37.6 and 42.4, but with a reader after it (grad_norm)
-// 50.2 and 44.2.
+// STREAM: past the caches, of a gradient that is more than they hold.  4096 x 128000 bf16 385 us, through them 403.  Of one
+// that the last-level cache holds the next reader gains more than the writer loses: 128 x 151000 binary32 with the
+// gradient's norm after it 50.2 us, through the caches 44.2.
 template <typename T, bool STREAM>
 __global__ __launch_bounds__(256) void backward_kernel(const BackArgs a) {
   constexpr int N = 16 / sizeof(T), THREADS = 256;
