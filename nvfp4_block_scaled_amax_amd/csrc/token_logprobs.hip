@@ -15,11 +15,11 @@
 // it.  More than fit (many equal or rising entries in few cells) are found one by one.  The order in which the
 // collecting atomics run changes nothing: the numbers are distinct and their places follow from them.
 //
-// Bound by the row's bytes; the exponential of every entry hides behind them at 16 workgroups' wavefronts a
+// Bound by the row's bytes; the exponential of every entry hides behind them at eight workgroups a
 // compute unit.  Measured on one MI355X: 4096 x 128000 bf16 185 us without alternatives, 203 us with 20 (5.2
-// TB/s); 515 x 50251 binary32 of which a quarter is not read 15.5 us (5.0 TB/s); gradient, 4096 x 128000 bf16 385 us (5.4 TB/s).  512 x 128000 with
-// 20 alternatives of rows of which half the entries are equal, or of which few threads hold all large ones, 120-140
-// us, of other rows 37.
+// TB/s); 515 x 50251 binary32 of which a quarter is not read 15.5 us (5.0 TB/s); gradient, 4096 x 128000 bf16 385 us
+// (5.4 TB/s).  512 x 128000 with 20 alternatives of rows of which half the entries are equal, or of which few threads
+// hold all large ones, 120-140 us, of other rows 37.
 #include "nvfp4_answer.h"
 #include "train_common.h"
 
@@ -346,7 +346,10 @@ __device__ __forceinline__ void no_top(const Args& a, int64_t row) {
   }
 }
 
-template <typename T, int THREADS, bool TOP, bool SPLIT>
+// ODD: bf16 rows some of which begin at odd 2-byte addresses, where 16-byte loads are slow: they are loaded from the
+// 4-byte boundary below, with the word behind, and shifted (4096 x 127999 182 us, loaded where they lie 217; with 20
+// alternatives 208 and 245).  The entries are the same and so are all results.
+template <typename T, int THREADS, bool TOP, bool SPLIT, bool ODD>
 __global__ __launch_bounds__(THREADS) void forward_kernel(const Args a) {
   constexpr int N = 16 / sizeof(T);
   __shared__ Stat slots[THREADS / 64];
@@ -395,18 +398,35 @@ __global__ __launch_bounds__(THREADS) void forward_kernel(const Args a) {
   constexpr int kAhead = Cells<THREADS, N>::kStepsAhead;
   struct Batch {
     Vec<T, N> v[kAhead];
+    uint32_t behind[ODD ? kAhead : 1];
+  };
+  const uint32_t shift = ODD ? (uint32_t)(uintptr_t)x & 2 : 0;
+  const T* from = (const T*)((const char*)x - shift);
+  const uint32_t next_word = shift ? N : 0;
+  const auto fetch = [&](Batch& b, int k, uint32_t at) {
+    b.v[k] = load_vec<N>(from + at);
+    if constexpr (ODD) b.behind[k] = *(const uint32_t*)(from + at + next_word);
+  };
+  const auto vector = [&](const Batch& b, int k) {
+    Vec<T, N> v = b.v[k];
+    if constexpr (ODD) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v.w[i] = __builtin_amdgcn_alignbyte(i < 3 ? b.v[k].w[i + 1] : b.behind[k], b.v[k].w[i], shift);
+    }
+    return v;
   };
   const auto load = [&](uint32_t at) {
     Batch b;
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) b.v[k] = load_vec<N>(x + at + k * step);
+    for (int k = 0; k < kAhead; ++k) fetch(b, k, at + k * step);
     return b;
   };
   const auto load_rest = [&](uint32_t at) {
     Batch b = {};
 #pragma unroll
     for (int k = 0; k < kAhead; ++k)
-      if (at + k * step + N <= hi) b.v[k] = load_vec<N>(x + at + k * step);
+      if (at + k * step + N <= hi) fetch(b, k, at + k * step);
     return b;
   };
   const uint32_t batches = (hi - lo) / (step * kAhead);          // that all threads have
@@ -419,7 +439,7 @@ __global__ __launch_bounds__(THREADS) void forward_kernel(const Args a) {
   uint32_t in = 0;
   const auto take = [&] {
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) unit(now.v[k], at + k * step);
+    for (int k = 0; k < kAhead; ++k) unit(vector(now, k), at + k * step);
     at += kAhead * step;
     in += kAhead;
     if (TOP && in == cells.block) {
@@ -441,7 +461,7 @@ __global__ __launch_bounds__(THREADS) void forward_kernel(const Args a) {
   for (int k = 0; k < kAhead; ++k) {
     const uint32_t to = at + k * step;
     if (to + N <= hi) {
-      unit(now.v[k], to);
+      unit(vector(now, k), to);
     } else if (to < hi) {
       float w[N];
 #pragma unroll
@@ -551,7 +571,11 @@ __global__ __launch_bounds__(256) void backward_kernel(const BackArgs a) {
   const T* x = (const T*)a.logits + row * a.stride;
   T* grad = (T*)a.grad + row * a.grad_stride;
   constexpr int kAhead = 4;
-  uint32_t at = lo + threadIdx.x * N;
+  // Vectors begin at a line of grad's (each entry's value is its own); the few before are a thread's each.  4096 x 127999
+  // bf16 389 us, from the part's begin 463; 8192 x 8191 56 and 74; 4096 x 127999 binary32 785 and 915.
+  const uint32_t before = (uint32_t)(-(uintptr_t)(grad + lo) & 127) / sizeof(T);
+  const bool first = threadIdx.x < before && lo + threadIdx.x < hi;
+  uint32_t at = lo + before + threadIdx.x * N;
   constexpr uint32_t step = THREADS * N;
   const auto whole_batch = [&](uint32_t at) { return at + (kAhead - 1) * step + N <= hi; };
   struct Batch {
@@ -568,6 +592,7 @@ __global__ __launch_bounds__(256) void backward_kernel(const BackArgs a) {
   if (i < a.given) mine = token(a.tokens, a.wide, row * a.given + i);
   if (__ballot(mine >= 0) == 0) {
     const Vec<T, N> zero = zero_vec<T, N>();
+    if (first) grad[lo + threadIdx.x] = from_f32<T>(0.0f);
     for (; at < hi; at += step) store_vec<kAny>(grad, at, hi, zero);
     return;
   }
@@ -611,6 +636,7 @@ __global__ __launch_bounds__(256) void backward_kernel(const BackArgs a) {
     for (int k = 0; k < N; ++k) r[k] = value(v[k]);
     store_vec<kAny, STREAM>(grad, to, hi, make_vec<T>(r));
   };
+  if (first) grad[lo + threadIdx.x] = from_f32<T>(value(to_f32(x[lo + threadIdx.x])));
   while (more) {
     const uint32_t then = at + kAhead * step;
     more = whole_batch(then);
@@ -639,10 +665,16 @@ int splits_of(int64_t rows, int64_t vocab) {
   return (int)(want < kMaxSplits ? want : kMaxSplits);
 }
 
+template <typename T, int THREADS, bool SPLIT, bool ODD>
+void launch_forward(const Args& a, dim3 grid, hipStream_t s) {
+  if (a.top) forward_kernel<T, THREADS, true, SPLIT, ODD><<<grid, THREADS, 0, s>>>(a);
+  else forward_kernel<T, THREADS, false, SPLIT, ODD><<<grid, THREADS, 0, s>>>(a);
+}
 template <typename T, int THREADS, bool SPLIT>
 void launch_forward(const Args& a, dim3 grid, hipStream_t s) {
-  if (a.top) forward_kernel<T, THREADS, true, SPLIT><<<grid, THREADS, 0, s>>>(a);
-  else forward_kernel<T, THREADS, false, SPLIT><<<grid, THREADS, 0, s>>>(a);
+  const bool odd = sizeof(T) == 2 && (((uintptr_t)a.logits & 2) || (a.stride & 1));
+  if (odd) launch_forward<T, THREADS, SPLIT, sizeof(T) == 2>(a, grid, s);
+  else launch_forward<T, THREADS, SPLIT, false>(a, grid, s);
 }
 
 template <typename T>

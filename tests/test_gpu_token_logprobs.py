@@ -356,6 +356,35 @@ def test_far_rows(nv):
     assert abs(x[-2, 0].item() - 1) < 0.01 and abs(x[-2, 1].item() + 1 / vocab) < 1e-6
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rows,vocab,top", [(3, 5, 5), (2, 777, 20), (3, 20003, 20), (2, 70001, 20), (2100, 1003, 9)])
+def test_a_row_where_it_lies(nv, rows, vocab, top, dtype):
+    """At every element of 16 bytes: the bits of the aligned rows, forward and backward, whatever the gradient's
+    place."""
+    x = logits_of((rows, vocab), 8).to(dtype).cuda()
+    t = tokens_of(rows, 2, vocab, 1, 0.2).cuda()
+    wide = (vocab + 15) // 8 * 8
+    even = torch.zeros(rows, wide, dtype=dtype, device="cuda")
+    even[:, :vocab] = x
+    want = nv.token_logprobs(even[:, :vocab], t, top=top)
+    d, h = torch.randn(rows, 2, device="cuda"), torch.randn(rows, device="cuda")
+    back = dict(entropy=want[1], dentropy=h)
+    grad = nv.token_logprobs_backward(even[:, :vocab], t, want[4], d, **back)
+    for shift in range(1, 8):
+        held = torch.full((rows, wide + 8), 5.0, dtype=dtype, device="cuda")
+        held[:, shift:shift + vocab] = x
+        there = held[:, shift:shift + vocab]
+        for a, b in zip(nv.token_logprobs(there, t, top=top), want):
+            assert torch.equal(a, b)
+        assert torch.equal(nv.token_logprobs_backward(there, t, want[4], d, **back), grad)
+        out = torch.full((rows, wide + 8), 7.0, dtype=dtype, device="cuda")
+        nv.token_logprobs_backward(x, t, want[4], d, **back, grad=out[:, shift:shift + vocab])
+        assert torch.equal(out[:, shift:shift + vocab], grad)
+        assert (out[:, :shift] == 7).all() and (out[:, shift + vocab:] == 7).all()
+        nv.token_logprobs_backward(there, t, want[4], d, **back, grad=there)
+        assert torch.equal(there, grad) and (held[:, :shift] == 5).all() and (held[:, shift + vocab:] == 5).all()
+
+
 @pytest.mark.parametrize("dtype,rows", [(BF16, 1400), (F32, 700)])
 def test_a_gradient_that_no_cache_holds(nv, dtype, rows):
     """More than 128 MB at once: the bits of 100 rows at a time."""
