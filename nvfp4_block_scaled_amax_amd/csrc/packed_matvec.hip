@@ -420,7 +420,7 @@ __global__ __launch_bounds__(W * 64) void matvec_kernel(const Matvec a) {
   }
 }
 
-// `room`: shared memory for x, so that one (150 KB), two or more workgroups share a compute unit.
+// `room`: shared memory for x, so that one (150 KB) to four workgroups share a compute unit.
 template <typename X, bool FEW, int MT, int W, bool EXPERT, bool SHORT = false>
 void launch(Matvec a, int64_t columns, int room, int deal, hipStream_t stream) {
   const int64_t tiles = (a.rows + 15) / 16, units = (a.cols + kUnit - 1) / kUnit;
@@ -462,7 +462,8 @@ void launch(Matvec a, int64_t columns, int room, int deal, hipStream_t stream) {
 // rule takes where no size stands with them.
 template <typename X>
 void launch(const Matvec& a, hipStream_t stream) {
-  constexpr int kOne = 150 * 1024, kTwo = 75 * 1024, kFour = 40 * 1024, kGroup = sizeof(X) == 4 ? 3 : 1;
+  constexpr int kOne = 150 * 1024, kTwo = 75 * 1024, kThree = 40 * 1024, kFour = 34 * 1024;
+  constexpr int kGroup = sizeof(X) == 4 ? 3 : 1;
   const int64_t units = (a.cols + kUnit - 1) / kUnit;
   if (a.expert) {
     // What an expert gets is not known here: `all` / E columns on average.
@@ -471,15 +472,17 @@ void launch(const Matvec& a, hipStream_t stream) {
     if (a.cols < kUnit) launch<X, false, 1, 4, true, true>(a, 16, kOne, 0, stream);
     // Many columns, 64 a pass: 65, 32 columns 67-77, 16 84.
     else if (all >= 20 * E && work > 25000) launch<X, false, 4, 8, true>(a, 64, kOne, 0, stream);
-    // Few: the scaled products, 10.7, with 8 wavefronts 11.2, scaled weights 12.4.
+    // Few: the scaled products, 10.7, with 8 wavefronts 11.2, scaled weights 12.4; four workgroups a compute unit (4 rows
+    // to 4 of 64 experts of 2048 x 5120 25.2, three 27.9).
     else if (all * kGroup <= E && rows < 64000) launch<X, true, 1, 4, true>(a, 4, kFour, 1, stream);
     // 32 columns a pass: 49.3, 16 columns 49.3-56, 64 54.7.
     else if (units > 4 && all > 5 * E && work > 14700) launch<X, false, 2, 16, true>(a, 32, kOne, 0, stream);
     // Long rows and few of them: 16 wavefronts share a tile's units, 20.1, 8 21.3, 4 25.7.
     else if (units > 4 && rows < 25000) launch<X, false, 1, 16, true>(a, 16, kOne, 0, stream);
     // The others: small workgroups, whose starts (the list of rows, x) hide behind each other's loads, 18.3, with 8
-    // wavefronts 19.5, with 16 23.9.
-    else launch<X, false, 1, 4, true>(a, 16, kFour, 0, stream);
+    // wavefronts 19.5, with 16 23.9.  Four workgroups a compute unit where x is short (24 rows to 4 of 64 experts of
+    // 5120 x 2048 62, three 68), three where it is long (of 2048 x 5120 63.5, four 64.6).
+    else launch<X, false, 1, 4, true>(a, 16, units <= 4 ? kFour : kThree, 0, stream);
     return;
   }
   const int64_t columns = a.out_rows * kGroup, work = a.rows * ((columns + 15) / 16);
@@ -496,7 +499,7 @@ void launch(const Matvec& a, hipStream_t stream) {
   } else if (columns <= 16 || work <= 14700) {
     // 16 columns a pass, by the smallest workgroup that holds them whole: of 4 wavefronts 5.8, where 8 take 6.8 and 16
     // 9.4; of 8 10.2, where 4 take 11.5 and 16 12.7; of 16 21.7, where 8 take 22.6 and 4 27.8.
-    if (x <= 36) launch<X, false, 1, 4, false>(a, some, kFour, 0, stream);
+    if (x <= 36) launch<X, false, 1, 4, false>(a, some, kThree, 0, stream);
     else if (x <= 72) launch<X, false, 1, 8, false>(a, some, kTwo, 0, stream);
     // Long rows and few of them: the scaled products, 8 columns a pass, 10.6, the other forms 14.3 or more.
     else if (a.rows * ((columns + 7) / 8) <= 4100)

@@ -347,8 +347,9 @@ __device__ __forceinline__ void no_top(const Args& a, int64_t row) {
 }
 
 // ODD: bf16 rows some of which begin at odd 2-byte addresses, where 16-byte loads are slow: they are loaded from the
-// 4-byte boundary below, with the word behind, and shifted (4096 x 127999 182 us, loaded where they lie 217; with 20
-// alternatives 208 and 245).  The entries are the same and so are all results.
+// 4-byte boundary below, with the word behind (both words hold a part of the row), and shifted: 4096 x 127999
+// 182 us, loaded where they lie 217; with 20 alternatives 208 and 245.  The entries are the same and so are
+// all results.
 template <typename T, int THREADS, bool TOP, bool SPLIT, bool ODD>
 __global__ __launch_bounds__(THREADS) void forward_kernel(const Args a) {
   constexpr int N = 16 / sizeof(T);
