@@ -280,6 +280,44 @@ def test_graphs_and_streams(nv, xtype):
         assert same(y, want) and same(eager, want)
 
 
+@pytest.mark.parametrize("xtype", [BF16, F32])
+@pytest.mark.parametrize("tokens,rows,cols", [(1, 300, 14336), (16, 200, 5120), (40, 700, 4112), (20, 9000, 1040)])
+def test_a_graph_of_more_shared_memory(nv, tokens, rows, cols, xtype):
+    """The forms that ask for more shared memory than a launch gets by itself, first called within a capture."""
+    codes, scales, alpha, value = weights((1, rows, cols), 1)
+    args = codes[0].cuda(), scales[0].cuda(), alpha.cuda()
+    x, graph = torch.zeros(tokens, cols, dtype=xtype, device="cuda"), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        y = nv.packed_matvec(x, *args)
+    for seed in range(3):
+        now = whole((tokens, cols), seed)
+        x.copy_(now)
+        graph.replay()
+        eager = nv.packed_matvec(x, *args)
+        torch.cuda.synchronize()
+        want = rounded(now.double() @ value[0].t(), alpha, xtype)
+        assert same(y, want) and same(eager, want)
+
+
+def test_two_streams_at_once(nv):
+    """Calls on two streams that overlap: each has the result it has alone."""
+    codes, scales, alpha, value = weights((1, 4099, 2064), 1)
+    args = codes[0].cuda(), scales[0].cuda(), alpha.cuda()
+    inputs = [whole((t, 2064), t) for t in (1, 7, 16, 33)]
+    there = [x.to(BF16).cuda() for x in inputs]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(40):
+        with torch.cuda.stream(streams[i % 2]):
+            got.append(nv.packed_matvec(there[(i // 2) % 4], *args, dtype=F32))
+    torch.cuda.synchronize()
+    want = [rounded(x.double() @ value[0].t(), alpha, F32) for x in inputs]
+    for i, y in enumerate(got):
+        assert same(y, want[(i // 2) % 4])
+
+
 def test_refusals(nv):
     codes, scales, alpha, _ = weights((2, 32, 64), 0)
     c, s, a = codes.cuda(), scales.cuda(), alpha.cuda()

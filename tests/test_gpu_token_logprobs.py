@@ -462,3 +462,23 @@ def test_refusals(nv):
     for kind, text, call in bad:
         with pytest.raises(kind, match=text):
             call()
+
+
+def test_two_streams_at_once(nv):
+    """Calls on two streams that overlap, rows shared by several workgroups among them: each has the bits it has alone."""
+    cases = [(logits_of(shape, 3).to(dtype).cuda(), tokens_of(shape[0], 2, shape[1], 4).cuda())
+             for shape, dtype in (((2, 90001), BF16), ((700, 5003), F32), ((3, 128000), BF16), ((2500, 700), BF16))]
+    want = [nv.token_logprobs(x, t, top=20) for x, t in cases]
+    d = [torch.ones(t.shape, device="cuda") for _, t in cases]
+    grads = [nv.token_logprobs_backward(x, t, w[4], g) for (x, t), w, g in zip(cases, want, d)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = []
+    for i in range(40):
+        k = (i + i // 4) % 4
+        with torch.cuda.stream(streams[i % 2]):
+            out = nv.token_logprobs(*cases[k], top=20)
+            got.append((k, out, nv.token_logprobs_backward(*cases[k], out[4], d[k])))
+    torch.cuda.synchronize()
+    for k, out, grad in got:
+        assert all(torch.equal(a, b) for a, b in zip(out, want[k])) and torch.equal(grad, grads[k])
