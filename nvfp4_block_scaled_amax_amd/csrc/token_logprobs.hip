@@ -659,8 +659,8 @@ constexpr int64_t kMaxVocab = int64_t(1) << 28, kMaxTokenRows = int64_t(1) << 30
 // 20 alternatives, one workgroup a row against several: 4 x 128000 23.5 us, 12.1; 192 x 128000 26.1, 25.6; 64 x 65536
 // 16.3, 14.5; 128 x 65536 16.6, 16.1; 4 x 40960 11.5 both; 4 x 32768 10.6, 11.7; 100 x 32768 11.4, 13.7.
 int splits_of(int64_t rows, int64_t vocab) {
-  if (rows <= 0 || vocab < 40960 || rows * 640 > vocab) return 1;
-  int64_t want = 512 / rows;
+  if (rows <= 0 || rows > 512 || vocab < 40960 || rows * 640 > vocab) return 1;
+  int64_t want = 512 / rows;                            // 1 at least
   const int64_t most = (vocab + 4095) / 4096;
   want = want < most ? want : most;
   return (int)(want < kMaxSplits ? want : kMaxSplits);

@@ -6,6 +6,7 @@ import os
 import re
 import shutil
 import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -93,6 +94,34 @@ LONG = dict(vocab=100000, xs=100000)
     (dict(st=F + 16), EALIAS), (dict(ws=G, **LONG), EALIAS)])
 def test_token_logprobs_refuses(L, kw, status):
     assert logprobs(L, **kw) == status
+
+
+LONG_ROWS = r"""
+import ctypes, sys
+import nvfp4_block_scaled_amax_amd as nv
+L, n = nv.lib(), ctypes.c_int(0)
+if ctypes.CDLL("libamdhip64.so").hipGetDeviceCount(ctypes.byref(n)) == 0 and n.value:
+    sys.exit(77)                                    # nothing may be launched on these addresses
+at = [0x10000000000 * i for i in range(1, 8)]
+for rows, vocab in ((512, 328320), (513, 328319), (513, 328320), (600, 400000), (1024, 1 << 20), (1 << 14, 1 << 24)):
+    for top in (0, 64):
+        print(rows, vocab, top, L.nvfp4_token_logprobs_workspace(rows, vocab, top),
+              L.nvfp4_token_logprobs(at[0], vocab, None, rows, vocab, 0, top, 0, 1, 1.0, None, at[2], at[3], at[4],
+                                     at[5], None, None), flush=True)
+"""
+
+
+def test_token_logprobs_of_many_long_rows_return(L):
+    """More rows than are shared among workgroups, however long: no workspace, and the call comes back (without a
+    device, with the status of a launch that failed)."""
+    env = dict(os.environ, HIP_VISIBLE_DEVICES="-1", ROCR_VISIBLE_DEVICES="-1", PYTHONPATH=ROOT)
+    r = subprocess.run([sys.executable, "-c", LONG_ROWS], env=env, capture_output=True, text=True, timeout=120)
+    if r.returncode == 77:
+        pytest.skip("a GPU is there all the same")
+    assert r.returncode == 0, (r.returncode, r.stdout, r.stderr)
+    lines = r.stdout.split("\n")[:-1]
+    assert len(lines) == 12 and all(line.split()[3:] == ["0", str(EHIP)] for line in lines), r.stdout
+    assert L.nvfp4_token_logprobs_workspace(2 ** 63 - 1, 2 ** 63 - 1, 64) == 0
 
 
 def back(L, x=A, xs=100, t=B, st=C, ent=D, dl=E, dh=F, rows=2, vocab=100, given=1, ty=BF16, it=I64, temp=1.0, g=G,

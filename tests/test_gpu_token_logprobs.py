@@ -482,3 +482,29 @@ def test_two_streams_at_once(nv):
     torch.cuda.synchronize()
     for k, out, grad in got:
         assert all(torch.equal(a, b) for a, b in zip(out, want[k])) and torch.equal(grad, grads[k])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rows,vocab,top", [(513, 328320, 0), (513, 328321, 20), (600, 400000, 64), (600, 400000, 0)])
+def test_many_long_rows(nv, rows, vocab, top, dtype):
+    """More rows than are shared among workgroups, of lengths at which fewer would be: the first, the middle and the
+    last one against 64 bits, all of them with the bits of calls for fewer rows that are a workgroup's each."""
+    x = torch.randn(rows, vocab, generator=torch.Generator("cuda").manual_seed(1), device="cuda").mul_(2.5).to(dtype)
+    tokens = tokens_of(rows, 2, vocab, 3, 0.2)
+    at = [0, rows // 2, rows - 1]
+    tokens[at, 0] = tokens[at, 0].clamp(min=0)
+    assert nv.lib().nvfp4_token_logprobs_workspace(rows, vocab, top) == 0
+    got = nv.token_logprobs(x, tokens.cuda(), top=top)
+    r = reference(x[at], tokens[at], 1.0, top)
+    bound = lambda v: r["dz"][:, None] + U * (8 * v.abs() + 4 * r["z"][:, None])
+    logp, entropy, top_logp, top_index, stats = [None if v is None else v.cpu()[at] for v in got]
+    near(logp, r["logp"], bound(r["logp"]))
+    near(entropy, r["h"], r["dh"])
+    near(stats[:, 1], r["z"], r["dz"] + 2 * U * r["z"])
+    assert torch.equal(stats[:, 0].double(), r["m"])
+    if top:
+        assert torch.equal(top_index, r["top"])
+        near(top_logp, r["top_logp"], bound(r["top_logp"]))
+    for part in (slice(0, 300), slice(rows - 300, rows)):
+        for a, b in zip(got, nv.token_logprobs(x[part], tokens[part].cuda(), top=top)):
+            assert (a is None and b is None) or torch.equal(a[part], b)
