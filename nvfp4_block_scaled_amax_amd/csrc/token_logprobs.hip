@@ -277,7 +277,8 @@ __device__ __forceinline__ void find_top(const T* row, uint32_t lo, uint32_t hi,
     }
   };
   // vectors with an entry that reaches the limit, and of these the candidates
-  const float least = low ? entry(low) : -INFINITY;
+  // (a limit below -inf's number, of which the bits that were not looked for are 0, is no entry's)
+  const float least = low > order(-INFINITY) ? entry(low) : -INFINITY;
   constexpr int kVectors = kHeld<THREADS> / 4;
   visit([&](const Vec<T, N>& v, uint32_t at) {
     float most = v[0];

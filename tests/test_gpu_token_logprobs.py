@@ -508,3 +508,27 @@ def test_many_long_rows(nv, rows, vocab, top, dtype):
     for part in (slice(0, 300), slice(rows - 300, rows)):
         for a, b in zip(got, nv.token_logprobs(x[part], tokens[part].cuda(), top=top)):
             assert (a is None and b is None) or torch.equal(a[part], b)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rows", [2, 2100])
+@pytest.mark.parametrize("top", [1, 2, 5, 20, 24, 64])
+def test_fewer_entries_than_alternatives(nv, rows, top, dtype):
+    """Rows of every length up to about twice `top` vectors of 16 bytes with one entry above -inf, with two in one
+    vector, with top - 1 and with `top` of them: the others follow in their order."""
+    n = 16 // dtype.itemsize
+    for vocab in [v for vectors in range(1, 2 * top + 10) for v in (vectors * n - 1, vectors * n) if v >= top]:
+        for live in {1, min(2, vocab), top, max(top - 1, 1)}:
+            row = torch.full((vocab,), -INF)
+            at = torch.arange(live) + vocab // 2 if live <= 2 else torch.randperm(vocab, generator=gen(vocab))[:live]
+            row[at % vocab] = torch.randn(live, generator=gen(live)).to(dtype).float()
+            want = torch.sort(row, descending=True, stable=True)
+            index = torch.full((rows, top), -5, device="cuda")
+            logp = torch.full((rows, top), 5.0, device="cuda")
+            x = row.to(dtype).cuda().expand(rows, vocab).contiguous()
+            nv.token_logprobs(x, top=top, top_logp=logp, top_index=index)
+            assert torch.equal(index.cpu(), want.indices[:top].expand(rows, top)), (vocab, live)
+            few = torch.log_softmax(row.double(), 0)[want.indices[:top]]
+            # (a dozen roundings of numbers below 16, and up to 64 terms)
+            assert torch.equal(torch.isinf(logp[0].cpu()), torch.isinf(few))
+            assert (logp.cpu() - few).nan_to_num(0.0, 0.0, 0.0).abs().max() <= 16 * 16 * U + 64 * U
