@@ -85,6 +85,8 @@ nvfp4_status nvfp4_token_logprobs(const void* logits, int64_t stride, const void
 /* Their gradient: with g_i = dlogp[i] (0 for a token of -1) and h = dentropy (0 where NULL), per row
  *   grad_j = round((sum_i g_i [tokens[i] == j] - p_j (sum_i g_i + h (ln p_j + entropy))) / T),
  *   ln p_j = (x_j - m) / T - z
+ * p_j below 2^-149 is 0.  A finite gradient is found for every T where the sums of |g_i| and |h| entropy, and
+ * 111 |h|, are below 3e38.
  * A row that was not read has a gradient of 0.  A row without a distribution, or with a token beyond
  * the vocabulary, has one of NaN.  Equal tokens of a row add up.
  * logits, tokens, given >= 1, vocab, T as in the forward call, which wrote stats and entropy

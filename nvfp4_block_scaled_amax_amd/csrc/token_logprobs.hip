@@ -29,7 +29,7 @@ namespace {
 constexpr int kMost = NVFP4_LOGPROBS_MAX;
 constexpr float kLowest = -3.402823466e38f;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kNone = -1000.0f;             // 2^kNone is 0: stands for any d below
+constexpr float kNone = -160.0f;              // 2^kNone is 0: stands for any d below
 
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -556,9 +556,10 @@ struct BackArgs {
   float c, inv_t;
 };
 
-// A workgroup takes a part of a row.  With y = log2 p: grad = p (A y + B), A = -h ln 2 / T,
-// B = -(sum g + h entropy) / T; the given tokens' entries are read before anything is written (grad may be
-// logits) and written again at the end with what their g adds.
+// A workgroup takes a part of a row.  With y = log2 p: grad = p (A y + B) / T, A = -h ln 2,
+// B = -(sum g + h entropy); the given tokens' entries are read before anything is written (grad may be
+// logits) and written again at the end with what their g adds.  A 1 / T above 1 multiplies p, one below 1 A and B: no
+// factor of a finite gradient is infinite.
 // STREAM: past the caches, of a gradient that is more than they hold.  4096 x 128000 bf16 385 us, through them 403.  Of one
 // that the last-level cache holds the next reader gains more than the writer loses: 128 x 151000 binary32 with the
 // gradient's norm after it 50.2 us, through the caches 44.2.
@@ -606,13 +607,14 @@ __global__ __launch_bounds__(256) void backward_kernel(const BackArgs a) {
   if (mine >= (int64_t)a.vocab) g = NAN;
   const float m = a.stats[row * 2], z = a.stats[row * 2 + 1];
   const float h = a.dentropy ? a.dentropy[row] : 0.0f, all = reduce64(g, Sum());
-  const float A = -h * kLn2 * a.inv_t;
-  float B = a.dentropy ? -fmaf(h, a.entropy[row], all) * a.inv_t : -all * a.inv_t;
+  const float below = fminf(a.inv_t, 1.0f), above = fmaxf(a.inv_t, 1.0f);
+  const float A = -h * kLn2 * below;
+  float B = a.dentropy ? -fmaf(h, a.entropy[row], all) * below : -all * below;
   if (!(z == z)) B = NAN;                          // no distribution
   const float z2 = z * kLog2e;
-  const auto value = [&](float e) {
+  const auto value = [&](float e, float by) {
     const float y = fmaxf(fmaf(e - m, a.c, -z2), kNone);
-    return exp2_(y) * fmaf(A, y, B);
+    return exp2_(y) * by * fmaf(A, y, B);
   };
   // the first of equal tokens in this part takes their sum
   float fix = 0.0f;
@@ -629,16 +631,16 @@ __global__ __launch_bounds__(256) void backward_kernel(const BackArgs a) {
         fix += up[j];
         if (j < i) fixes = false;
       }
-    if (fixes) fix = fmaf(fix, a.inv_t, value(to_f32(x[mine])));
+    if (fixes) fix = fmaf(fix, below, value(to_f32(x[mine]), 1.0f)) * above;
   }
   __syncthreads();
   const auto unit = [&](const Vec<T, N>& v, uint32_t to) {
     float r[N];
 #pragma unroll
-    for (int k = 0; k < N; ++k) r[k] = value(v[k]);
+    for (int k = 0; k < N; ++k) r[k] = value(v[k], above);
     store_vec<kAny, STREAM>(grad, to, hi, make_vec<T>(r));
   };
-  if (first) grad[lo + threadIdx.x] = from_f32<T>(value(to_f32(x[lo + threadIdx.x])));
+  if (first) grad[lo + threadIdx.x] = from_f32<T>(value(to_f32(x[lo + threadIdx.x]), above));
   while (more) {
     const uint32_t then = at + kAhead * step;
     more = whole_batch(then);

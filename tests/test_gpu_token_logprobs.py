@@ -532,3 +532,15 @@ def test_fewer_entries_than_alternatives(nv, rows, top, dtype):
             # (a dozen roundings of numbers below 16, and up to 64 terms)
             assert torch.equal(torch.isinf(logp[0].cpu()), torch.isinf(few))
             assert (logp.cpu() - few).nan_to_num(0.0, 0.0, 0.0).abs().max() <= 16 * 16 * U + 64 * U
+
+
+@pytest.mark.parametrize("kind", ["model", "masked", "lowest", "equal", "ties"])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("entropy", [False, True])
+@pytest.mark.parametrize("T", [1e-37, 1e-36, 1e-20, 1e-3, 1e5, 1e30])
+def test_backward_at_extreme_temperatures(nv, T, entropy, dtype, kind):
+    """Entries of probability 0 have a gradient of 0 however large 1 / T is."""
+    x = logits_of((3, 500), 5, kind).to(dtype).cuda()
+    tokens = tokens_of(3, 4, 500, 3)
+    tokens[0, 0] = x[0].argmax().item()
+    check_backward(nv, x, tokens, torch.tensor(T, dtype=F32).item(), 2, entropy)
