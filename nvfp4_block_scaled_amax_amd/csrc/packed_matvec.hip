@@ -420,6 +420,8 @@ __global__ __launch_bounds__(W * 64) void matvec_kernel(const Matvec a) {
   }
 }
 
+constexpr int kOne = 150 * 1024, kTwo = 75 * 1024, kThree = 40 * 1024, kFour = 34 * 1024;
+
 // `room`: shared memory for x, so that one (150 KB) to four workgroups share a compute unit.
 template <typename X, bool FEW, int MT, int W, bool EXPERT, bool SHORT = false>
 void launch(Matvec a, int64_t columns, int room, int deal, hipStream_t stream) {
@@ -439,6 +441,7 @@ void launch(Matvec a, int64_t columns, int room, int deal, hipStream_t stream) {
   a.lds = (int)(want < room ? want : room);
   if (a.lds < least) a.lds = least;
   constexpr int kSums = W * MT * (FEW ? 256 : 1024);
+  static_assert(kSums <= kOne && 3 * ((kUnit * 2 * W) + 16) <= kOne, "no call asks for more than a workgroup's own");
   const int bytes = a.lds > kSums ? a.lds : kSums;
   // The passes over the rows of x (of an expert: over twice its share) go one after the other or, where that leaves
   // compute units without a workgroup, side by side: 2048 x 8192 by 64 rows 15.1 us, 40.9 one after the other with 64
@@ -450,8 +453,8 @@ void launch(Matvec a, int64_t columns, int room, int deal, hipStream_t stream) {
   const dim3 grid((unsigned)groups, (unsigned)a.experts,
                   (unsigned)std::min<int64_t>((likely + per_pass - 1) / per_pass, full));
   const auto kernel = matvec_kernel<X, FEW, MT, W, EXPERT, SHORT>;
-  if (bytes > 60 * 1024)
-    (void)hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (bytes > 60 * 1024)      // (the most that any call asks for: calls of several threads agree)
+    (void)hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, kOne);
   kernel<<<grid, W * 64, bytes, stream>>>(a);
 }
 
@@ -462,7 +465,6 @@ void launch(Matvec a, int64_t columns, int room, int deal, hipStream_t stream) {
 // rule takes where no size stands with them.
 template <typename X>
 void launch(const Matvec& a, hipStream_t stream) {
-  constexpr int kOne = 150 * 1024, kTwo = 75 * 1024, kThree = 40 * 1024, kFour = 34 * 1024;
   constexpr int kGroup = sizeof(X) == 4 ? 3 : 1;
   const int64_t units = (a.cols + kUnit - 1) / kUnit;
   if (a.expert) {

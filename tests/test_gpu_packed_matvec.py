@@ -5,6 +5,8 @@ x and the weights are small multiples of fixed units.  Then the sum is exact and
 product with alpha and one rounding.  Values of ordinary size get the bound of a sum of `cols` terms."""
 from __future__ import annotations
 
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -316,6 +318,32 @@ def test_two_streams_at_once(nv):
     want = [rounded(x.double() @ value[0].t(), alpha, F32) for x in inputs]
     for i, y in enumerate(got):
         assert same(y, want[(i // 2) % 4])
+
+
+def test_two_threads_at_once(nv):
+    """Calls of two threads of one form with more shared memory than a launch gets by itself, of different sizes."""
+    codes, scales, alpha, value = weights((1, 96, 14336), 1)
+    inputs = [whole((t, 14336), t) for t in (1, 2, 3, 4)]
+    there = [x.to(BF16).cuda() for x in inputs]
+    args = codes[0].cuda(), scales[0].cuda(), alpha.cuda()
+    got = [[], []]
+
+    def calls(k):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for i in range(200):
+                got[k].append(nv.packed_matvec(there[2 * (i % 2) + k], *args, dtype=F32))
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=calls, args=(k,)) for k in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    want = [rounded(x.double() @ value[0].t(), alpha, F32) for x in inputs]
+    for k in range(2):
+        assert len(got[k]) == 200
+        for i, y in enumerate(got[k]):
+            assert same(y, want[2 * (i % 2) + k])
 
 
 def test_refusals(nv):
