@@ -236,9 +236,9 @@ __global__ __launch_bounds__(W * 64) void matvec_kernel(const Matvec a) {
       }
     }
   };
-  // rows of x of which a turn of the wavefronts (a unit each) fits: at least one
+  // rows of x of which a turn of the wavefronts (a unit each, where there are as many) fits: at least one
   const int turn = kUnit * deal;
-  const int per_pass = min(MT * kCols, a.lds / (turn * 2 + 16)) / kGroup;
+  const int per_pass = min(MT * kCols, a.lds / (min(turn, all * kUnit) * 2 + 16)) / kGroup;
   for (int first = blockIdx.z * per_pass; first < count; first += per_pass * gridDim.z) {
     const int here = min(per_pass, count - first), wide = here * kGroup;
     // x: all of it, or as many elements of each column as fit, a multiple of a turn
@@ -426,7 +426,11 @@ constexpr int kOne = 150 * 1024, kTwo = 75 * 1024, kThree = 40 * 1024, kFour = 3
 template <typename X, bool FEW, int MT, int W, bool EXPERT, bool SHORT = false>
 void launch(Matvec a, int64_t columns, int room, int deal, hipStream_t stream) {
   const int64_t tiles = (a.rows + 15) / 16, units = (a.cols + kUnit - 1) / kUnit;
-  const auto turn = [](int deal) { return (kUnit * 2 << deal) + 16; };     // bytes of a column
+  const auto turn = [](int deal) { return (kUnit * 2 << deal) + 16; };     // bytes of a turn's units of a column
+  // The least room for a column: a turn, or the row where it is shorter (a turn of 8 wavefronts for rows of 5 units left
+  // room for 5 of 8 columns, and the weights were read twice: 4096 x 3584 by 4 rows 8.1 us, 5.9 at once; 8960 x 2560 by 16
+  // rows 23.6, 16.0; 4096 x 5120 by 3 binary32 rows 29.8, 11.3).
+  const auto column = [&](int deal) { return std::min<int64_t>(turn(deal), units * (kUnit * 2) + 16); };
   const int64_t hit = a.experts < a.out_rows ? a.experts : a.out_rows;       // weights that are read
   // enough workgroups for the compute units: where the rows are few, more wavefronts deal a tile's units, as
   // far as there are units and every column fits
@@ -437,7 +441,7 @@ void launch(Matvec a, int64_t columns, int room, int deal, hipStream_t stream) {
     ++a.deal;
   // all of x, or what there is
   const int64_t want = columns * (units * (2 * kUnit) + 16);
-  const int least = 3 * turn(a.deal);
+  const int least = 3 * (int)column(a.deal);
   a.lds = (int)(want < room ? want : room);
   if (a.lds < least) a.lds = least;
   constexpr int kSums = W * MT * (FEW ? 256 : 1024);
@@ -447,7 +451,7 @@ void launch(Matvec a, int64_t columns, int room, int deal, hipStream_t stream) {
   // compute units without a workgroup, side by side: 2048 x 8192 by 64 rows 15.1 us, 40.9 one after the other with 64
   // rows a pass; 512 x 496 by 1024 rows 7.1, 246.
   constexpr int kFull = EXPERT ? 4096 : 8192;                                // wavefronts
-  const int64_t per_pass = std::min(MT * (FEW ? 4 : 16), a.lds / turn(a.deal)) / (sizeof(X) == 4 ? 3 : 1);
+  const int64_t per_pass = std::min<int64_t>(MT * (FEW ? 4 : 16), a.lds / column(a.deal)) / (sizeof(X) == 4 ? 3 : 1);
   const int64_t groups = (tiles + (W >> a.deal) - 1) / (W >> a.deal), full = kFull / (groups * hit * W) + 1;
   const int64_t likely = (a.out_rows * (EXPERT ? 2 : 1) + a.experts - 1) / a.experts;
   const dim3 grid((unsigned)groups, (unsigned)a.experts,

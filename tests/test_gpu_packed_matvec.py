@@ -5,6 +5,7 @@ x and the weights are small multiples of fixed units.  Then the sum is exact and
 product with alpha and one rounding.  Values of ordinary size get the bound of a sum of `cols` terms."""
 from __future__ import annotations
 
+import ctypes
 import threading
 
 import numpy as np
@@ -318,6 +319,44 @@ def test_two_streams_at_once(nv):
     want = [rounded(x.double() @ value[0].t(), alpha, F32) for x in inputs]
     for i, y in enumerate(got):
         assert same(y, want[(i // 2) % 4])
+
+
+class KernelNode(ctypes.Structure):
+    """hipKernelNodeParams."""
+    _fields_ = [("block", ctypes.c_uint * 3), ("extra", ctypes.c_void_p), ("func", ctypes.c_void_p),
+                ("grid", ctypes.c_uint * 3), ("params", ctypes.c_void_p), ("shared", ctypes.c_uint)]
+
+
+def launch_of(call):
+    """Grid and bytes of shared memory of the one kernel that a call launches, from a capture of it."""
+    hip = ctypes.CDLL("libamdhip64.so")
+    graph = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(graph):
+        call()
+    raw, count = ctypes.c_void_p(graph.raw_cuda_graph()), ctypes.c_size_t(1)
+    node, got = (ctypes.c_void_p * 1)(), KernelNode()
+    assert hip.hipGraphGetNodes(raw, None, ctypes.byref(count)) == 0 and count.value == 1
+    assert hip.hipGraphGetNodes(raw, node, ctypes.byref(count)) == 0
+    assert hip.hipGraphKernelNodeGetParams(ctypes.c_void_p(node[0]), ctypes.byref(got)) == 0
+    return tuple(got.grid), got.shared
+
+
+@pytest.mark.parametrize("tokens,rows,cols,xtype,passes", [
+    (4, 4096, 1536, BF16, 1), (4, 2048, 2560, BF16, 1), (4, 4096, 3584, BF16, 1), (8, 4096, 2560, BF16, 1),
+    (8, 4096, 5120, BF16, 1), (16, 8960, 1536, BF16, 1), (16, 8960, 2560, BF16, 1), (16, 1024, 2560, BF16, 2),
+    (24, 14336, 1536, BF16, 1), (1, 4096, 2560, F32, 1), (5, 1024, 2560, F32, 3)])
+def test_columns_that_fit_go_at_once(nv, tokens, rows, cols, xtype, passes):
+    """Rows of x that a workgroup has room for, of lengths that are no power of two of units: as few passes, each of
+    which reads the weights, as the columns of the form make (1024 weight rows take the form of 8 columns: two
+    passes for 16 of bf16, three for 5 rows of binary32, three columns each).  Passes go side by side, a layer
+    of the grid each."""
+    codes, scales, alpha, value = weights((1, rows, cols), 2)
+    x, args = whole((tokens, cols), 3), (codes[0].cuda(), scales[0].cuda(), alpha.cuda())
+    there = x.to(xtype).cuda()
+    got = nv.packed_matvec(there, *args, dtype=F32)
+    assert same(got, rounded(x.double() @ value[0].t(), alpha, F32))
+    grid, shared = launch_of(lambda: nv.packed_matvec(there, *args, dtype=F32, y=got))
+    assert grid[1:] == (1, passes), (grid, shared)
 
 
 def test_two_threads_at_once(nv):
