@@ -544,3 +544,40 @@ def test_backward_at_extreme_temperatures(nv, T, entropy, dtype, kind):
     tokens = tokens_of(3, 4, 500, 3)
     tokens[0, 0] = x[0].argmax().item()
     check_backward(nv, x, tokens, torch.tensor(T, dtype=F32).item(), 2, entropy)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("vocab", [50001, 131072])
+def test_in_place_strides_and_guards_of_shared_rows(nv, vocab, dtype):
+    """The same of rows that several workgroups share, with a workspace between guards."""
+    assert nv.lib().nvfp4_token_logprobs_workspace(5, vocab, 9) > 0
+    test_in_place_strides_and_guards(nv, vocab, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("rows,vocab,top", [(5, 50001, 64), (1, 40960, 64), (64, 41000, 1), (2, 300003, 64), (3, 90000, 0)])
+def test_shared_rows_between_guards(nv, rows, vocab, top, dtype):
+    """Every output and the workspace of rows that several workgroups share, whatever they held before."""
+    need = nv.lib().nvfp4_token_logprobs_workspace(rows, vocab, top)
+    assert need > 0
+    x, tokens = logits_of((rows, vocab), 7).to(dtype).cuda(), tokens_of(rows, 3, vocab, 1, 0.2).cuda()
+    tokens[-1] = -1 if rows > 1 else 5
+    want = nv.token_logprobs(x, tokens, top=top)
+    for byte in (0, 0x7F, 0xFF):
+        held = [torch.full((size + 64,), byte, dtype=torch.uint8, device="cuda")
+                for size in (rows * 12, rows * 4, rows * top * 4, rows * top * 8, rows * 8, need)]
+        mid = [t[32:-32] for t in held]
+        logp, entropy, top_logp, stats = (mid[i].view(torch.float32) for i in (0, 1, 2, 4))
+        nv.token_logprobs(x, tokens, top=top, logp=logp.view(rows, 3), entropy=entropy, stats=stats.view(rows, 2),
+                          top_logp=top_logp.view(rows, top) if top else None,
+                          top_index=mid[3].view(torch.int64).view(rows, top) if top else None, workspace=mid[5])
+        for t in held:
+            assert (t[:32] == byte).all() and (t[-32:] == byte).all()
+        for w, t in zip(want, mid):
+            assert w is None or torch.equal(w.view(-1).view(torch.uint8), t)
+
+
+@pytest.mark.parametrize("vocab", [60000, 140001])
+def test_tokens_that_are_none_or_beyond_of_shared_rows(nv, vocab):
+    assert nv.lib().nvfp4_token_logprobs_workspace(4, vocab, 3) > 0
+    test_tokens_that_are_none_or_beyond(nv, 4, vocab)
