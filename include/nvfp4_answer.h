@@ -40,7 +40,8 @@ int nvfp4_answer_abi_version(void);
  * (expert NULL: E = picks = 1 and e = 0).  The product of a code and its scale is exact; the sum is
  * binary32, multiplied by alpha and rounded once (the weights are not rounded to bf16 as
  * nvfp4_dequantize rounds them).  A non-finite x, scale or alpha reaches the outputs as IEEE
- * arithmetic has it; the sum is taken before alpha, so that |x| beyond 1e30 may overflow in it.
+ * arithmetic has it; the sum is taken before alpha, so that |x| beyond 1e30 may overflow in it, and what a binary32 x has
+ * below 2^-133 is cut off.
  * A row whose expert lies outside 0 .. E - 1 is zero.
  * x [tokens][cols] of `xtype` with row stride x_stride (elements, >= cols); codes [E][rows][cols/2]
  * (8-byte aligned), scales [E][rows][cols/16] and alpha [E] as nvfp4_quantize_batched writes them;
@@ -71,7 +72,7 @@ nvfp4_status nvfp4_packed_matvec(const void* x, int64_t x_stride, const uint8_t*
  * of `itype` (NULL where given is 0); logp float [rows][given]; entropy float [rows] or NULL;
  * top_logp float and top_index int64 [rows][top] (NULL where top is 0); stats float [rows][2].
  * 0 <= given, top <= NVFP4_LOGPROBS_MAX, top <= vocab, 1 <= vocab <= 2^28, 0 <= rows <= 2^30; T > 0 and
- * 1 / T finite.  workspace: nvfp4_token_logprobs_workspace(...) bytes, 16-byte aligned, any content (may
+ * log2(e) / T < 3e38 (T from 4.9e-39 on), T finite.  workspace: nvfp4_token_logprobs_workspace(...) bytes, 16-byte aligned, any content (may
  * be NULL where that is 0).  One launch; two for few long rows, which several workgroups share. */
 #define NVFP4_LOGPROBS_MAX 64
 int64_t nvfp4_token_logprobs_workspace(int64_t rows, int64_t vocab, int64_t top);
@@ -85,7 +86,7 @@ nvfp4_status nvfp4_token_logprobs(const void* logits, int64_t stride, const void
 /* Their gradient: with g_i = dlogp[i] (0 for a token of -1) and h = dentropy (0 where NULL), per row
  *   grad_j = round((sum_i g_i [tokens[i] == j] - p_j (sum_i g_i + h (ln p_j + entropy))) / T),
  *   ln p_j = (x_j - m) / T - z
- * p_j below 2^-149 is 0.  A finite gradient is found for every T where the sums of |g_i| and |h| entropy, and
+ * p_j below 2^-126 counts as 0.  A finite gradient is found for every T where the sums of |g_i| and |h| entropy, and
  * 111 |h|, are below 3e38.
  * A row that was not read has a gradient of 0.  A row without a distribution, or with a token beyond
  * the vocabulary, has one of NaN.  Equal tokens of a row add up.

@@ -31,7 +31,7 @@ __all__ = ["quantize", "fakequant", "amax", "quantize_from_amax", "fakequant_fro
            "layer_norm", "layer_norm_backward", "distill_loss", "adamw_plan", "adamw_step",
            "AdamWPlan", "ADAMW_BLOCK",
            "packed_matvec", "token_logprobs", "token_logprobs_backward", "grad_norm", "clip_grads",
-           "grad_norm_workspace",           "MATVEC_MAX_ROWS", "LOGPROBS_MAX",
+           "grad_norm_workspace", "MATVEC_MAX_ROWS", "LOGPROBS_MAX",
            "NVFP4Error", "MODES", "RULES", "STATS", "FUSED_WS_WORDS", "LIB_PATH"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnvfp4_amax.so")

@@ -130,7 +130,8 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor = None, *, top: in
     """Log probabilities of given tokens under softmax(logits / temperature)
     -> (logp, entropy, top_logp, top_index, stats).
 
-    logits is [..., vocab], bfloat16 or float32; 2-D ones may have a row stride.  tokens: int32 or
+    logits is [..., vocab], bfloat16 or float32, contiguous; 2-D ones may have a row stride.  (The
+    logits[:, :-1] of a batch are neither: pass all of them, with -1 for each last token.)  tokens: int32 or
     int64, [...] (one a row) or [..., given]; logp has their shape.  A token of -1 is none (logp 0), and
     rows that have none but these are not read (zeros; top_index -1).  entropy is [...], in nats.  top:
     how many of the largest entries to return, in falling order, the lowest index first among equals:

@@ -462,11 +462,12 @@ void launch(Matvec a, int64_t columns, int room, int deal, hipStream_t stream) {
   kernel<<<grid, W * 64, bytes, stream>>>(a);
 }
 
-// Which form, after sweeps of all of them over 608 single matrices (128 to 131072 rows, 848 to 16384 columns, 2 to 256
-// rows of x of both types) and 450 of 4 to 64 experts (256 to 8192 rows, 512 to 10848 columns, one token to
-// 128, 1 to 8 picks, some experts picked more often), weights from memory: the single ones are within 3 % of the
-// fastest form on average, the experts' within 6 %.  The figures are us, geometric means of the cases that a
-// rule takes where no size stands with them.
+// Which form, by sweeps of all of them over 1158 single matrices (128 to 131072 rows, 848 to 16384 columns, 1 to 256
+// rows of x of both types) and 534 of 4 to 64 experts (256 to 8192 rows, 512 to 10848 columns, one token to
+// 128, 1 to 8 picks, some experts picked more often), weights from memory.  The rules were fitted to 608 and 450 of these,
+// where single ones are 3 % off the fastest form on average and the experts' 6 %; over all of them it is 4.5 % (57 % at
+// most: 16 binary32 rows to 8960 x 1536) and 7 % (86 %: one binary32 row to 8 of 64 experts of 1408 x 2560).  The
+// figures are us, geometric means of all cases that a rule takes where no size stands with them.
 template <typename X>
 void launch(const Matvec& a, hipStream_t stream) {
   constexpr int kGroup = sizeof(X) == 4 ? 3 : 1;
@@ -476,17 +477,18 @@ void launch(const Matvec& a, hipStream_t stream) {
     const int64_t E = a.experts, all = a.out_rows * kGroup, rows = a.rows * std::min<int64_t>(E, a.out_rows);
     const int64_t work = rows * ((all + 16 * E - 1) / (16 * E));
     if (a.cols < kUnit) launch<X, false, 1, 4, true, true>(a, 16, kOne, 0, stream);
-    // Many columns, 64 a pass: 65, 32 columns 67-77, 16 84.
+    // Many columns, 64 a pass: 62, 32 columns 65-76, 16 82.
     else if (all >= 20 * E && work > 25000) launch<X, false, 4, 8, true>(a, 64, kOne, 0, stream);
-    // Few: the scaled products, 10.7, with 8 wavefronts 11.2, scaled weights 12.4; four workgroups a compute unit (4 rows
+    // Few: the scaled products, 10.7, with 8 wavefronts 11.3, scaled weights 12.4; four workgroups a compute unit (4 rows
     // to 4 of 64 experts of 2048 x 5120 25.2, three 27.9).
     else if (all * kGroup <= E && rows < 64000) launch<X, true, 1, 4, true>(a, 4, kFour, 1, stream);
-    // 32 columns a pass: 49.3, 16 columns 49.3-56, 64 54.7.
+    // 32 columns a pass: 53.0, 16 columns 52.9-63, 64 57.3.
     else if (units > 4 && all > 5 * E && work > 14700) launch<X, false, 2, 16, true>(a, 32, kOne, 0, stream);
-    // Long rows and few of them: 16 wavefronts share a tile's units, 20.1, 8 21.3, 4 25.7.
+    // Long rows and few of them: 16 wavefronts share a tile's units, 21.5, 8 21.2, 4 24.6 (of the first 450 cases 21.7,
+    // 22.5, 26.8).
     else if (units > 4 && rows < 25000) launch<X, false, 1, 16, true>(a, 16, kOne, 0, stream);
-    // The others: small workgroups, whose starts (the list of rows, x) hide behind each other's loads, 18.3, with 8
-    // wavefronts 19.5, with 16 23.9.  Four workgroups a compute unit where x is short (24 rows to 4 of 64 experts of
+    // The others: small workgroups, whose starts (the list of rows, x) hide behind each other's loads, 18.9, with 8
+    // wavefronts 20.2, with 16 24.7.  Four workgroups a compute unit where x is short (24 rows to 4 of 64 experts of
     // 5120 x 2048 62, three 68), three where it is long (of 2048 x 5120 63.5, four 64.6).
     else launch<X, false, 1, 4, true>(a, 16, units <= 4 ? kFour : kThree, 0, stream);
     return;
@@ -499,25 +501,25 @@ void launch(const Matvec& a, hipStream_t stream) {
     launch<X, false, 1, 4, false, true>(a, 16, kOne, 0, stream);
   } else if (columns <= 4) {
     // The scaled products; 4 wavefronts for short rows and for so many that each workgroup's x is read often
-    // (50251 x 4080 28.3, 8 wavefronts 30.3; 4096 x 1024 4.2 and 5.0), 8 for the others (8192 x 8192 12.0 and 15.5).
+    // (50251 x 4080 28.2, 8 wavefronts 30.4; 4096 x 1024 4.0 and 4.8), 8 for the others (8192 x 8192 11.7 and 15.5).
     if (units <= 2 || a.rows > 32768) launch<X, true, 1, 4, false>(a, columns, kOne, 1, stream);
     else launch<X, true, 1, 8, false>(a, columns, kOne, 1, stream);
   } else if (columns <= 16 || work <= 14700) {
-    // 16 columns a pass, by the smallest workgroup that holds them whole: of 4 wavefronts 5.8, where 8 take 6.8 and 16
-    // 9.4; of 8 10.2, where 4 take 11.5 and 16 12.7; of 16 21.7, where 8 take 22.6 and 4 27.8.
+    // 16 columns a pass, by the smallest workgroup that holds them whole: of 4 wavefronts 6.0, where 8 take 6.9 and 16
+    // 9.4; of 8 8.7, where 4 take 9.9 and 16 11.5; of 16 20.7, where 8 take 20.9 and 4 24.9.
     if (x <= 36) launch<X, false, 1, 4, false>(a, some, kThree, 0, stream);
     else if (x <= 72) launch<X, false, 1, 8, false>(a, some, kTwo, 0, stream);
-    // Long rows and few of them: the scaled products, 8 columns a pass, 10.6, the other forms 14.3 or more.
+    // Long rows and few of them: the scaled products, 8 columns a pass, 9.1, the other forms 12.5 or more.
     else if (a.rows * ((columns + 7) / 8) <= 4100)
       launch<X, true, 2, 8, false>(a, std::min<int64_t>(columns, 8), kOne, 0, stream);
-    // (more than one pass over rows of up to 10 units, by 8 wavefronts: 12.1, by 16 14.3)
+    // (more than one pass over rows of up to 10 units, by 8 wavefronts: 11.6, by 16 13.2)
     else if (columns > 16 && units <= 10) launch<X, false, 1, 8, false>(a, some, kTwo, 0, stream);
     else launch<X, false, 1, 16, false>(a, some, kOne, 0, stream);
   } else if (columns <= 32 || work <= 35000) {
-    // 32 columns a pass: 22.4, 16 columns 26.4, 64 29.2.
+    // 32 columns a pass: 21.0, 16 columns 22.6, 64 26.9.
     launch<X, false, 2, 16, false>(a, std::min<int64_t>(columns, 32), kOne, 0, stream);
   } else {
-    // 64 columns a pass: 54.3, 32 columns 62.4, 16 68.3.
+    // 64 columns a pass: 49.2, 32 columns 57.2, 16 56.9.
     launch<X, false, 4, 8, false>(a, std::min<int64_t>(columns, 64), kOne, 0, stream);
   }
 }

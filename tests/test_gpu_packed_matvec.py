@@ -99,6 +99,23 @@ def test_every_bit_of_32_bit_rows_counts(nv, bits):
     assert same(got, x)
 
 
+@pytest.mark.parametrize("tokens", [1, 7])
+@pytest.mark.parametrize("power", [-100, -110, -111, -120, -126, -133, -140])
+def test_small_32_bit_rows(nv, tokens, power):
+    """x of 24 significant bits against one weight of 1 per row, and an alpha that brings the sums back: what x
+    has below 2^-133, the smallest bf16, is cut off, and nothing else."""
+    cols = 256
+    x = torch.randint(1 << 23, 1 << 24, (tokens, cols), generator=gen(1)).double() * 2.0 ** (power - 23)
+    x = x.float()
+    code = torch.zeros(cols, cols, dtype=torch.int64)
+    code[torch.arange(cols), torch.arange(cols)] = 2                    # 1.0
+    codes = (code[:, 0::2] | code[:, 1::2] << 4).to(torch.uint8)
+    scales = torch.full((cols, cols // 16), 0x38, dtype=torch.uint8)
+    got = nv.packed_matvec(x.cuda(), codes.cuda(), scales.cuda(), torch.full((1,), 2.0 ** 100).cuda())
+    off = (x.double() - got.cpu().double() * 2.0 ** -100).abs()
+    assert (off < 2.0 ** -133).all() and (power < -110 or not off.any())
+
+
 @pytest.mark.parametrize("picks,itype,tokens,E,rows,cols", [
     (None, torch.int64, 9, 4, 40, 144), (1, torch.int32, 1, 8, 33, 272), (2, torch.int32, 5, 3, 64, 128),
     (4, torch.int64, 24, 16, 100, 1024), (8, torch.int64, 128, 64, 48, 96), (3, torch.int32, 40, 2, 17, 400)])
